@@ -242,6 +242,106 @@ int w4_gemv_topk(const uint32_t* qw, const uint16_t* scales, const uint16_t* bia
 int logits_argmax_topk_noalloc(const float* logits, int64_t ldl, int64_t M, int64_t V, int64_t k,
                                int32_t* idx, float* val, w4_stream_t stream);
 
+/*
+ * The step from the q|k|v projection to the output projection of a decoder layer: rotary
+ * positions, the append of keys and values to a paged cache, and the attention of the new
+ * tokens over it.  w4_gemv and gemm_f16 give the f32 rows that rope_f16 and kv_append_rope
+ * take; attention_paged gives the f16 rows that they take as x and A.
+ */
+enum {
+  W4_F16 = 0,  /* f16 */
+  W4_F32 = 1,  /* f32 */
+  W4_E4M3 = 2  /* 8-bit floats: 4 exponent bits, 3 mantissa bits, no infinities, largest 448 */
+};
+
+/*
+ * A paged key/value cache (the struct itself is host memory, read during the call).  Token t of
+ * page p of kv head h has its dim elements at  k + p * stride_page + h * stride_head +
+ * t * stride_token  (elements; v alike, with the same strides), so both [pages][heads]
+ * [page_size][dim] and [pages][page_size][heads][dim] fit.  type: W4_F16, or W4_E4M3, whose
+ * value is code * scale[head] (k_scale, v_scale: device f32 [heads], positive; NULL: 1).
+ * Requires pages, page_size, heads >= 1, pages * page_size < 2^31, heads <= 1024, dim a multiple
+ * of 8 (e4m3: 16), 8 <= dim <= 256; k and v 16-byte aligned, strides >= 0 and multiples of 16 bytes;
+ * distinct tokens must not share elements.
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t pages, page_size, heads, dim;
+  int64_t stride_page, stride_head, stride_token;
+  int32_t type;
+} w4_kv_cache;
+
+/*
+ * rope_f16 -- rotary positions: y = f16 of x with the first R dims of every head rotated.
+ *   x   [T][H][D] f16 or f32 (x_type W4_F16, W4_F32), the heads of a token contiguous, ldx
+ *       elements between tokens;  y f16 [T][H][D], ldy;  pos int32 [T];  freq f32 [R/2];
+ *   pair i of a head: dims (i, i + R/2), or (2i, 2i + 1) if interleaved != 0;
+ *   (a, b) -> mscale * (a cos - b sin, b cos + a sin) of the angle pos[t] * freq[i], which is
+ *   reduced in f64 (positions of any size keep their precision); inverse != 0 negates the angle,
+ *   which is the gradient of the rotation.  Dims from R on are passed on.  Any scaling for long
+ *   contexts is in freq and mscale.
+ * Requires T, H >= 1, T < 2^24, H <= 1024, D % 8 == 0, 8 <= D <= 256, R even, 0 <= R <= D (freq may be NULL at
+ * 0), ldx, ldy >= H * D and multiples of 8, mscale finite; x, y 16-byte aligned, pos, freq 4-byte.
+ * y may be x (f16, ldy == ldx); any other overlap is not allowed.  Products and sums are f32,
+ * rounded once to f16.
+ */
+int rope_f16(const void* x, int32_t x_type, int64_t ldx, const int32_t* pos, const float* freq, uint16_t* y,
+             int64_t ldy, int64_t T, int64_t H, int64_t D, int64_t R, int32_t interleaved, int32_t inverse,
+             float mscale, w4_stream_t stream);
+
+/*
+ * kv_append_rope -- T new tokens into a paged cache, with the rotation on the way, in one launch:
+ *   K of the cache's slot[t] = rotated k[t], V = v[t], q_out[t] = f16 of the rotated q[t]
+ * rotated as by rope_f16 (R, interleaved, mscale, pos, freq).  q [T][Hq][dim], k, v [T][heads][dim], all f16
+ * or all f32 (x_type); q_out f16 [T][Hq][dim].  q and q_out may both be NULL (no queries).
+ * slot int64 [T]: page * page_size + token of the page.  A slot below 0 or past the cache is
+ * not written (padding tokens: -1); slots have to be distinct (two tokens of one slot leave
+ * either's values, dim by dim).  Nothing else of the cache is touched.  An f16 cache takes one rounding
+ * from f32; an e4m3 cache takes value / scale, rounded to nearest even and saturated at +-448
+ * (NaN stays NaN).
+ * Requires what rope_f16 requires of T, Hq, R, the ld's, the alignment and mscale, and of the
+ * cache what w4_kv_cache says; slot 8-byte aligned.  q_out may be q (f16, ldqo == ldq).
+ */
+int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
+                   const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot,
+                   const int32_t* pos, const float* freq, int64_t T, int64_t R, int32_t interleaved, float mscale,
+                   w4_stream_t stream);
+
+/*
+ * attention_paged -- attention of the new tokens of B sequences over a paged cache that holds
+ * their keys and values already (kv_append_rope before it on the stream): single tokens of
+ * decode, draft tokens, chunks of a prompt, mixed.
+ *   q f16 [T][Hq][dim] (ldq), out f16 [T][Hq][dim] (ldo); query head h reads kv head
+ *   h / (Hq / heads);  q_start int32 [B + 1]: sequence b has the rows q_start[b] ..
+ *   q_start[b+1] - 1; NULL: one row each (T == B);  kv_len int32 [B]: its cached tokens, the new ones
+ *   included;  table int32 [B][W] (row stride ldt): page j of a sequence holds its tokens
+ *   j * page_size ...
+ * Row i of a sequence with n rows stands at p = kv_len - n + i and sees the keys
+ * max(0, p + 1 - window) <= j <= p (window 0: all of 0 .. p):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j.
+ * A row that sees no key (kv_len < n, or 0) is 0.  Rows that belong to no sequence are left as
+ * they were.  What no row sees (pages past a sequence's end, tokens of a page past
+ * it, tokens outside the window) does not reach the result, whatever it holds.  Lengths, starts
+ * and the table are read on the device (a captured graph may be replayed as they grow) and kept
+ * in bounds there: starts to 0 .. T, kv_len to 0 .. W * page_size; a page number outside the cache
+ * is not read, and the rows that would see it are NaN.
+ * max_q: no sequence has more rows (1: decode); rows past it in a sequence are unspecified.
+ * Scores, the softmax and its sums are f32; the weights are rounded to f16 before their product
+ * with v, the result once to f16.
+ * Requires B, W, max_q >= 1, T < 2^24, B <= 2^20, B <= T when q_start is NULL, max_q <= T,
+ * 1 <= Hq <= 1024, Hq % heads == 0, W * page_size <= 2^30, ldt >= W, window >= 0, scale > 0 and finite,
+ * ldq, ldo >= Hq * dim and multiples of 8; q, out 16-byte aligned, the int32 arrays 4-byte.  The cache:
+ * see w4_kv_cache.  Workspace (query it): partial results where the keys of a row are split over
+ * workgroups; contents need no initialisation.  Deterministic.
+ */
+int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
+                    int64_t W, const int32_t* kv_len, const int32_t* q_start, int64_t B, int64_t T, int64_t max_q,
+                    int64_t Hq, int64_t window, float scale, uint16_t* out, int64_t ldo, void* ws, size_t* ws_bytes,
+                    w4_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

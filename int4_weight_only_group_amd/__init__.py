@@ -13,15 +13,17 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 import torch
 
-from ._lib import lib, LIB_PATH  # noqa: F401
+from ._lib import KvCache, lib, LIB_PATH  # noqa: F401
 
 __all__ = [
     "W4Error", "w4_pack", "w4_quantize", "w4_gemv", "w4_gemv_sym128", "w4_dequant_f16_t_sym128", "w4_dequant_f16_t", "gemm_f16", "gemm_f16_dequant_next", "gemm_f16_dequant_next_sym128", "logits_argmax_topk",
     "logits_argmax_topk_noalloc", "w4_gemv_topk", "gemv_topk_workspace_bytes",
     "topk_workspace_bytes", "gemm_workspace_bytes", "status_string",
+    "rope_frequencies", "rope_f16", "kv_append_rope", "attention_paged", "attention_workspace_bytes",
 ]
 
 W4_OK = 0
@@ -439,3 +441,230 @@ def w4_gemv_topk(qw: torch.Tensor, scales: torch.Tensor, biases: torch.Tensor, x
                                               v, kdim, k, logits.data_ptr(), idx.data_ptr(), val.data_ptr(),
                                               ws_ptr, cap, _stream()))
     return logits, idx, val
+
+
+# ------------------------------------------------- rotary positions, paged cache, attention
+
+_F16, _F32, _E4M3 = 0, 1, 2
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                     original: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device: str | torch.device = "cuda") -> tuple[torch.Tensor, float]:
+    """(freq float32 [rot/2], mscale) for rope_f16 and kv_append_rope: freq[i] = base^(-2i / rot),
+    for contexts `factor` times as long as the model was trained on changed by `scaling`:
+    "linear" divides every frequency by factor; "ntk" raises the base to
+    base * factor^(rot / (rot - 2)), which divides the lowest frequency by factor and leaves the
+    highest; "yarn" divides the frequencies that turn less than beta_slow times in `original` positions,
+    leaves those that turn more than beta_fast times, blends between in the pair's index, and
+    has mscale 0.1 ln(factor) + 1."""
+    if rot < 0 or rot % 2 or base <= 1.0 or factor < 1.0:
+        raise ValueError("rot must be even and not negative, base > 1, factor >= 1")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("ntk needs rot >= 4")
+        base = base * factor ** (rot / (rot - 2))
+    freq = base ** (-2.0 * i / max(rot, 1))
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        if original < 1 or not beta_fast > beta_slow > 0:
+            raise ValueError("yarn needs original >= 1 and beta_fast > beta_slow > 0")
+
+        def index(turns):  # the (real) index of the pair that turns so often in `original` positions
+            return rot * math.log(original / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        lo = max(math.floor(index(beta_fast)), 0)
+        hi = min(math.ceil(index(beta_slow)), rot - 1)
+        ramp = ((i - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        freq = freq * (1.0 - ramp) + freq / factor * ramp
+        mscale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in (None, "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.float().to(device), mscale
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> int:
+    """Elements between the tokens of a [tokens][heads][dim] tensor with contiguous heads."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    _dev(t, name, t.dtype if dtype is None else dtype)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens][heads][dim]")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return s0 if n > 1 else max(s0, h * d)
+
+
+def _row_type(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.float32:
+        return _F32
+    if t.dtype == torch.float16:
+        return _F16
+    raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+
+
+def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> int:
+    _dev(t, name, dtype)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and hold {n} elements")
+    return t.data_ptr()
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
+    _dev(k_cache, "k_cache", k_cache.dtype if isinstance(k_cache, torch.Tensor) else torch.float16)
+    _dev(v_cache, "v_cache", k_cache.dtype)
+    if k_cache.dtype == torch.float16:
+        kind = _F16
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a float16 cache takes no scales")
+    elif k_cache.dtype == torch.float8_e4m3fn:
+        kind = _E4M3
+    else:
+        raise TypeError(f"the caches must be torch.float16 or torch.float8_e4m3fn, got {k_cache.dtype}")
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [pages][kv heads][page size][dim]")
+    shape, st = k_cache.shape, k_cache.stride()
+    stv = v_cache.stride()
+    if (st[3] != 1 and shape[3] > 1) or any(a != b and n > 1 for a, b, n in zip(st, stv, shape)):
+        raise ValueError("k_cache and v_cache must have the same strides and a contiguous dim")
+    c = KvCache()
+    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
+    if k_scale is not None:
+        c.k_scale = _vec(k_scale, "k_scale", torch.float32, shape[1])
+    if v_scale is not None:
+        c.v_scale = _vec(v_scale, "v_scale", torch.float32, shape[1])
+    c.pages, c.heads, c.page_size, c.dim = shape
+    c.stride_page, c.stride_head, c.stride_token = (s if n > 1 else 0 for s, n in zip(st, shape[:3]))
+    c.type = kind
+    return c
+
+
+def rope_f16(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, interleaved: bool = False,
+             mscale: float = 1.0, inverse: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary positions: x float16 or float32 [T][H][D] (heads contiguous), positions int32 [T],
+    freq float32 [R/2] (see rope_frequencies) -> float16 [T][H][D] with the first R dims of every
+    head rotated by positions * freq, times mscale.  Pairs are (i, i + R/2), or (2i, 2i + 1) if
+    interleaved.  inverse rotates back: the gradient of the rotation.  out may be x (float16)."""
+    ldx = _rows(x, "x")
+    kind = _row_type(x, "x")
+    t, h, d = x.shape
+    if out is None:
+        out = torch.empty((t, h, d), dtype=torch.float16, device=x.device)
+    ldy = _rows(out, "out", torch.float16)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    rot = 2 * freq.numel()
+    _check("rope_f16", lib().rope_f16(x.data_ptr(), kind, ldx, _vec(positions, "positions", torch.int32, t),
+                                      _vec(freq, "freq", torch.float32, rot // 2) if rot else None, out.data_ptr(),
+                                      ldy, t, h, d, rot, interleaved, inverse, mscale, _stream()))
+    return out
+
+
+def kv_append_rope(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                   slots: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *,
+                   q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, interleaved: bool = False,
+                   mscale: float = 1.0, k_scale: torch.Tensor | None = None,
+                   v_scale: torch.Tensor | None = None) -> torch.Tensor | None:
+    """New tokens into a paged cache with the rotation on the way (see rope_f16), one launch.
+
+    k, v [T][kv heads][dim] and q [T][heads][dim], all float16 or all float32 (views of the rows
+    of one q|k|v product will do); caches [pages][kv heads][page size][dim], any strides with a
+    contiguous dim, float16 or float8_e4m3fn (value = code * scale[head], scales float32 [kv heads]);
+    slots int64 [T] = page * page size + token of the page, distinct, -1: not written.
+    Returns the rotated queries, float16 (None without q)."""
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    ldk = _rows(k, "k")
+    kind = _row_type(k, "k")
+    ldv = _rows(v, "v", k.dtype)
+    t, heads, d = k.shape
+    if v.shape != k.shape or heads != c.heads or d != c.dim:
+        raise ValueError("k and v must be [T][kv heads][dim] of the cache")
+    ldq = ldqo = hq = 0
+    if q is not None:
+        ldq = _rows(q, "q", k.dtype)
+        hq = q.shape[1]
+        if q.shape[0] != t or q.shape[2] != d:
+            raise ValueError("q must be [T][heads][dim] with k's T and dim")
+        if q_out is None:
+            q_out = torch.empty((t, hq, d), dtype=torch.float16, device=q.device)
+        ldqo = _rows(q_out, "q_out", torch.float16)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = 2 * freq.numel()
+    _check("kv_append_rope", lib().kv_append_rope(
+        None if q is None else q.data_ptr(), ldq, None if q is None else q_out.data_ptr(), ldqo, hq, k.data_ptr(), ldk,
+        v.data_ptr(), ldv, kind, c, _vec(slots, "slots", torch.int64, t),
+        _vec(positions, "positions", torch.int32, t),
+        _vec(freq, "freq", torch.float32, rot // 2) if rot else None, t, rot, interleaved, mscale, _stream()))
+    return q_out
+
+
+def attention_workspace_bytes(k_cache: torch.Tensor, b: int, t: int, max_q: int, heads: int, pages_per_seq: int,
+                              window: int = 0) -> int:
+    """Workspace bytes attention_paged needs for t query rows of b sequences over this cache, with
+    tables of pages_per_seq pages."""
+    c = _kv_cache(k_cache, k_cache, None, None)
+    need = ctypes.c_size_t(0)
+    p, ld = 16, heads * int(c.dim)
+    _check("attention_paged", lib().attention_paged(p, ld, c, p, pages_per_seq, pages_per_seq, p, p, b, t, max_q,
+                                                    heads, window, 1.0, p, ld, None, ctypes.byref(need), None))
+    return int(need.value)
+
+
+def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                    kv_len: torch.Tensor, *, q_start: torch.Tensor | None = None, max_q: int | None = None,
+                    scale: float | None = None, window: int = 0, k_scale: torch.Tensor | None = None,
+                    v_scale: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the new tokens of B sequences over a paged cache that holds them already.
+
+    q float16 [T][heads][dim]: sequence b has the rows q_start[b] .. q_start[b+1] - 1 (q_start
+    int32 [B + 1]; None: one row each); kv_len int32 [B]: its cached tokens, the new ones included;
+    table int32 [B][pages of a sequence]; caches and scales as for kv_append_rope.  Row i of n
+    stands at p = kv_len - n + i and sees the keys max(0, p + 1 - window) .. p (window 0: from 0);
+    scale defaults to dim ** -0.5.  max_q: the longest sequence's rows (default: T; give it, 1 for
+    decode: it chooses the kernel).  Returns float16 [T][heads][dim]; a row that sees no key is 0,
+    rows past the last sequence are not written.  One is allocated for out and the workspace
+    (attention_workspace_bytes) when not given or too small."""
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    ldq = _rows(q, "q", torch.float16)
+    t, hq, d = q.shape
+    if d != c.dim:
+        raise ValueError("q must have the cache's dim")
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=torch.float16, device=q.device)
+    ldo = _rows(out, "out", torch.float16)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    _dev(table, "table", torch.int32)
+    ldt = _rowmajor(table, "table")
+    b, width = table.shape
+    len_ptr = _vec(kv_len, "kv_len", torch.int32, b)
+    start_ptr = None
+    if q_start is not None:
+        start_ptr = _vec(q_start, "q_start", torch.int32, b + 1)
+        if max_q is None:
+            max_q = t
+    elif max_q is None:
+        max_q = 1
+    if scale is None:
+        scale = d ** -0.5
+    args = (q.data_ptr(), ldq, c, table.data_ptr(), ldt, width, len_ptr, start_ptr, b, t, max_q, hq, window, scale,
+            out.data_ptr(), ldo)
+    size = ctypes.c_size_t(0)
+    fn = lib().attention_paged
+    _check("attention_paged", fn(*args, None, ctypes.byref(size), None))
+    ws_ptr = None
+    if size.value:
+        if workspace is None or workspace.numel() * workspace.element_size() < size.value:
+            workspace = torch.empty(size.value, dtype=torch.uint8, device=q.device)
+        ws_ptr = workspace.data_ptr()
+    _check("attention_paged", fn(*args, ws_ptr, ctypes.byref(size) if ws_ptr else None, _stream()))
+    return out

@@ -1,10 +1,12 @@
 // The C ABI (include/w4.h): argument checks on the host, then one launch path per call.
 // Nothing here allocates device memory or keeps per-call state.
 #include <atomic>
+#include <cmath>
 #include <cstring>
 
 #include "../../include/w4.h"
 #include "w4_internal.h"
+#include "w4_kv.h"
 
 namespace {
 
@@ -101,6 +103,42 @@ int gemm_dequant_next(const uint16_t* A, int64_t lda, const uint16_t* B, int64_t
   w4::launch_gemm_dequant(A, lda, B, ldb, C, ldc, (int)M, (int)N, (int)K, ws, qw, scales, biases, wt, ldwt, (int)Nq,
                           (int)Kq, sym, (hipStream_t)stream);
   return launched();
+}
+
+constexpr int64_t kMaxTokens = (int64_t)1 << 24, kMaxHeads = 1024, kMaxHeadDim = 256;
+
+// x rows [T][H][D] (f16 or f32, the heads of a token contiguous) and their rotation
+int check_rows(const void* x, int64_t ld, int64_t H, int64_t D) {
+  if (H < 1 || H > kMaxHeads || ld < H * D || ld > kMaxDim) return W4_ERR_SHAPE;
+  if (!al16(x) || ld % 8 != 0) return W4_ERR_ALIGN;
+  return W4_OK;
+}
+int check_rope(int64_t T, int64_t D, int64_t R, int32_t x_type, const int32_t* pos, const float* freq, float mscale) {
+  if (!pos || (!freq && R > 0)) return W4_ERR_NULL;
+  if (T < 1 || T >= kMaxTokens || D < 8 || D > kMaxHeadDim || D % 8 != 0 || R < 0 || R > D || R % 2 != 0)
+    return W4_ERR_SHAPE;
+  if ((x_type != W4_F16 && x_type != W4_F32) || !std::isfinite(mscale)) return W4_ERR_SHAPE;
+  if (!al4(pos) || !al4(freq)) return W4_ERR_ALIGN;
+  return W4_OK;
+}
+
+// w4_kv_cache's requirements; on W4_OK c is the kernels' view of it
+int check_cache(const w4_kv_cache* h, w4::KvCache& c) {
+  if (!h || !h->k || !h->v) return W4_ERR_NULL;
+  if (h->type != W4_F16 && h->type != W4_E4M3) return W4_ERR_SHAPE;
+  const bool e4m3 = h->type == W4_E4M3;
+  const int64_t unit = e4m3 ? 16 : 8, most = ((int64_t)1 << 31) - 1;
+  if (h->pages < 1 || h->page_size < 1 || h->pages > most || h->page_size > most / h->pages) return W4_ERR_SHAPE;
+  if (h->heads < 1 || h->heads > kMaxHeads || h->dim < 8 || h->dim > kMaxHeadDim || h->dim % unit != 0)
+    return W4_ERR_SHAPE;
+  for (int64_t s : {h->stride_page, h->stride_head, h->stride_token}) {
+    if (s < 0 || s > ((int64_t)1 << 40)) return W4_ERR_SHAPE;
+    if (s % unit != 0) return W4_ERR_ALIGN;
+  }
+  if (!al16(h->k) || !al16(h->v) || !al4(h->k_scale) || !al4(h->v_scale)) return W4_ERR_ALIGN;
+  c = {h->k, h->v, h->k_scale, h->v_scale, h->stride_page, h->stride_head, h->stride_token,
+       (int)h->pages, (int)h->page_size, (int)h->heads, (int)h->dim, e4m3};
+  return W4_OK;
 }
 
 }  // namespace
@@ -333,6 +371,84 @@ int logits_argmax_topk_noalloc(const float* logits, int64_t ldl, int64_t M, int6
     if (scratch == nullptr) return W4_ERR_INTERNAL;
     (void)hipGetLastError();
     w4::launch_topk(logits, ldl, (int)M, (int)V, (int)k, idx, val, scratch, (hipStream_t)stream);
+    return launched();
+  } catch (...) {
+    return W4_ERR_INTERNAL;
+  }
+}
+
+int rope_f16(const void* x, int32_t x_type, int64_t ldx, const int32_t* pos, const float* freq, uint16_t* y,
+             int64_t ldy, int64_t T, int64_t H, int64_t D, int64_t R, int32_t interleaved, int32_t inverse,
+             float mscale, w4_stream_t stream) {
+  try {
+    if (!x || !y) return W4_ERR_NULL;
+    if (int e = check_rope(T, D, R, x_type, pos, freq, mscale)) return e;
+    if (int e = check_rows(x, ldx, H, D)) return e;
+    if (int e = check_rows(y, ldy, H, D)) return e;
+    if (int e = check_device()) return e;
+    (void)hipGetLastError();
+    w4::launch_rope(x, x_type == W4_F32, ldx, pos, freq, y, ldy, (int)T, (int)H, (int)D, (int)R, interleaved != 0,
+                    inverse != 0, mscale, (hipStream_t)stream);
+    return launched();
+  } catch (...) {
+    return W4_ERR_INTERNAL;
+  }
+}
+
+int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
+                   const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot,
+                   const int32_t* pos, const float* freq, int64_t T, int64_t R, int32_t interleaved, float mscale,
+                   w4_stream_t stream) {
+  try {
+    if (!k || !v || !slot || (!q) != (!q_out)) return W4_ERR_NULL;
+    w4::KvCache c;
+    if (int e = check_cache(cache, c)) return e;
+    if (int e = check_rope(T, c.dim, R, x_type, pos, freq, mscale)) return e;
+    if (int e = check_rows(k, ldk, c.heads, c.dim)) return e;
+    if (int e = check_rows(v, ldv, c.heads, c.dim)) return e;
+    if (q) {
+      if (int e = check_rows(q, ldq, Hq, c.dim)) return e;
+      if (int e = check_rows(q_out, ldqo, Hq, c.dim)) return e;
+    }
+    if (((uintptr_t)slot & 7u) != 0) return W4_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    (void)hipGetLastError();
+    w4::launch_kv_append(q, ldq, q_out, ldqo, (int)Hq, k, ldk, v, ldv, x_type == W4_F32, c, slot, pos, freq, (int)T,
+                         (int)R, interleaved != 0, mscale, (hipStream_t)stream);
+    return launched();
+  } catch (...) {
+    return W4_ERR_INTERNAL;
+  }
+}
+
+int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
+                    int64_t W, const int32_t* kv_len, const int32_t* q_start, int64_t B, int64_t T, int64_t max_q,
+                    int64_t Hq, int64_t window, float scale, uint16_t* out, int64_t ldo, void* ws, size_t* ws_bytes,
+                    w4_stream_t stream) {
+  try {
+    if (!q || !table || !kv_len || !out) return W4_ERR_NULL;
+    w4::KvCache c;
+    if (int e = check_cache(cache, c)) return e;
+    if (T < 1 || T >= kMaxTokens || B < 1 || B > ((int64_t)1 << 20) || max_q < 1 || max_q > T) return W4_ERR_SHAPE;
+    if (!q_start && (B > T || max_q != 1)) return W4_ERR_SHAPE;
+    if (W < 1 || W > ((int64_t)1 << 30) / c.page_size || ldt < W || ldt > kMaxDim) return W4_ERR_SHAPE;
+    if (Hq < 1 || Hq % c.heads != 0 || window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return W4_ERR_SHAPE;
+    if (int e = check_rows(q, ldq, Hq, c.dim)) return e;
+    if (int e = check_rows(out, ldo, Hq, c.dim)) return e;
+    if (!al4(table) || !al4(kv_len) || !al4(q_start)) return W4_ERR_ALIGN;
+    w4::AttnArgs a;
+    a.q = q, a.out = out, a.ldq = ldq, a.ldo = ldo, a.c = c;
+    a.table = table, a.ldt = ldt, a.kv_len = kv_len, a.q_start = q_start;
+    a.W = (int)W, a.B = (int)B, a.T = (int)T, a.max_q = (int)max_q, a.Hq = (int)Hq;
+    a.window = window >= ((int64_t)1 << 30) ? 0 : (int)window;  // no sequence is longer
+    a.scale = scale;
+    const size_t need = w4::attention_ws_bytes(a);
+    const int w = workspace(ws, ws_bytes, need);
+    if (w < 0) return w;
+    if (w == 1) return W4_OK;
+    if (int e = check_device()) return e;
+    (void)hipGetLastError();
+    w4::launch_attention(a, need ? ws : nullptr, (hipStream_t)stream);
     return launched();
   } catch (...) {
     return W4_ERR_INTERNAL;
