@@ -332,7 +332,7 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
  * Scores, the softmax and its sums are f32; the weights are rounded to f16 before their product
  * with v, the result once to f16.
  * Requires B, W, max_q >= 1, T < 2^24, B <= 2^20, B <= T when q_start is NULL, max_q <= T,
- * 1 <= Hq <= 1024, Hq % heads == 0, W * page_size <= 2^30, ldt >= W, window >= 0, scale > 0 and finite,
+ * 1 <= Hq <= 1024, Hq % heads == 0, T * Hq <= 2^30, W * page_size <= 2^30, ldt >= W, window >= 0, scale > 0 and finite,
  * ldq, ldo >= Hq * dim and multiples of 8; q, out 16-byte aligned, the int32 arrays 4-byte.  The cache:
  * see w4_kv_cache.  Workspace (query it): partial results where the keys of a row are split over
  * workgroups; contents need no initialisation.  Deterministic.

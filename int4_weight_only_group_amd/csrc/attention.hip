@@ -1,9 +1,22 @@
 // attention_paged: softmax(scale q k^T) v of new tokens over a paged cache.
 //
 // Query i of a sequence with n new and L cached tokens stands at position p = L - n + i and sees
-// the keys max(0, p + 1 - window) <= j <= p.  Keys are taken in blocks; m, the largest score so
-// far, and l, the sum of exp(s - m), are kept in f32, and what was summed before is scaled by
-// exp(m_old - m_new) whenever m grows:  out = sum_j exp(s_j - m) v_j / l.
+// the keys max(0, p + 1 - window) <= j <= p.  Keys are taken in tiles; m, about the largest score
+// so far, and l, the sum of exp(s - m), are kept in f32 per row, and what was summed before is
+// scaled by exp(m_old - m_new) when m moves:  out = sum_j exp(s_j - m) v_j / l.  Scores are kept
+// in units of log 2 (the scale carries log2 e), so the exponential is exp2.
+//
+// Rows.  The G = Hq / Hkv query heads of a kv head read the same keys, so a row is a (token, head
+// of the group) pair, numbered token * G + head, and a tile of keys serves them all.
+//
+// Both kernels compute S^T = K Q^T and O^T = V^T P^T on the matrix cores, with q rows as columns:
+// a lane then holds scores of one row only (m, l and the rescaling are per-lane scalars), and the
+// accumulator layout of S^T is the operand layout of P^T up to the order of the keys, which V's
+// transposing LDS reads follow; the weights never leave their lane.
+//
+// Keys that no row of the workgroup sees are not read: zeros stand in for them (what a page holds
+// past its sequence's end may be anything).  A page number outside the cache gives NaN keys.
+#include <algorithm>
 #include <cmath>
 
 #include "w4_internal.h"
@@ -13,95 +26,947 @@ namespace w4 {
 
 namespace {
 
-// One wave per (token, query head): 64 keys at a time, a key per lane for the scores and
-// D/64 dims per lane for the sums over v.
-__global__ __launch_bounds__(64) void attention_row_kernel(AttnArgs g) {
-  __shared__ float qs[256];
-  const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x, D = g.c.dim;
-  int b = 0, first = t, n = 1;
+typedef __attribute__((address_space(3))) void lds_void_t;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// m moves only when a score exceeds it by more than this (in powers of two): weights stay below
+// 2^8, which f16 and the f32 sums hold, and most tiles then rescale nothing.
+constexpr float kSlack = 8.f;
+
+alignas(16) __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
+alignas(16) __device__ const uint32_t kNans[4] = {0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u};
+
+// LDS DMA: lane l's 16 (4) bytes land at lds + 16 l (4 l).  Inline asm, because the compiler would
+// wait for all of it before every later LDS read; the kernels wait explicitly.  The s_nop covers the
+// wait states after the write of m0.
+__device__ __forceinline__ void dma16(const void* p, uint32_t lds) {
+  asm volatile("s_nop 1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+__device__ __forceinline__ void dma4(const void* p, uint32_t lds) {
+  asm volatile("s_nop 1\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt holds 0..63");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// f over the lanes l, l ^ 32 (and l ^ 16): every lane gets the result
+template <bool QUARTERS, class F>
+__device__ __forceinline__ float across(float v, F f) {
+  uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto h = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  uint32_t a = h[0], b = h[1];
+  v = f(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+  if constexpr (QUARTERS) {
+    x = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    a = r[0], b = r[1];
+    v = f(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+  }
+  return v;
+}
+__device__ __forceinline__ float fmax2(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float add2(float a, float b) { return a + b; }
+
+// LDS layout of a tile: key row r holds DP f16 = DP / 8 chunks of 16 bytes; chunk c of it lies at
+// chunk c ^ k_swz(r) (K: 16-byte reads of 16 rows at one chunk touch all 64 banks) or c ^ v_swz(r)
+// (V: transposing reads of 4 rows x 4 chunks, or 8 rows x 2, do).  With DP = 64 two rows share
+// the 256 bytes of the banks, so their parity is part of the bank already.
+template <int DP>
+__device__ __forceinline__ int k_swz(int r) {
+  return DP == 64 ? (r >> 1) & 7 : r & 15;
+}
+template <int DP>
+__device__ __forceinline__ int v_swz(int r) {
+  return DP == 64 ? ((r >> 1) & 1) << 2 | ((r >> 2) & 1) << 1 : (r & 3) << 2 | ((r >> 2) & 1) << 1;
+}
+
+// n / d for 0 <= n < 2^31: (n * mul) >> shift, mul = floor(2^shift / d) + 1, shift = 31 + ceil(log2 d).
+// The product's error is below n / 2^shift < 1 / d, so the floor is exact.
+struct Divider {
+  uint64_t mul;
+  int shift, d;
+};
+Divider divider(int d) {
+  int s = 0;
+  while (((int64_t)1 << s) < d) ++s;
+  return {(((uint64_t)1 << (31 + s)) / (uint64_t)d) + 1, 31 + s, d};
+}
+// mul <= 2^32 (d a power of two: 2^31 + 1), so the product is below 2^63 + 2^31
+__device__ __forceinline__ int divide(int n, const Divider& d) { return (int)(((uint64_t)(uint32_t)n * d.mul) >> d.shift); }
+
+struct Plan {
+  AttnArgs a;
+  Divider page, group;
+  int G, splits;
+  int tiles, keys;  // many rows: row tiles at most, keys of a tile
+  bool skip_short;  // both kernels run: sequences of at most kFewRows rows are the first one's
+  float c;          // scale * log2 e
+  float* part;      // [work item][split][rows][dim] sums, then [..][rows][2] (m, l)
+};
+
+constexpr int kFewRows = 16;  // rows of the decode kernel's tile
+
+struct Seq {
+  int first, n, len;  // first row, rows, cached tokens
+};
+__device__ __forceinline__ Seq sequence(const AttnArgs& g, int b) {
+  Seq s;
   if (g.q_start) {
-    int lo = 0, hi = g.B;  // the last sequence that starts at or before t
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (g.q_start[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    first = g.q_start[b];
-    n = min(g.q_start[b + 1], g.T) - first;
-    if (t < first || t >= first + n) return;
+    s.first = min(max(g.q_start[b], 0), g.T);
+    s.n = min(max(g.q_start[b + 1], s.first), g.T) - s.first;
   } else {
-    if (t >= g.B) return;
-    b = t;
+    s.first = b, s.n = 1;
   }
-  const int64_t most = (int64_t)g.W * g.c.page_size;
-  const int L = (int)max((int64_t)0, min((int64_t)g.kv_len[b], most));
-  const int p = L - n + (t - first), end = p + 1;  // keys below `end`
-  const int beg = g.window > 0 ? max(0, end - g.window) : 0;
-  const uint16_t* q = g.q + (int64_t)t * g.ldq + (int64_t)h * D;
-  for (int d = lane; d < D; d += 64) qs[d] = (float)__builtin_bit_cast(f16, q[d]);
-  __syncthreads();
-  const int kvh = h / (g.Hq / g.c.heads);
-  const float ks = g.c.e4m3 && g.c.k_scale ? g.c.k_scale[kvh] : 1.f;
-  const float vs = g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f;
-  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  bool bad = false;
-  for (int j0 = beg; j0 < end; j0 += 64) {
-    const int j = j0 + lane;
-    int64_t at = -1;
-    if (j < end) {
-      const int page = g.table[b * g.ldt + j / g.c.page_size];
-      if (page < 0 || page >= g.c.pages) bad = true;
-      else at = page * g.c.stride_page + kvh * g.c.stride_head + (j % g.c.page_size) * g.c.stride_token;
-    }
-    float s = -INFINITY;
-    if (at >= 0) {
-      float sum = 0.f;
-      for (int d = 0; d < D; ++d) {
-        const float k = g.c.e4m3
-                            ? __builtin_amdgcn_cvt_f32_fp8(reinterpret_cast<const uint8_t*>(g.c.k)[at + d], 0)
-                            : (float)reinterpret_cast<const f16*>(g.c.k)[at + d];
-        sum += qs[d] * k;
-      }
-      s = sum * (g.scale * ks);
-    }
-    float mt = s;
-    for (int x = 32; x; x >>= 1) mt = fmaxf(mt, __shfl_xor(mt, x));
-    const float mn = fmaxf(m, mt), ms = mn == -INFINITY ? 0.f : mn;
-    const float e = s == -INFINITY ? 0.f : expf(s - ms);
-    float sum = e;
-    for (int x = 32; x; x >>= 1) sum += __shfl_xor(sum, x);
-    const float al = m == -INFINITY ? 0.f : expf(m - ms);
-    l = l * al + sum;
-    m = mn;
-    for (int i = 0; i < 4; ++i) acc[i] *= al;
-    for (int x = 0; x < 64 && j0 + x < end; ++x) {
-      const float w = __shfl(e, x);
-      const int64_t va = __shfl((long long)at, x);
-      if (va < 0) continue;
-      for (int i = 0; i < 4; ++i) {
-        const int d = lane + 64 * i;
-        if (d < D)
-          acc[i] += w * (g.c.e4m3
-                             ? __builtin_amdgcn_cvt_f32_fp8(reinterpret_cast<const uint8_t*>(g.c.v)[va + d], 0)
-                             : (float)reinterpret_cast<const f16*>(g.c.v)[va + d]);
-      }
-    }
-  }
-  const float f = __any(bad) ? NAN : l == 0.f ? 0.f : vs / l;
-  uint16_t* out = g.out + (int64_t)t * g.ldo + (int64_t)h * D;
+  s.len = min(max(g.kv_len[b], 0), g.W * g.c.page_size);
+  return s;
+}
+
+// The keys [lo, hi) that the tokens t0 .. t1 of a sequence see (lo rounded down to `align`), in `act`
+// parts of `per` keys (the last may be shorter; one part of no keys writes the zeros).  per goes by
+// the sequence's length, so that the tiles of a prompt, whose lengths differ, have parts of one length.
+struct Keys {
+  int lo, hi, per, act;
+};
+__device__ __forceinline__ Keys keys_of(const Plan& p, const Seq& s, int t0, int t1, int align, int unit, int least) {
+  Keys k;
+  k.hi = max(0, s.len - s.n + t1 + 1);
+  k.lo = p.a.window ? max(0, s.len - s.n + t0 + 1 - p.a.window) : 0;
+  k.lo = min(k.lo / align * align, k.hi);
+  const int all = p.a.window ? k.hi - k.lo : s.len;
+  k.per = max(least, (max(all, k.hi - k.lo) + p.splits - 1) / p.splits);
+  k.per = (k.per + unit - 1) / unit * unit;
+  k.act = max(1, (k.hi - k.lo + k.per - 1) / k.per);
+  return k;
+}
+
+// 16 e4m3 codes as f16: exact (every value of the format is an f16)
+__device__ __forceinline__ void widen(const u32x4& v, f16x8 (&h)[2]) {
+#pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int d = lane + 64 * i;
-    if (d < D) out[d] = __builtin_bit_cast(uint16_t, (f16)(acc[i] * f));
+    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, false);
+    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, true);
+    h[i / 2][4 * (i & 1)] = (f16)a[0], h[i / 2][4 * (i & 1) + 1] = (f16)a[1];
+    h[i / 2][4 * (i & 1) + 2] = (f16)b[0], h[i / 2][4 * (i & 1) + 3] = (f16)b[1];
+  }
+}
+
+__device__ __forceinline__ bool any_special(const f16x8& v) {  // an infinity or NaN
+  const u32x4 x = __builtin_bit_cast(u32x4, v);
+  uint32_t bad = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= ((x[i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+  return bad != 0;
+}
+
+// A matrix product multiplies a weight of 0 with every v, and 0 * infinity is NaN: where some rows
+// of a tile do not see a key and its v is not finite, the finite values are multiplied as usual
+// and the others counted by kind with the weights' place taken by `seen` (1 where the row sees the
+// key); a row with a count gets the infinity or NaN.  cls: 0 finite, 1 +inf, 2 -inf, 3 NaN.
+__device__ __forceinline__ f16x8 of_kind(const f16x8& v, int cls) {
+  f16x8 o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint16_t x = __builtin_bit_cast(uint16_t, (f16)v[e]);
+    const int kind = (x & 0x7c00) != 0x7c00 ? 0 : (x & 0x3ff) ? 3 : (x & 0x8000) ? 2 : 1;
+    o[e] = kind != cls ? (f16)0.f : cls == 0 ? (f16)v[e] : (f16)1.f;
+  }
+  return o;
+}
+__device__ __forceinline__ float special(int cls) { return cls == 1 ? INFINITY : cls == 2 ? -INFINITY : NAN; }
+
+// ------------------------------------------------------------------------- few rows (decode)
+// At most 16 rows of a (sequence, kv head): decode, short drafts.  Bound: HBM, by the cache's bytes.
+// One workgroup per (sequence, kv head, part of the keys); its waves take 32-key tiles in turn,
+// each with LDS of its own and no barrier until the waves' sums are joined.  f16: a ring of two tiles,
+// tile t + 1 in flight while t is computed; page numbers run one tile further ahead, through LDS too
+// (in registers, the compiler's wait for them would be a wait for all tiles in flight).  e4m3: tile t + 1
+// is in flight in registers, and is widened to f16 on its way into LDS, exactly.
+constexpr int kFewKeys = 32;
+constexpr int kMinSplit = 128;  // keys of a part at least: a tile of each wave
+template <int DP>
+constexpr int few_waves() { return DP == 256 ? 2 : 4; }
+template <int DP, bool FP8>
+constexpr int few_ring() { return (FP8 ? 1 : 2) * 2 * kFewKeys * DP * 2; }  // bytes per wave
+template <int DP, bool FP8>
+constexpr int few_lds() { return few_waves<DP>() * (few_ring<DP, FP8>() + 1024); }
+
+template <int DP, bool FP8>
+__global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Plan p) {
+  constexpr int NW = few_waves<DP>(), KT = kFewKeys, TILE = KT * DP * 2, RING = few_ring<DP, FP8>();
+  constexpr int STEPS = DP / 32, DB = DP / 16;
+  extern __shared__ __align__(16) unsigned char lds[];
+  __shared__ float join[NW][16][2];
+  const AttnArgs& g = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x % p.splits, item = blockIdx.x / p.splits;
+  const int kvh = item % g.c.heads, b = item / g.c.heads;
+  const Seq s = sequence(g, b);
+  if (s.n == 0 || (p.skip_short && s.n * p.G > kFewRows)) return;  // those go to the other kernel
+  const int n = min(s.n, kFewRows / p.G), rows = n * p.G;
+  const Keys k = keys_of(p, s, 0, n - 1, 1, KT, kMinSplit);
+  if (split >= k.act) return;
+  const int k0 = k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
+  const int tiles = (k1 - k0 + KT - 1) / KT;
+  const int mine = tiles > wave ? (tiles - wave + NW - 1) / NW : 0;
+  const int D = g.c.dim;
+
+  unsigned char* ring = lds + wave * RING;
+  const int32_t* table = g.table + (int64_t)b * g.ldt;
+  auto first_key = [&](int t) { return k0 + (t * NW + wave) * KT; };
+
+  // Q^T operand: lane (row = lane % 16, grp = lane / 16), step t: dims 32 t + 8 grp ..
+  const int row = lane & 15, grp = lane >> 4;
+  const int tok = divide(min(row, rows - 1), p.group);
+  f16x8 q[STEPS];
+  {
+    const uint16_t* src = g.q + (int64_t)(s.first + tok) * g.ldq +
+                          (int64_t)(kvh * p.G + min(row, rows - 1) - tok * p.G) * D;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int d = 32 * t + 8 * grp;
+      f16x8 z = {};
+      q[t] = row < rows && d < D ? *reinterpret_cast<const f16x8*>(src + d) : z;
+    }
+  }
+  // the keys that this lane's row sees: [see0, see1); that all rows see: [all0, all1)
+  const int see1 = s.len - s.n + tok + 1, see0 = g.window ? see1 - g.window : 0;
+  const int all1 = s.len - s.n + 1, all0 = g.window ? s.len - s.n + n - g.window : 0;
+  const float c = FP8 && g.c.k_scale ? p.c * g.c.k_scale[kvh] : p.c;
+  float m = -INFINITY, l = 0.f;
+  f32x4 acc[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i) acc[i] = {0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](int t, const unsigned char* kt) {
+    const unsigned char* vt = kt + TILE;
+    const int j0 = first_key(t);
+    f32x4 sc[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      sc[kb] = {0.f, 0.f, 0.f, 0.f};
+      const int r = 16 * kb + row;
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const f16x8 a = *reinterpret_cast<const f16x8*>(kt + r * DP * 2 + (((4 * st + grp) ^ k_swz<DP>(r)) * 16));
+        sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[st], sc[kb], 0, 0, 0);
+      }
+    }
+    // sc[kb][e]: key j0 + 16 kb + 4 grp + e of this lane's row
+    auto seen = [&](int kb, int e) {
+      const int j = j0 + 16 * kb + 4 * grp + e;
+      return j >= see0 && j < see1;
+    };
+    const bool edge = j0 + KT > all1 || j0 < all0;
+    if (edge) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[kb][e] = seen(kb, e) ? sc[kb][e] : -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(sc[0][e], sc[1][e]));
+    top *= c;
+    if (__any(top > m + kSlack)) {
+      const float mn = fmaxf(m, across<true>(top, fmax2));
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) acc[i] *= f;
+      m = mn;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+    f16x8 w;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = __builtin_amdgcn_exp2f(sc[kb][e] * c - ms);
+        l += x;
+        w[4 * kb + e] = (f16)x;
+      }
+    // V^T operand: dims 16 i + lane % 16, keys 4 grp .. + 3 and 16 + 4 grp .. + 3
+    auto v_frag = [&](int i) {
+      s16x4 v[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = 16 * u + 4 * grp + ((lane & 15) >> 2), ch = 2 * i + ((lane & 3) >> 1);
+        v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+            vt + r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8));
+      }
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    bool odd = false;
+    if (edge && n > 1) {
+#pragma unroll
+      for (int i = 0; i < DB; ++i) odd |= any_special(v_frag(i));
+    }
+    if (__any(odd)) {
+      f16x8 one;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) one[e] = seen(e >> 2, e & 3) ? (f16)1.f : (f16)0.f;
+#pragma unroll
+      for (int i = 0; i < DB; ++i) {
+        const f16x8 v = v_frag(i);
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_kind(v, 0), w, acc[i], 0, 0, 0);
+        for (int cls = 1; cls < 4; ++cls) {
+          const f32x4 z = {0.f, 0.f, 0.f, 0.f};
+          const f32x4 cnt = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_kind(v, cls), one, z, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] += cnt[e] > 0.f ? special(cls) : 0.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < DB; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_frag(i), w, acc[i], 0, 0, 0);
+    }
+  };
+
+  if constexpr (!FP8) {
+    constexpr int CH = DP / 8, RPI = 64 / CH, NI = KT / RPI;  // chunks of a row; rows and count of a DMA instruction
+    const uint32_t ring_at = (uint32_t)(uintptr_t)(lds_void_t*)ring;
+    const int* ids = reinterpret_cast<const int*>(lds + NW * RING + wave * 1024);  // 4 tiles' page numbers
+    const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
+    auto fetch_ids = [&](int t) {
+      const int j = min(first_key(t) + (lane & 31), k1 - 1);
+      dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
+    };
+    const uint16_t* kbase = reinterpret_cast<const uint16_t*>(g.c.k) + kvh * g.c.stride_head;
+    const uint16_t* vbase = reinterpret_cast<const uint16_t*>(g.c.v) + kvh * g.c.stride_head;
+    auto fetch = [&](int t) {
+      const uint32_t st = ring_at + (t & 1) * 2 * TILE;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = i * RPI + lane / CH, ch = lane % CH;
+        const int j = first_key(t) + r, page = divide(j, p.page), id = ids[(t & 3) * 64 + r];
+        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token;
+        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+        const int ck = (ch ^ k_swz<DP>(r)) * 8, cv = (ch ^ v_swz<DP>(r)) * 8;
+        const void* ks = in && !good             ? (const void*)kNans
+                         : in && ck < D          ? (const void*)(kbase + at + ck)
+                                                 : (const void*)kZeros;
+        const void* vs = in && good && cv < D ? (const void*)(vbase + at + cv) : (const void*)kZeros;
+        dma16(ks, st + i * 1024);
+        dma16(vs, st + TILE + i * 1024);
+      }
+    };
+    // in the order of issue: data(t), ids(t + 2), data(t + 1), ids(t + 3), ...: a wait that leaves the
+    // newest data in flight covers the tile before it and the page numbers of the one after it
+    if (mine > 0) {
+      fetch_ids(0);
+      if (mine > 1) fetch_ids(1);
+      wait_vm<0>();
+      fetch(0);
+      if (mine > 2) fetch_ids(2);
+      if (mine > 1) fetch(1);
+    }
+    for (int t = 0; t < mine; ++t) {
+      if (t + 1 < mine)
+        wait_vm<2 * NI>();
+      else
+        wait_vm<0>();
+      compute(t, ring + (t & 1) * 2 * TILE);
+      if (t + 2 < mine) {
+        wait_lds();  // the stage has been read
+        if (t + 3 < mine) fetch_ids(t + 3);
+        fetch(t + 2);
+      }
+    }
+  } else {
+    constexpr int CH = DP / 16, RPI = 64 / CH, NI = KT / RPI;  // chunks of 16 codes
+    const uint8_t* kbase = reinterpret_cast<const uint8_t*>(g.c.k) + kvh * g.c.stride_head;
+    const uint8_t* vbase = reinterpret_cast<const uint8_t*>(g.c.v) + kvh * g.c.stride_head;
+    u32x4 kr[NI], vr[NI];
+    auto page_id = [&](int t) { return table[divide(min(first_key(t) + (lane & 31), k1 - 1), p.page)]; };
+    auto load = [&](int t, int ids) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = i * RPI + lane / CH, d = lane % CH * 16;
+        const int j = first_key(t) + r, page = divide(j, p.page), id = __shfl(ids, r);
+        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token + d;
+        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+        const uint32_t fill = in && !good ? 0x7f7f7f7fu : 0u;
+        kr[i] = {fill, fill, fill, fill};
+        vr[i] = {0, 0, 0, 0};
+        if (in && good && d < D) {
+          kr[i] = *reinterpret_cast<const u32x4*>(kbase + at);
+          vr[i] = *reinterpret_cast<const u32x4*>(vbase + at);
+        }
+      }
+    };
+    auto store = [&]() {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = i * RPI + lane / CH, ch = lane % CH * 2;
+        f16x8 h[2];
+        widen(kr[i], h);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<f16x8*>(ring + r * DP * 2 + ((ch + e) ^ k_swz<DP>(r)) * 16) = h[e];
+        widen(vr[i], h);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<f16x8*>(ring + TILE + r * DP * 2 + ((ch + e) ^ v_swz<DP>(r)) * 16) = h[e];
+      }
+    };
+    int ids = 0;
+    if (mine > 0) {
+      load(0, page_id(0));
+      if (mine > 1) ids = page_id(1);
+    }
+    for (int t = 0; t < mine; ++t) {
+      store();
+      if (t + 1 < mine) {
+        load(t + 1, ids);
+        if (t + 2 < mine) ids = page_id(t + 2);
+      }
+      compute(t, ring);
+    }
+  }
+
+  // join the waves: each leaves (m, l) and its sums in LDS
+  l = across<true>(l, add2);
+  float* sums = reinterpret_cast<float*>(ring);  // [16][DP + 4]
+  constexpr int LD = DP + 4;
+  static_assert(16 * LD * 4 <= RING, "a wave's sums fit in its ring");
+  wait_lds();
+#pragma unroll
+  for (int i = 0; i < DB; ++i) *reinterpret_cast<f32x4*>(&sums[row * LD + 16 * i + 4 * grp]) = acc[i];
+  if (grp == 0) join[wave][row][0] = m, join[wave][row][1] = l;
+  __syncthreads();
+  const int64_t part = ((int64_t)item * p.splits + split) * kFewRows;
+  float* sums_out = p.part + part * D;
+  float* ml_out = p.part + (int64_t)g.B * g.c.heads * p.splits * kFewRows * D + part * 2;
+  const float vs = FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
+    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+    float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) mt = fmaxf(mt, join[w][r][0]);
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float mw = join[w][r][0], f = mw == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw - mt);
+      lt += join[w][r][1] * f;
+      o += *reinterpret_cast<const f32x4*>(lds + w * RING + (r * LD + d) * 4) * f;
+    }
+    if (k.act > 1) {
+      *reinterpret_cast<f32x4*>(&sums_out[r * D + d]) = o;
+      if (d == 0) ml_out[2 * r] = mt, ml_out[2 * r + 1] = lt;
+    } else {
+      const int tk = divide(r, p.group);
+      const float f = lt == 0.f ? 0.f : vs / lt;
+      f16x4 h;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = (f16)(o[e] * f);
+      *reinterpret_cast<f16x4*>(g.out + (int64_t)(s.first + tk) * g.ldo + (int64_t)(kvh * p.G + r - tk * p.G) * D +
+                                d) = h;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ many rows
+// Chunks of prompts.  Bound: the matrix cores.  A workgroup takes 128 rows of a (sequence, kv head), 32 per
+// wave, and a part of their keys; the four waves share key tiles, double buffered in LDS: tile t + 1
+// is fetched while t is computed, one barrier per tile.
+constexpr int kManyRows = 128, kManyWaves = 4;
+template <int DP>
+constexpr int many_keys() { return DP == 256 ? 32 : 64; }
+template <int DP>
+constexpr int many_lds() { return 2 * 2 * many_keys<DP>() * DP * 2 + kManyWaves * 1024; }
+
+__device__ __forceinline__ int tiles_of(const Plan& p, int n) {
+  const int rows = n * p.G;
+  return p.skip_short && rows <= kFewRows ? 0 : (rows + kManyRows - 1) / kManyRows;
+}
+
+// The sequence and tile of the tile-th row tile of the batch; b = -1 past the last.  64 sequences at a
+// time, one per lane.
+__device__ __forceinline__ void locate(const Plan& p, int tile, int& b, int& at) {
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  for (int b0 = 0; b0 < p.a.B; b0 += 64) {
+    const int mine = b0 + lane < p.a.B ? tiles_of(p, sequence(p.a, b0 + lane).n) : 0;
+    int incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int x = __shfl_up(incl, d);
+      if (lane >= d) incl += x;
+    }
+    const unsigned long long hit = __ballot(base + incl > tile);
+    if (hit) {
+      const int at_lane = __builtin_ctzll(hit);
+      b = b0 + at_lane;
+      at = tile - base - (__shfl(incl, at_lane) - __shfl(mine, at_lane));
+      b = __builtin_amdgcn_readfirstlane(b);
+      at = __builtin_amdgcn_readfirstlane(at);
+      return;
+    }
+    base += __shfl(incl, 63);
+  }
+  b = -1, at = 0;
+}
+
+template <int DP, bool FP8>
+__global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan p) {
+  constexpr int NW = kManyWaves, KT = many_keys<DP>(), TILE = KT * DP * 2, RW = KT / NW;
+  constexpr int STEPS = DP / 16, DB = DP / 32, KB = KT / 32;
+  extern __shared__ __align__(16) unsigned char lds[];
+  const AttnArgs& g = p.a;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // the last tiles of a sequence see the most keys: they go first
+  const int kvh = blockIdx.x % g.c.heads, rest = blockIdx.x / g.c.heads;
+  const int split = rest % p.splits, slot = p.tiles - 1 - rest / p.splits;
+  int b, tile;
+  locate(p, slot, b, tile);
+  if (b < 0) return;
+  const Seq s = sequence(g, b);
+  const int D = g.c.dim, all_rows = s.n * p.G, r0 = tile * kManyRows, r1 = min(all_rows, r0 + kManyRows);
+  const Keys k = keys_of(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT);
+  if (split >= k.act) return;
+  const int k0 = k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
+  const int tiles = (k1 - k0 + KT - 1) / KT;
+  const int32_t* table = g.table + (int64_t)b * g.ldt;
+
+  // Q^T operand: lane (row = lane % 32, h = lane / 32), step t: dims 16 t + 8 h ..
+  const int h = lane >> 5, wr0 = r0 + 32 * wave, wr1 = min(r1, wr0 + 32);
+  const bool live = wr0 < r1;  // a wave of no rows helps to fetch
+  const int row = min(wr0 + (lane & 31), r1 - 1), tok = divide(row, p.group);
+  f16x8 q[STEPS];
+  {
+    const uint16_t* src = g.q + (int64_t)(s.first + tok) * g.ldq + (int64_t)(kvh * p.G + row - tok * p.G) * D;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int d = 16 * t + 8 * h;
+      f16x8 z = {};
+      q[t] = d < D ? *reinterpret_cast<const f16x8*>(src + d) : z;
+    }
+  }
+  const int at0 = s.len - s.n + 1;  // keys before and at token 0's position
+  const int see1 = at0 + tok, see0 = g.window ? see1 - g.window : 0;
+  const int tok_a = divide(min(wr0, r1 - 1), p.group), tok_b = divide(max(wr0, wr1) - 1, p.group);
+  const int all1 = at0 + tok_a, all0 = g.window ? at0 + tok_b - g.window : 0;  // what all rows of the wave see
+  const int any1 = at0 + tok_b, any0 = g.window ? at0 + tok_a - g.window : 0;  // and what any does
+  const float c = FP8 && g.c.k_scale ? p.c * g.c.k_scale[kvh] : p.c;
+  float m = -INFINITY, l = 0.f;
+  f32x16 acc[DB];
+#pragma unroll
+  for (int i = 0; i < DB; ++i)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
+
+  auto compute = [&](int t, const unsigned char* kt) {
+    const unsigned char* vt = kt + TILE;
+    const int j0 = k0 + t * KT;
+    if (!live || j0 >= any1 || j0 + KT <= any0) return;
+    f32x16 sc[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) sc[kb][e] = 0.f;
+      const int r = 32 * kb + (lane & 31);
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st) {
+        const f16x8 a = *reinterpret_cast<const f16x8*>(kt + r * DP * 2 + (((2 * st + h) ^ k_swz<DP>(r)) * 16));
+        sc[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[st], sc[kb], 0, 0, 0);
+      }
+    }
+    // sc[kb][e]: key j0 + 32 kb + 8 (e / 4) + 4 h + e % 4 of this lane's row
+    auto seen = [&](int kb, int e) {
+      const int j = j0 + 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3);
+      return j >= see0 && j < see1;
+    };
+    const bool edge = j0 + KT > all1 || j0 < all0;
+    if (edge) {
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sc[kb][e] = seen(kb, e) ? sc[kb][e] : -INFINITY;
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[kb][e]);
+    top *= c;
+    if (__any(top > m + kSlack)) {
+      const float mn = fmaxf(m, across<false>(top, fmax2));
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] *= f;
+      m = mn;
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+    f16x8 w[2 * KB];  // 16 keys each
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x = __builtin_amdgcn_exp2f(sc[kb][e] * c - ms);
+        l += x;
+        w[2 * kb + (e >> 3)][e & 7] = (f16)x;
+      }
+    // V^T operand: dims 32 i + lane % 32, keys 16 ks + 4 h .. + 3 and 16 ks + 8 + 4 h .. + 3
+    auto v_frag = [&](int i, int ks) {
+      s16x4 v[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = 16 * ks + 8 * u + 4 * h + ((lane & 15) >> 2);
+        const int ch = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
+            vt + r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8));
+      }
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    bool odd = false;
+    if (edge) {
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int ks = 0; ks < 2 * KB; ++ks) odd |= any_special(v_frag(i, ks));
+    }
+    if (__any(odd)) {
+#pragma unroll
+      for (int i = 0; i < DB; ++i) {
+#pragma unroll
+        for (int ks = 0; ks < 2 * KB; ++ks)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(of_kind(v_frag(i, ks), 0), w[ks], acc[i], 0, 0, 0);
+        for (int cls = 1; cls < 4; ++cls) {
+          f32x16 cnt;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) cnt[e] = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < 2 * KB; ++ks) {
+            f16x8 one;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) one[e] = seen(ks >> 1, 8 * (ks & 1) + e) ? (f16)1.f : (f16)0.f;
+            cnt = __builtin_amdgcn_mfma_f32_32x32x16_f16(of_kind(v_frag(i, ks), cls), one, cnt, 0, 0, 0);
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[i][e] += cnt[e] > 0.f ? special(cls) : 0.f;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int ks = 0; ks < 2 * KB; ++ks)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_frag(i, ks), w[ks], acc[i], 0, 0, 0);
+    }
+  };
+  // every wave's part of a stage is there, and the other stage has been read
+  auto meet = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+
+  if constexpr (!FP8) {
+    constexpr int CH = DP / 8, RPI = 64 / CH, NI = RW / RPI;
+    const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+    const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);
+    const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
+    const uint16_t* kbase = reinterpret_cast<const uint16_t*>(g.c.k) + kvh * g.c.stride_head;
+    const uint16_t* vbase = reinterpret_cast<const uint16_t*>(g.c.v) + kvh * g.c.stride_head;
+    auto fetch_ids = [&](int t) {
+      const int j = min(k0 + t * KT + RW * wave + lane % RW, k1 - 1);
+      dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
+    };
+    auto fetch = [&](int t) {
+      const uint32_t st = lds_at + (t & 1) * 2 * TILE + wave * (TILE / NW);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int rw = i * RPI + lane / CH, r = RW * wave + rw, ch = lane % CH;
+        const int j = k0 + t * KT + r, page = divide(j, p.page), id = ids[(t & 3) * 64 + rw];
+        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token;
+        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+        const int ck = (ch ^ k_swz<DP>(r)) * 8, cv = (ch ^ v_swz<DP>(r)) * 8;
+        const void* ks = in && !good             ? (const void*)kNans
+                         : in && ck < D          ? (const void*)(kbase + at + ck)
+                                                 : (const void*)kZeros;
+        const void* vs = in && good && cv < D ? (const void*)(vbase + at + cv) : (const void*)kZeros;
+        dma16(ks, st + i * 1024);
+        dma16(vs, st + TILE + i * 1024);
+      }
+    };
+    if (tiles > 0) {
+      fetch_ids(0);
+      wait_vm<0>();
+      fetch(0);
+      if (tiles > 1) fetch_ids(1);
+    }
+    for (int t = 0; t < tiles; ++t) {
+      meet();
+      if (t + 1 < tiles) {
+        fetch(t + 1);
+        if (t + 2 < tiles) fetch_ids(t + 2);
+      }
+      compute(t, lds + (t & 1) * 2 * TILE);
+    }
+  } else {
+    constexpr int CH = DP / 16, RPI = 64 / CH, NI = (RW + RPI - 1) / RPI;
+    const uint8_t* kbase = reinterpret_cast<const uint8_t*>(g.c.k) + kvh * g.c.stride_head;
+    const uint8_t* vbase = reinterpret_cast<const uint8_t*>(g.c.v) + kvh * g.c.stride_head;
+    static_assert(RW % RPI == 0, "whole rows of a load");
+    u32x4 kr[NI], vr[NI];
+    auto page_id = [&](int t) { return table[divide(min(k0 + t * KT + RW * wave + lane % RW, k1 - 1), p.page)]; };
+    auto load = [&](int t, int ids) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int rw = i * RPI + lane / CH, d = lane % CH * 16;
+        const int j = k0 + t * KT + RW * wave + rw, page = divide(j, p.page), id = __shfl(ids, rw);
+        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token + d;
+        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+        const uint32_t fill = in && !good ? 0x7f7f7f7fu : 0u;
+        kr[i] = {fill, fill, fill, fill};
+        vr[i] = {0, 0, 0, 0};
+        if (in && good && d < D) {
+          kr[i] = *reinterpret_cast<const u32x4*>(kbase + at);
+          vr[i] = *reinterpret_cast<const u32x4*>(vbase + at);
+        }
+      }
+    };
+    auto store = [&](unsigned char* st) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = RW * wave + i * RPI + lane / CH, ch = lane % CH * 2;
+        f16x8 x[2];
+        widen(kr[i], x);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<f16x8*>(st + r * DP * 2 + ((ch + e) ^ k_swz<DP>(r)) * 16) = x[e];
+        widen(vr[i], x);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<f16x8*>(st + TILE + r * DP * 2 + ((ch + e) ^ v_swz<DP>(r)) * 16) = x[e];
+      }
+    };
+    int ids = 0;
+    if (tiles > 0) {
+      load(0, page_id(0));
+      if (tiles > 1) ids = page_id(1);
+      store(lds);
+    }
+    for (int t = 0; t < tiles; ++t) {
+      __syncthreads();
+      if (t + 1 < tiles) {
+        load(t + 1, ids);
+        if (t + 2 < tiles) ids = page_id(t + 2);
+      }
+      compute(t, lds + (t & 1) * 2 * TILE);
+      if (t + 1 < tiles) store(lds + ((t + 1) & 1) * 2 * TILE);
+    }
+  }
+
+  // acc[i][e]: dim 32 i + 8 (e / 4) + 4 h + e % 4 of this lane's row
+  if (wr0 + (lane & 31) >= r1) return;
+  l = across<false>(l, add2);
+  const int64_t part = (((int64_t)slot * g.c.heads + kvh) * p.splits + split) * kManyRows + (row - r0);
+  float* sums = p.part + part * D;
+  float* ml = p.part + (int64_t)p.tiles * g.c.heads * p.splits * kManyRows * D + part * 2;
+  const float f = l == 0.f ? 0.f : (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+  uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D;
+#pragma unroll
+  for (int i = 0; i < DB; ++i)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int d = 32 * i + 8 * a + 4 * h;
+      if (d >= D) break;
+      if (k.act > 1) {
+        f32x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = acc[i][4 * a + e];
+        *reinterpret_cast<f32x4*>(sums + d) = o;
+      } else {
+        f16x4 o;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = (f16)(acc[i][4 * a + e] * f);
+        *reinterpret_cast<f16x4*>(out + d) = o;
+      }
+    }
+  if (k.act > 1 && h == 0) ml[0] = m, ml[1] = l;
+}
+
+// ------------------------------------------------------------------------------- the parts
+// out of a row whose keys were in several parts: with M = max m,  sum_s 2^(m_s - M) (sums_s, l_s), in the
+// order of the parts.  A wave per row, or (wide) the four waves of a workgroup on one row, a
+// quarter of the parts each.
+template <bool FEW, int EL>
+__global__ __launch_bounds__(256) void attention_join_kernel(Plan p, int wide) {
+  __shared__ float sums[4][64 * EL];
+  __shared__ float ls[4];
+  const AttnArgs& g = p.a;
+  constexpr int ROWS = FEW ? kFewRows : kManyRows;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = g.c.dim;
+  const int per_item = wide ? ROWS : ROWS / 4;
+  const int item = blockIdx.x / per_item, r = wide ? blockIdx.x % per_item : blockIdx.x % per_item * 4 + wave;
+  const int kvh = item % g.c.heads;
+  int b = item / g.c.heads, tile = 0;
+  const int64_t items = (int64_t)(FEW ? g.B : p.tiles) * g.c.heads;
+  Keys k;
+  Seq s;
+  int row;
+  if constexpr (FEW) {
+    s = sequence(g, b);
+    const int n = min(s.n, kFewRows / p.G);
+    if (s.n == 0 || (p.skip_short && s.n * p.G > kFewRows) || r >= n * p.G) return;
+    k = keys_of(p, s, 0, n - 1, 1, kFewKeys, kMinSplit);
+    row = r;
+  } else {
+    locate(p, item / g.c.heads, b, tile);
+    if (b < 0) return;
+    s = sequence(g, b);
+    row = tile * kManyRows + r;
+    if (row >= s.n * p.G) return;
+    const int last = min(s.n * p.G, (tile + 1) * kManyRows) - 1;
+    const int kt = p.keys;
+    k = keys_of(p, s, divide(tile * kManyRows, p.group), divide(last, p.group), kt, kt, 2 * kt);
+  }
+  if (k.act <= 1) return;  // written already
+  const float* part = p.part + ((int64_t)item * p.splits * ROWS + r) * D;
+  const float* ml = p.part + items * p.splits * ROWS * D + ((int64_t)item * p.splits * ROWS + r) * 2;
+  float top = -INFINITY;
+  for (int x = lane; x < k.act; x += 64) top = fmaxf(top, ml[(int64_t)x * ROWS * 2]);
+  for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
+  const int step = wide ? 4 : 1, d = lane * EL;
+  float o[EL] = {}, l = 0.f;
+#pragma unroll 4
+  for (int x = wide ? wave : 0; x < k.act; x += step) {
+    const float mx = ml[(int64_t)x * ROWS * 2], f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - top);
+    l += ml[(int64_t)x * ROWS * 2 + 1] * f;
+    if (d < D) {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) o[e] += part[(int64_t)x * ROWS * D + d + e] * f;
+    }
+  }
+  if (wide) {
+#pragma unroll
+    for (int e = 0; e < EL; ++e) sums[wave][d + e] = o[e];
+    if (lane == 0) ls[wave] = l;
+    __syncthreads();
+    if (wave != 0) return;
+    l = ls[0] + ls[1] + ls[2] + ls[3];
+#pragma unroll
+    for (int e = 0; e < EL; ++e) o[e] = sums[0][d + e] + sums[1][d + e] + sums[2][d + e] + sums[3][d + e];
+  }
+  if (d >= D) return;
+  const int tok = divide(row, p.group);
+  const float f = l == 0.f ? 0.f : (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+  uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
+#pragma unroll
+  for (int e = 0; e < EL; ++e) out[e] = __builtin_bit_cast(uint16_t, (f16)(o[e] * f));
+}
+
+// ------------------------------------------------------------------------------- the launch
+// Which kernels run: the one for few rows if no sequence has more than 16 rows, by max_q; the
+// other if all have the same number (or there is one): both, each leaving the other's sequences, when
+// they may differ.
+struct Launch {
+  bool few, many;
+  int few_splits, many_splits, tiles;
+  size_t few_bytes, many_bytes;
+};
+
+constexpr int kCus = 256;
+
+Launch plan(const AttnArgs& a) {
+  Launch x{};
+  const int G = a.Hq / a.c.heads;
+  const int64_t most = (int64_t)a.W * a.c.page_size;
+  x.few = (int64_t)a.max_q * G <= kFewRows;
+  x.many = !x.few;
+  if (x.many && a.B > 1 && G <= kFewRows && (int64_t)a.B * a.max_q != a.T) x.few = true;
+  const size_t row = (size_t)(a.c.dim + 2) * sizeof(float);
+  if (x.few) {
+    const int64_t items = (int64_t)a.B * a.c.heads;
+    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kFewRows) : most;
+    x.few_splits = (int)std::max<int64_t>(1, std::min((keys + kMinSplit - 1) / kMinSplit, (2 * kCus + items - 1) / items));
+    if (x.few_splits > 1) x.few_bytes = items * x.few_splits * kFewRows * row;
+  }
+  if (x.many) {
+    x.tiles = (int)((int64_t)a.T * G / kManyRows + std::min(a.B, a.T));
+    const int64_t items = (int64_t)x.tiles * a.c.heads;
+    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kManyRows) : most;
+    x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (2 * kCus + items - 1) / items));
+    if (x.many_splits > 1) x.many_bytes = items * x.many_splits * kManyRows * row;
+  }
+  return x;
+}
+
+template <int DP, bool FP8>
+void launch_few(const Plan& p, int items, hipStream_t st) {
+  static std::once_flag flags[kMaxDevices];
+  once_per_device(flags, [] {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(attention_few_kernel<DP, FP8>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, few_lds<DP, FP8>());
+  });
+  attention_few_kernel<DP, FP8><<<items * p.splits, 64 * few_waves<DP>(), few_lds<DP, FP8>(), st>>>(p);
+}
+
+template <int DP, bool FP8>
+void launch_many(const Plan& p, int items, hipStream_t st) {
+  static std::once_flag flags[kMaxDevices];
+  once_per_device(flags, [] {
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(attention_many_kernel<DP, FP8>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, many_lds<DP>());
+  });
+  attention_many_kernel<DP, FP8><<<items * p.splits, 64 * kManyWaves, many_lds<DP>(), st>>>(p);
+}
+
+template <bool FEW>
+void launch_join(const Plan& p, int items, hipStream_t st) {
+  const int wide = p.splits >= 8, D = p.a.c.dim;
+  const int grid = items * (FEW ? kFewRows : kManyRows) / (wide ? 1 : 4);
+  if (D <= 64)
+    attention_join_kernel<FEW, 1><<<grid, 256, 0, st>>>(p, wide);
+  else if (D <= 128)
+    attention_join_kernel<FEW, 2><<<grid, 256, 0, st>>>(p, wide);
+  else
+    attention_join_kernel<FEW, 4><<<grid, 256, 0, st>>>(p, wide);
+}
+
+template <bool FP8>
+void launch_dims(const Launch& x, Plan p, void* ws, hipStream_t st) {
+  const int D = p.a.c.dim;
+  if (x.few) {
+    p.splits = x.few_splits, p.part = reinterpret_cast<float*>(ws);
+    const int items = p.a.B * p.a.c.heads;
+    if (D <= 64) launch_few<64, FP8>(p, items, st);
+    else if (D <= 128) launch_few<128, FP8>(p, items, st);
+    else launch_few<256, FP8>(p, items, st);
+    if (p.splits > 1) launch_join<true>(p, items, st);
+  }
+  if (x.many) {
+    p.splits = x.many_splits, p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + x.few_bytes);
+    const int items = x.tiles * p.a.c.heads;
+    p.tiles = x.tiles;
+    p.keys = D <= 128 ? 64 : 32;
+    if (D <= 64) launch_many<64, FP8>(p, items, st);
+    else if (D <= 128) launch_many<128, FP8>(p, items, st);
+    else launch_many<256, FP8>(p, items, st);
+    if (p.splits > 1) launch_join<false>(p, items, st);
   }
 }
 
 }  // namespace
 
-size_t attention_ws_bytes(const AttnArgs&) { return 0; }
+size_t attention_ws_bytes(const AttnArgs& a) {
+  const Launch x = plan(a);
+  return x.few_bytes + x.many_bytes;
+}
 
-void launch_attention(const AttnArgs& a, void*, hipStream_t st) {
-  attention_row_kernel<<<dim3(a.T, a.Hq), 64, 0, st>>>(a);
+void launch_attention(const AttnArgs& a, void* ws, hipStream_t st) {
+  const Launch x = plan(a);
+  Plan p{};
+  p.a = a, p.G = a.Hq / a.c.heads, p.page = divider(a.c.page_size), p.group = divider(p.G);
+  p.skip_short = x.few && x.many, p.c = a.scale * kLog2e;
+  if (a.c.e4m3)
+    launch_dims<true>(x, p, ws, st);
+  else
+    launch_dims<false>(x, p, ws, st);
 }
 
 }  // namespace w4

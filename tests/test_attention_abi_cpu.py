@@ -93,7 +93,8 @@ def test_attention_refusals():
     for bad in (dict(B=0), dict(B=(1 << 20) + 1), dict(T=0), dict(T=1 << 24), dict(max_q=0), dict(max_q=7), dict(W=0),
                 dict(W=1 << 27, ldt=1 << 27), dict(ldt=3), dict(Hq=0), dict(Hq=3), dict(window=-1), dict(scale=0.0),
                 dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(ldq=504), dict(ldo=504),
-                dict(q_start=None), dict(q_start=None, max_q=1, B=7), dict(Hq=1026, ldq=1026 * 128, ldo=1026 * 128)):
+                dict(q_start=None), dict(q_start=None, max_q=1, B=7), dict(Hq=1026, ldq=1026 * 128, ldo=1026 * 128),
+                dict(T=(1 << 20) + 1, Hq=1024, ldq=1 << 17, ldo=1 << 17)):
         assert attend(**bad) == SHAPE, bad
     for bad in (dict(q=P + 8), dict(out=P + 8), dict(ldq=516), dict(ldo=516), dict(table=P + 2), dict(kv_len=P + 1),
                 dict(q_start=P + 2)):
