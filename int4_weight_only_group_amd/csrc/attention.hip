@@ -18,6 +18,7 @@
 // past its sequence's end may be anything).  A page number outside the cache gives NaN keys.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "w4_internal.h"
 #include "w4_kv.h"
@@ -29,6 +30,9 @@ namespace {
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
+typedef __attribute__((address_space(3))) f16x4 lds_f16x4;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 // m moves only when a score exceeds it by more than this (in powers of two): weights stay below
@@ -46,6 +50,10 @@ __device__ __forceinline__ void dma16(const void* p, uint32_t lds) {
 }
 __device__ __forceinline__ void dma4(const void* p, uint32_t lds) {
   asm volatile("s_nop 1\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+// the same from a wave-uniform base and a 32-bit offset per lane
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 1\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(lds) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_vm() {
@@ -155,29 +163,24 @@ __device__ __forceinline__ void widen(const u32x4& v, f16x8 (&h)[2]) {
   }
 }
 
-__device__ __forceinline__ bool any_special(const f16x8& v) {  // an infinity or NaN
-  const u32x4 x = __builtin_bit_cast(u32x4, v);
-  uint32_t bad = 0;
+// A matrix product multiplies a weight of 0 with every v, and 0 * infinity is NaN.  So in tiles that
+// some rows do not see whole (edge tiles) the product takes v with 0 for what is not finite, and
+// if there was any, it is added afterwards, to the rows that see it (its weight is positive).
+// finite: v so cleaned; odd: its cleared elements, as 16-bit masks, are or-ed into it.
+__device__ __forceinline__ f16x8 finite(const f16x8& v, uint32_t& odd) {
+  u32x4 x = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) bad |= ((x[i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-  return bad != 0;
-}
-
-// A matrix product multiplies a weight of 0 with every v, and 0 * infinity is NaN: where some rows
-// of a tile do not see a key and its v is not finite, the finite values are multiplied as usual
-// and the others counted by kind with the weights' place taken by `seen` (1 where the row sees the
-// key); a row with a count gets the infinity or NaN.  cls: 0 finite, 1 +inf, 2 -inf, 3 NaN.
-__device__ __forceinline__ f16x8 of_kind(const f16x8& v, int cls) {
-  f16x8 o;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint16_t x = __builtin_bit_cast(uint16_t, (f16)v[e]);
-    const int kind = (x & 0x7c00) != 0x7c00 ? 0 : (x & 0x3ff) ? 3 : (x & 0x8000) ? 2 : 1;
-    o[e] = kind != cls ? (f16)0.f : cls == 0 ? (f16)v[e] : (f16)1.f;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t top = ((x[i] & 0x7c007c00u) + 0x04000400u) & 0x80008000u;  // exponent all ones
+    const uint32_t mask = (top - (top >> 15)) | top;
+    odd |= mask;
+    x[i] &= ~mask;
   }
-  return o;
+  return __builtin_bit_cast(f16x8, x);
 }
-__device__ __forceinline__ float special(int cls) { return cls == 1 ? INFINITY : cls == 2 ? -INFINITY : NAN; }
+__device__ __forceinline__ float special_of(f16 v) {  // v if it is not finite, else 0
+  return (__builtin_bit_cast(uint16_t, v) & 0x7c00) == 0x7c00 ? (float)v : 0.f;
+}
 
 // ------------------------------------------------------------------------- few rows (decode)
 // At most 16 rows of a (sequence, kv head): decode, short drafts.  Bound: HBM, by the cache's bytes.
@@ -301,24 +304,23 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
       }
       return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    bool odd = false;
     if (edge && n > 1) {
+      uint32_t odd = 0;
 #pragma unroll
-      for (int i = 0; i < DB; ++i) odd |= any_special(v_frag(i));
-    }
-    if (__any(odd)) {
-      f16x8 one;
+      for (int i = 0; i < DB; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(finite(v_frag(i), odd), w, acc[i], 0, 0, 0);
+      if (__any(odd != 0)) {
+#pragma unroll 1
+        for (int r = 0; r < KT; ++r) {
+          const int j = j0 + r;
+          const bool see = j >= see0 && j < see1;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) one[e] = seen(e >> 2, e & 3) ? (f16)1.f : (f16)0.f;
+          for (int i = 0; i < DB; ++i) {
+            const int d = 16 * i + 4 * grp;
+            const f16x4 v = *reinterpret_cast<const f16x4*>(vt + r * DP * 2 + ((d / 8) ^ v_swz<DP>(r)) * 16 + (d & 4) * 2);
 #pragma unroll
-      for (int i = 0; i < DB; ++i) {
-        const f16x8 v = v_frag(i);
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_kind(v, 0), w, acc[i], 0, 0, 0);
-        for (int cls = 1; cls < 4; ++cls) {
-          const f32x4 z = {0.f, 0.f, 0.f, 0.f};
-          const f32x4 cnt = __builtin_amdgcn_mfma_f32_16x16x32_f16(of_kind(v, cls), one, z, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] += cnt[e] > 0.f ? special(cls) : 0.f;
+            for (int e = 0; e < 4; ++e) acc[i][e] += see ? special_of(v[e]) : 0.f;
+          }
         }
       }
     } else {
@@ -513,7 +515,7 @@ __device__ __forceinline__ void locate(const Plan& p, int tile, int& b, int& at)
 }
 
 template <int DP, bool FP8>
-__global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan p) {
+__global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_many_kernel(Plan p) {
   constexpr int NW = kManyWaves, KT = many_keys<DP>(), TILE = KT * DP * 2, RW = KT / NW;
   constexpr int STEPS = DP / 16, DB = DP / 32, KB = KT / 32;
   extern __shared__ __align__(16) unsigned char lds[];
@@ -560,21 +562,51 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
 
-  auto compute = [&](int t, const unsigned char* kt) {
-    const unsigned char* vt = kt + TILE;
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+  // LDS offsets of a lane's fragments within a tile; the swizzles fold into the lane's part, up to the
+  // chunk bits that count steps (K) or dims blocks (V) below 256 bytes
+  constexpr int KA = STEPS < 8 ? STEPS : 8, VA = DB < 4 ? DB : 4;
+  uint32_t k_at[KA], v_at[VA];
+#pragma unroll
+  for (int st = 0; st < KA; ++st) {
+    const int r = lane & 31;
+    k_at[st] = (uint32_t)(r * DP * 2 + (((2 * st + h) ^ k_swz<DP>(r)) * 16));
+  }
+#pragma unroll
+  for (int i = 0; i < VA; ++i) {
+    const int r = 4 * h + ((lane & 15) >> 2), ch = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    v_at[i] = (uint32_t)(r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8);
+  }
+
+  auto compute = [&](int t, uint32_t kt) {  // kt: LDS address of the K tile, V's behind it
     const int j0 = k0 + t * KT;
     if (!live || j0 >= any1 || j0 + KT <= any0) return;
+    // Fragments are read four at a time, a group ahead of the products that use them, and the compiler
+    // is kept from moving more of them up (it would fill the register file with them and spill).
+    auto k_frag = [&](int f) {  // step f / KB, key block f % KB
+      const int st = f / KB;
+      return *reinterpret_cast<const lds_f16x8*>(kt + k_at[st % KA] + (uint32_t)(st / KA * 256 + f % KB * 32 * DP * 2));
+    };
     f32x16 sc[KB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
+    for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
       for (int e = 0; e < 16; ++e) sc[kb][e] = 0.f;
-      const int r = 32 * kb + (lane & 31);
+    f16x8 fr[2][4];
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const f16x8 a = *reinterpret_cast<const f16x8*>(kt + r * DP * 2 + (((2 * st + h) ^ k_swz<DP>(r)) * 16));
-        sc[kb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, q[st], sc[kb], 0, 0, 0);
+    for (int f = 0; f < 4; ++f) fr[0][f] = k_frag(f);
+#pragma unroll
+    for (int gr = 0; gr < STEPS * KB / 4; ++gr) {
+      if (gr + 1 < STEPS * KB / 4) {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) fr[(gr + 1) & 1][f] = k_frag(4 * (gr + 1) + f);
       }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int x = 4 * gr + f;
+        sc[x % KB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[gr & 1][f], q[x / KB], sc[x % KB], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
     // sc[kb][e]: key j0 + 32 kb + 8 (e / 4) + 4 h + e % 4 of this lane's row
     auto seen = [&](int kb, int e) {
@@ -616,49 +648,55 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan
       }
     // V^T operand: dims 32 i + lane % 32, keys 16 ks + 4 h .. + 3 and 16 ks + 8 + 4 h .. + 3
     auto v_frag = [&](int i, int ks) {
-      s16x4 v[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = 16 * ks + 8 * u + 4 * h + ((lane & 15) >> 2);
-        const int ch = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-        v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
-            vt + r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8));
-      }
-      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      const uint32_t at = kt + v_at[i % VA] + (uint32_t)(TILE + i / VA * 256 + 16 * ks * DP * 2);
+      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
+      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 8 * DP * 2));
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
-    bool odd = false;
-    if (edge) {
-      for (int i = 0; i < DB; ++i)
+    uint32_t odd = 0;
+    auto weigh = [&](auto clean) {  // O^T += V^T P^T: product x is keys block x % (2 KB), dims block x / (2 KB)
+      constexpr int N = DB * 2 * KB;
 #pragma unroll
-        for (int ks = 0; ks < 2 * KB; ++ks) odd |= any_special(v_frag(i, ks));
-    }
-    if (__any(odd)) {
+      for (int f = 0; f < 4; ++f) fr[0][f] = v_frag(f / (2 * KB), f % (2 * KB));
 #pragma unroll
-      for (int i = 0; i < DB; ++i) {
+      for (int gr = 0; gr < N / 4; ++gr) {
+        if (gr + 1 < N / 4) {
 #pragma unroll
-        for (int ks = 0; ks < 2 * KB; ++ks)
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(of_kind(v_frag(i, ks), 0), w[ks], acc[i], 0, 0, 0);
-        for (int cls = 1; cls < 4; ++cls) {
-          f32x16 cnt;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) cnt[e] = 0.f;
-#pragma unroll
-          for (int ks = 0; ks < 2 * KB; ++ks) {
-            f16x8 one;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) one[e] = seen(ks >> 1, 8 * (ks & 1) + e) ? (f16)1.f : (f16)0.f;
-            cnt = __builtin_amdgcn_mfma_f32_32x32x16_f16(of_kind(v_frag(i, ks), cls), one, cnt, 0, 0, 0);
+          for (int f = 0; f < 4; ++f) {
+            const int x = 4 * (gr + 1) + f;
+            fr[(gr + 1) & 1][f] = v_frag(x / (2 * KB), x % (2 * KB));
           }
-#pragma unroll
-          for (int e = 0; e < 16; ++e) acc[i][e] += cnt[e] > 0.f ? special(cls) : 0.f;
         }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const int x = 4 * gr + f, i = x / (2 * KB);
+          f16x8 v = fr[gr & 1][f];
+          if constexpr (decltype(clean)::value) v = finite(v, odd);
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[x % (2 * KB)], acc[i], 0, 0, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-    } else {
+    };
+    if (!edge) {
+      weigh(std::false_type{});
+      return;
+    }
+    weigh(std::true_type{});
+    if (__any(odd != 0)) {
+#pragma unroll 1
+      for (int r = 0; r < KT; ++r) {
+        const int j = j0 + r;
+        const bool see = j >= see0 && j < see1;
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
+        for (int i = 0; i < DB; ++i)
 #pragma unroll
-        for (int ks = 0; ks < 2 * KB; ++ks)
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_frag(i, ks), w[ks], acc[i], 0, 0, 0);
+          for (int a = 0; a < 4; ++a) {
+            const f16x4 v = *reinterpret_cast<const lds_f16x4*>(
+                  kt + (uint32_t)(TILE + r * DP * 2 + ((4 * i + a) ^ v_swz<DP>(r)) * 16 + 8 * h));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][4 * a + e] += see ? special_of(v[e]) : 0.f;
+          }
+      }
     }
   };
   // every wave's part of a stage is there, and the other stage has been read
@@ -666,7 +704,6 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan
 
   if constexpr (!FP8) {
     constexpr int CH = DP / 8, RPI = 64 / CH, NI = RW / RPI;
-    const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
     const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);
     const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
     const uint16_t* kbase = reinterpret_cast<const uint16_t*>(g.c.k) + kvh * g.c.stride_head;
@@ -675,12 +712,33 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan
       const int j = min(k0 + t * KT + RW * wave + lane % RW, k1 - 1);
       dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
     };
+    // A whole tile of whole pages: this wave's RW keys lie in one page, whose address is scalar; a lane adds
+    // its row and chunk.  (Per-lane addresses of every DMA cost more VALU work than the softmax.)
+    const bool plain = D == DP && g.c.page_size % RW == 0 && g.c.stride_token < (1 << 20);
+    const uint32_t lane_row = (uint32_t)(lane / CH) * (uint32_t)g.c.stride_token;
     auto fetch = [&](int t) {
+      int lane_here = lane;  // opaque, or the offsets below move out of the loop and cost 8 registers
+      asm volatile("" : "+v"(lane_here));
       const uint32_t st = lds_at + (t & 1) * 2 * TILE + wave * (TILE / NW);
+      const int jw = k0 + t * KT + RW * wave;
+      if (plain && k0 + (t + 1) * KT <= k1) {
+        const int id = __builtin_amdgcn_readfirstlane(ids[(t & 3) * 64]);
+        if ((uint32_t)id < (uint32_t)g.c.pages) {
+          const int64_t at = id * g.c.stride_page + (jw - divide(jw, p.page) * g.c.page_size) * g.c.stride_token;
 #pragma unroll
+          for (int i = 0; i < NI; ++i) {
+            const int r = RW * wave + i * RPI + lane_here / CH, ch = lane_here % CH;
+            const int64_t ai = at + i * RPI * g.c.stride_token;
+            dma16(kbase + ai, (lane_row + (ch ^ k_swz<DP>(r)) * 8) * 2, st + i * 1024);
+            dma16(vbase + ai, (lane_row + (ch ^ v_swz<DP>(r)) * 8) * 2, st + TILE + i * 1024);
+          }
+          return;
+        }
+      }
+#pragma unroll 1
       for (int i = 0; i < NI; ++i) {
         const int rw = i * RPI + lane / CH, r = RW * wave + rw, ch = lane % CH;
-        const int j = k0 + t * KT + r, page = divide(j, p.page), id = ids[(t & 3) * 64 + rw];
+        const int j = jw + rw, page = divide(j, p.page), id = ids[(t & 3) * 64 + rw];
         const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token;
         const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
         const int ck = (ch ^ k_swz<DP>(r)) * 8, cv = (ch ^ v_swz<DP>(r)) * 8;
@@ -704,7 +762,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan
         fetch(t + 1);
         if (t + 2 < tiles) fetch_ids(t + 2);
       }
-      compute(t, lds + (t & 1) * 2 * TILE);
+      compute(t, lds_at + (t & 1) * 2 * TILE);
     }
   } else {
     constexpr int CH = DP / 16, RPI = 64 / CH, NI = (RW + RPI - 1) / RPI;
@@ -756,7 +814,7 @@ __global__ __launch_bounds__(64 * kManyWaves, 2) void attention_many_kernel(Plan
         load(t + 1, ids);
         if (t + 2 < tiles) ids = page_id(t + 2);
       }
-      compute(t, lds + (t & 1) * 2 * TILE);
+      compute(t, lds_at + (t & 1) * 2 * TILE);
       if (t + 1 < tiles) store(lds + ((t + 1) & 1) * 2 * TILE);
     }
   }
