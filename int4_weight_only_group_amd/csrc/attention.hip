@@ -32,7 +32,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
 typedef __attribute__((address_space(3))) f16x4 lds_f16x4;
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+typedef __attribute__((address_space(3))) int lds_i32;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 
 constexpr float kLog2e = 1.44269504088896340736f;
 // m moves only when a score exceeds it by more than this (in powers of two): weights stay below
@@ -40,7 +44,8 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kSlack = 8.f;
 
 alignas(16) __device__ const uint32_t kZeros[4] = {0, 0, 0, 0};
-alignas(16) __device__ const uint32_t kNans[4] = {0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u};
+alignas(16) __device__ const uint32_t kNans[4] = {0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u};   // f16
+alignas(16) __device__ const uint32_t kNans8[4] = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};  // e4m3
 
 // LDS DMA: lane l's 16 (4) bytes land at lds + 16 l (4 l).  Inline asm, because the compiler would
 // wait for all of it before every later LDS read; the kernels wait explicitly.  The s_nop covers the
@@ -110,12 +115,20 @@ __device__ __forceinline__ int divide(int n, const Divider& d) { return (int)(((
 struct Plan {
   AttnArgs a;
   Divider page, group;
-  int G, splits;
-  int tiles, keys;  // many rows: row tiles at most, keys of a tile
+  int G;
+  int splits;       // few rows: parts of the keys of all sequences, about; many rows: of a row tile, at most
+  int tiles, keys;  // many rows: row tiles at most, keys of a key tile
+  int part_rows;    // rows kept of a part
   bool skip_short;  // both kernels run: sequences of at most kFewRows rows are the first one's
   float c;          // scale * log2 e
-  float* part;      // [work item][split][rows][dim] sums, then [..][rows][2] (m, l)
+  int4* head;       // of a sequence (few) or row tile (many): first part, parts, ...; see the kernels
+  float* part;      // [part][kv head][part_rows][dim + 4]: unscaled sums, m, l; nullptr: no parts
 };
+
+// A part's row in the workspace.
+__device__ __forceinline__ float* part_row(const Plan& p, int64_t part, int kvh, int row) {
+  return p.part + ((part * p.a.c.heads + kvh) * p.part_rows + row) * (p.a.c.dim + 4);
+}
 
 constexpr int kFewRows = 16;  // rows of the decode kernel's tile
 
@@ -152,15 +165,20 @@ __device__ __forceinline__ Keys keys_of(const Plan& p, const Seq& s, int t0, int
   return k;
 }
 
-// 16 e4m3 codes as f16: exact (every value of the format is an f16)
+// 8 and 16 e4m3 codes as f16: exact (every value of the format is an f16)
+__device__ __forceinline__ f16x8 widen8(uint32_t lo, uint32_t hi) {
+  f16x8 h;
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true);
+  h[0] = (f16)a[0], h[1] = (f16)a[1], h[2] = (f16)b[0], h[3] = (f16)b[1];
+  h[4] = (f16)c[0], h[5] = (f16)c[1], h[6] = (f16)d[0], h[7] = (f16)d[1];
+  return h;
+}
 __device__ __forceinline__ void widen(const u32x4& v, f16x8 (&h)[2]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const auto a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, false);
-    const auto b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v[i], 1.f, true);
-    h[i / 2][4 * (i & 1)] = (f16)a[0], h[i / 2][4 * (i & 1) + 1] = (f16)a[1];
-    h[i / 2][4 * (i & 1) + 2] = (f16)b[0], h[i / 2][4 * (i & 1) + 3] = (f16)b[1];
-  }
+  h[0] = widen8(v[0], v[1]);
+  h[1] = widen8(v[2], v[3]);
 }
 
 // A matrix product multiplies a weight of 0 with every v, and 0 * infinity is NaN.  So in tiles that
@@ -184,45 +202,190 @@ __device__ __forceinline__ float special_of(f16 v) {  // v if it is not finite, 
 
 // ------------------------------------------------------------------------- few rows (decode)
 // At most 16 rows of a (sequence, kv head): decode, short drafts.  Bound: HBM, by the cache's bytes.
-// One workgroup per (sequence, kv head, part of the keys); its waves take 32-key tiles in turn,
-// each with LDS of its own and no barrier until the waves' sums are joined.  f16: a ring of two tiles,
-// tile t + 1 in flight while t is computed; page numbers run one tile further ahead, through LDS too
-// (in registers, the compiler's wait for them would be a wait for all tiles in flight).  e4m3: tile t + 1
-// is in flight in registers, and is widened to f16 on its way into LDS, exactly.
+// A workgroup takes a part of one sequence's keys for one kv head; its waves take 32-key tiles in
+// turn, each with a ring of two tiles in LDS of its own and no barrier until the waves' sums are
+// joined.  Tile t + 1 is in flight while t is computed; the page numbers run one tile further ahead,
+// through LDS too (in registers, the compiler's wait for them would be a wait for all tiles in
+// flight).  e4m3 tiles stay e4m3 in LDS and are widened to f16, exactly, as fragments are read.
 constexpr int kFewKeys = 32;
-constexpr int kMinSplit = 128;  // keys of a part at least: a tile of each wave
-template <int DP>
-constexpr int few_waves() { return DP == 256 ? 2 : 4; }
+constexpr int kMinPart = 128;  // keys of a part at least
 template <int DP, bool FP8>
-constexpr int few_ring() { return (FP8 ? 1 : 2) * 2 * kFewKeys * DP * 2; }  // bytes per wave
+constexpr int few_ring() { return 2 * 2 * kFewKeys * DP * (FP8 ? 1 : 2); }  // bytes per wave
+// waves of a workgroup: two workgroups of them, at least, share a CU (160 KB of LDS), so that one starts or ends
+// while the other streams
 template <int DP, bool FP8>
-constexpr int few_lds() { return few_waves<DP>() * (few_ring<DP, FP8>() + 1024); }
+constexpr int few_waves() { return few_ring<DP, FP8>() <= 16384 ? 4 : few_ring<DP, FP8>() <= 32768 ? 2 : 1; }
+template <int DP, bool FP8>
+constexpr int few_lds() { return few_waves<DP, FP8>() * (few_ring<DP, FP8>() + 1024); }
+
+// Tile rows of ROWB bytes, as above (k_swz, v_swz are for f16: ROWB = 2 DP); the transposing 8-byte
+// reads of e4m3 take the 16-byte chunk of 16 rows, {0-3, 16-19} + 4 group for two groups at a time.
+template <int ROWB>
+__device__ __forceinline__ int k_swz_few(int r) {
+  return ROWB == 64 ? (r >> 2) & 3 : ROWB == 128 ? (r >> 1) & 7 : r & 15;
+}
+template <int ROWB, bool FP8>
+__device__ __forceinline__ int v_swz_few(int r) {
+  if constexpr (!FP8) return v_swz<ROWB / 2>(r);
+  return ROWB == 64    ? ((r >> 2) & 1) | ((r >> 4) & 1) << 1
+         : ROWB == 128 ? ((r >> 1) & 3) | ((r >> 4) & 1) << 2
+                       : (r & 7) | ((r >> 4) & 1) << 3;
+}
+
+// The keys [lo, hi) that a sequence's rows see; n < 0: not this kernel's sequence.
+struct FewKeys {
+  int n, lo, hi;
+};
+__device__ __forceinline__ FewKeys few_keys(const Plan& p, const Seq& s) {
+  FewKeys k;
+  if (s.n == 0 || (p.skip_short && s.n * p.G > kFewRows)) return {-1, 0, 0};
+  k.n = min(s.n, kFewRows / p.G);
+  k.hi = max(0, s.len - s.n + k.n);
+  k.lo = p.a.window ? min(max(0, s.len - s.n + 1 - p.a.window), k.hi) : 0;
+  return k;
+}
+// Parts of a sequence when parts should have about `per` keys.
+__device__ __forceinline__ int few_parts(const FewKeys& k, int per) {
+  return k.n < 0 ? 0 : max(1, (k.hi - k.lo + per - 1) / per);
+}
+
+// Sum over the workgroup, and over the threads before this one.
+template <int NW>
+__device__ __forceinline__ int64_t block_scan(int64_t mine, int64_t& before, int64_t* lds) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t incl = mine;
+#define W4_STEP(CTRL, ROWS)                                                                                    \
+  incl += (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_update_dpp(0, (int)(incl >> 32), CTRL, ROWS, 0xF, false) << 32 | \
+                    (uint32_t)__builtin_amdgcn_update_dpp(0, (int)incl, CTRL, ROWS, 0xF, false))
+  W4_STEP(0x111, 0xF);  // row_shr 1, 2, 4, 8: sums of the rows of 16
+  W4_STEP(0x112, 0xF);
+  W4_STEP(0x114, 0xF);
+  W4_STEP(0x118, 0xF);
+  W4_STEP(0x142, 0xA);  // row_bcast15 into rows 1 and 3, row_bcast31 into rows 2 and 3
+  W4_STEP(0x143, 0xC);
+#undef W4_STEP
+  before = incl - mine;
+  if constexpr (NW == 1) return (int64_t)__shfl((long long)incl, 63);
+  if (lane == 63) lds[wave] = incl;
+  __syncthreads();
+  int64_t all = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < wave) before += lds[w];
+    all += lds[w];
+  }
+  return all;
+}
+
+// Which sequence and which of its parts the part-th workgroup takes: the keys of all sequences are dealt
+// out in parts of about the same length, since lengths differ and the longest sequence alone would
+// set the time.  Every workgroup finds its own by a scan over the sequences.  b < 0: past the last.
+struct Dealt {
+  int b, index, count;
+  Seq s;
+};
+template <int NW>
+__device__ __forceinline__ Dealt deal(const Plan& p, int part) {
+  __shared__ int64_t sums[2][NW];
+  __shared__ Dealt found;
+  const int B = p.a.B, each = (B + 64 * NW - 1) / (64 * NW);
+  const int b0 = min(B, (int)threadIdx.x * each), b1 = min(B, b0 + each);
+  if (threadIdx.x == 0) found.b = -1;
+  int64_t mine = 0, before = 0;
+  Seq one{0, 0, 0};  // this thread's sequence when it has at most one
+  for (int b = b0; b < b1; ++b) {
+    one = sequence(p.a, b);
+    const FewKeys k = few_keys(p, one);
+    mine += k.hi - k.lo;
+  }
+  const int64_t all = block_scan<NW>(mine, before, sums[0]);
+  const int per = (int)min((int64_t)1 << 30, max((int64_t)kMinPart, (all + p.splits - 1) / p.splits + kFewKeys - 1)) &
+                  ~(kFewKeys - 1);
+  auto parts = [&](int b) { return few_parts(few_keys(p, each == 1 ? one : sequence(p.a, b)), per); };
+  mine = 0;
+  for (int b = b0; b < b1; ++b) mine += parts(b);
+  (void)block_scan<NW>(mine, before, sums[1]);
+  if (part >= before && part < before + mine) {
+    int64_t at = before;
+    for (int b = b0; b < b1; ++b) {
+      const int n = parts(b);
+      if (part < at + n) {
+        found = {b, (int)(part - at), n, each == 1 ? one : sequence(p.a, b)};
+        break;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  return found;
+}
 
 template <int DP, bool FP8>
-__global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Plan p) {
-  constexpr int NW = few_waves<DP>(), KT = kFewKeys, TILE = KT * DP * 2, RING = few_ring<DP, FP8>();
+__global__ __launch_bounds__((64 * few_waves<DP, FP8>())) void attention_few_kernel(Plan p) {
+  constexpr int NW = few_waves<DP, FP8>(), KT = kFewKeys, ES = FP8 ? 1 : 2, ROWB = DP * ES;
+  constexpr int TILE = KT * ROWB, RING = few_ring<DP, FP8>();
   constexpr int STEPS = DP / 32, DB = DP / 16;
   extern __shared__ __align__(16) unsigned char lds[];
   __shared__ float join[NW][16][2];
   const AttnArgs& g = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x % p.splits, item = blockIdx.x / p.splits;
-  const int kvh = item % g.c.heads, b = item / g.c.heads;
-  const Seq s = sequence(g, b);
-  if (s.n == 0 || (p.skip_short && s.n * p.G > kFewRows)) return;  // those go to the other kernel
-  const int n = min(s.n, kFewRows / p.G), rows = n * p.G;
-  const Keys k = keys_of(p, s, 0, n - 1, 1, KT, kMinSplit);
-  if (split >= k.act) return;
-  const int k0 = k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
+  const int kvh = blockIdx.x % g.c.heads, part = blockIdx.x / g.c.heads;
+  Dealt mine_is;
+  if (p.part) {
+    mine_is = deal<NW>(p, part);
+    if (mine_is.b < 0) return;
+  } else {  // no parts: a workgroup per sequence
+    mine_is = {part, 0, 1, sequence(g, part)};
+  }
+  auto scalar = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int b = scalar(mine_is.b), index = scalar(mine_is.index), count = scalar(mine_is.count);
+  const Seq s = {scalar(mine_is.s.first), scalar(mine_is.s.n), scalar(mine_is.s.len)};
+  const FewKeys k = few_keys(p, s);
+  if (k.n < 0) return;
+  const int n = k.n, rows = n * p.G;
+  const int per = ((k.hi - k.lo + count - 1) / count + KT - 1) & ~(KT - 1);
+  const int k0 = min(k.hi, k.lo + index * per), k1 = min(k.hi, k0 + per);
   const int tiles = (k1 - k0 + KT - 1) / KT;
   const int mine = tiles > wave ? (tiles - wave + NW - 1) / NW : 0;
   const int D = g.c.dim;
+  if (p.part && kvh == 0 && index == 0 && threadIdx.x == 0) p.head[b] = {part, count, 0, 0};
 
-  unsigned char* ring = lds + wave * RING;
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+  const uint32_t ring = lds_at + wave * RING;
   const int32_t* table = g.table + (int64_t)b * g.ldt;
   auto first_key = [&](int t) { return k0 + (t * NW + wave) * KT; };
 
-  // Q^T operand: lane (row = lane % 16, grp = lane / 16), step t: dims 32 t + 8 grp ..
+  constexpr int CH = ROWB / 16, RPI = 64 / CH, NI = KT / RPI;  // chunks of a row; rows and count of a DMA instruction
+  const int* ids = reinterpret_cast<const int*>(lds + NW * RING + wave * 1024);  // 4 tiles' page numbers
+  const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
+  auto fetch_ids = [&](int t) {
+    const int j = min(first_key(t) + (lane & 31), k1 - 1);
+    dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
+  };
+  const char* kbase = reinterpret_cast<const char*>(g.c.k) + kvh * g.c.stride_head * ES;
+  const char* vbase = reinterpret_cast<const char*>(g.c.v) + kvh * g.c.stride_head * ES;
+  auto fetch = [&](int t) {
+    const uint32_t st = ring + (t & 1) * 2 * TILE;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + lane / CH, ch = lane % CH;
+      const int j = first_key(t) + r, page = divide(j, p.page), id = ids[(t & 3) * 64 + r];
+      const int64_t at = (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES;
+      const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+      const int ck = (ch ^ k_swz_few<ROWB>(r)) * 16, cv = (ch ^ v_swz_few<ROWB, FP8>(r)) * 16;
+      const void* ks = in && !good         ? (const void*)(FP8 ? kNans8 : kNans)
+                       : in && ck < D * ES ? (const void*)(kbase + at + ck)
+                                           : (const void*)kZeros;
+      const void* vs = in && good && cv < D * ES ? (const void*)(vbase + at + cv) : (const void*)kZeros;
+      dma16(ks, st + i * 1024);
+      dma16(vs, st + TILE + i * 1024);
+    }
+  };
+  if (mine > 0) fetch_ids(0);
+  if (mine > 1) fetch_ids(1);
+
+  // Q^T operand: lane (row = lane % 16, grp = lane / 16), step t.  f16: dims 32 t + 8 grp ..; e4m3: a
+  // 16-byte chunk of K feeds two steps, so dims 16 (4 (t / 2) + grp) + 8 (t % 2) ..
   const int row = lane & 15, grp = lane >> 4;
   const int tok = divide(min(row, rows - 1), p.group);
   f16x8 q[STEPS];
@@ -231,7 +394,7 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
                           (int64_t)(kvh * p.G + min(row, rows - 1) - tok * p.G) * D;
 #pragma unroll
     for (int t = 0; t < STEPS; ++t) {
-      const int d = 32 * t + 8 * grp;
+      const int d = FP8 ? 16 * (4 * (t / 2) + grp) + 8 * (t & 1) : 32 * t + 8 * grp;
       f16x8 z = {};
       q[t] = row < rows && d < D ? *reinterpret_cast<const f16x8*>(src + d) : z;
     }
@@ -245,8 +408,8 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
 #pragma unroll
   for (int i = 0; i < DB; ++i) acc[i] = {0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int t, const unsigned char* kt) {
-    const unsigned char* vt = kt + TILE;
+  auto compute = [&](int t, uint32_t kt) {  // kt: LDS address of the K tile, V's behind it
+    const uint32_t vt = kt + TILE;
     const int j0 = first_key(t);
     f32x4 sc[2];
 #pragma unroll
@@ -254,22 +417,29 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
       sc[kb] = {0.f, 0.f, 0.f, 0.f};
       const int r = 16 * kb + row;
 #pragma unroll
-      for (int st = 0; st < STEPS; ++st) {
-        const f16x8 a = *reinterpret_cast<const f16x8*>(kt + r * DP * 2 + (((4 * st + grp) ^ k_swz<DP>(r)) * 16));
-        sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, q[st], sc[kb], 0, 0, 0);
+      for (int st = 0; st < STEPS; st += ES == 1 ? 2 : 1) {
+        const uint32_t at = kt + r * ROWB + ((((FP8 ? 2 * st : 4 * st) + grp) ^ k_swz_few<ROWB>(r)) * 16);
+        if constexpr (FP8) {
+          f16x8 a[2];
+          const u32x4 x = *reinterpret_cast<const lds_u32x4*>(at);
+          widen(x, a);
+          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], q[st], sc[kb], 0, 0, 0);
+          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], q[st + 1], sc[kb], 0, 0, 0);
+        } else {
+          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const lds_f16x8*>(at), q[st], sc[kb], 0, 0, 0);
+        }
       }
     }
     // sc[kb][e]: key j0 + 16 kb + 4 grp + e of this lane's row
-    auto seen = [&](int kb, int e) {
-      const int j = j0 + 16 * kb + 4 * grp + e;
-      return j >= see0 && j < see1;
-    };
     const bool edge = j0 + KT > all1 || j0 < all0;
     if (edge) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[kb][e] = seen(kb, e) ? sc[kb][e] : -INFINITY;
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + 16 * kb + 4 * grp + e;
+          sc[kb][e] = j >= see0 && j < see1 ? sc[kb][e] : -INFINITY;
+        }
     }
     float top = -INFINITY;
 #pragma unroll
@@ -295,145 +465,78 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
       }
     // V^T operand: dims 16 i + lane % 16, keys 4 grp .. + 3 and 16 + 4 grp .. + 3
     auto v_frag = [&](int i) {
-      s16x4 v[2];
+      if constexpr (FP8) {  // 8 rows x 16 codes: lane L of 16 points at row L / 2, half L % 2
+        const int x = (lane & 15) >> 1, r = (x & 4) * 4 + 4 * grp + (x & 3);
+        const auto v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_i32x2*>(
+            vt + r * ROWB + ((i ^ v_swz_few<ROWB, FP8>(r)) * 16) + (lane & 1) * 8));
+        return widen8(v[0], v[1]);
+      } else {
+        s16x4 v[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = 16 * u + 4 * grp + ((lane & 15) >> 2), ch = 2 * i + ((lane & 3) >> 1);
-        v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(
-            vt + r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8));
-      }
-      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    if (edge && n > 1) {
-      uint32_t odd = 0;
-#pragma unroll
-      for (int i = 0; i < DB; ++i)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(finite(v_frag(i), odd), w, acc[i], 0, 0, 0);
-      if (__any(odd != 0)) {
-#pragma unroll 1
-        for (int r = 0; r < KT; ++r) {
-          const int j = j0 + r;
-          const bool see = j >= see0 && j < see1;
-#pragma unroll
-          for (int i = 0; i < DB; ++i) {
-            const int d = 16 * i + 4 * grp;
-            const f16x4 v = *reinterpret_cast<const f16x4*>(vt + r * DP * 2 + ((d / 8) ^ v_swz<DP>(r)) * 16 + (d & 4) * 2);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] += see ? special_of(v[e]) : 0.f;
-          }
+        for (int u = 0; u < 2; ++u) {
+          const int r = 16 * u + 4 * grp + ((lane & 15) >> 2), ch = 2 * i + ((lane & 3) >> 1);
+          v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(
+              vt + r * ROWB + ((ch ^ v_swz_few<ROWB, FP8>(r)) * 16) + (lane & 1) * 8));
         }
+        return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
       }
-    } else {
+    };
+    if (!edge || n == 1) {  // one token: no row sees less of the tile than another
 #pragma unroll
       for (int i = 0; i < DB; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_frag(i), w, acc[i], 0, 0, 0);
+      return;
+    }
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < DB; ++i)
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(finite(v_frag(i), odd), w, acc[i], 0, 0, 0);
+    if (__any(odd != 0)) {
+#pragma unroll 1
+      for (int r = 0; r < KT; ++r) {
+        const int j = j0 + r;
+        const bool see = j >= see0 && j < see1;
+#pragma unroll
+        for (int i = 0; i < DB; ++i) {
+          const int byte = (16 * i + 4 * grp) * ES;
+          const uint32_t at = vt + r * ROWB + ((byte / 16) ^ v_swz_few<ROWB, FP8>(r)) * 16 + byte % 16;
+          f16x4 v;
+          if constexpr (FP8) {
+            const f16x8 x = widen8(*reinterpret_cast<const lds_i32*>(at), 0);
+            v = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+          } else {
+            v = *reinterpret_cast<const lds_f16x4*>(at);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][e] += see ? special_of(v[e]) : 0.f;
+        }
+      }
     }
   };
 
-  if constexpr (!FP8) {
-    constexpr int CH = DP / 8, RPI = 64 / CH, NI = KT / RPI;  // chunks of a row; rows and count of a DMA instruction
-    const uint32_t ring_at = (uint32_t)(uintptr_t)(lds_void_t*)ring;
-    const int* ids = reinterpret_cast<const int*>(lds + NW * RING + wave * 1024);  // 4 tiles' page numbers
-    const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
-    auto fetch_ids = [&](int t) {
-      const int j = min(first_key(t) + (lane & 31), k1 - 1);
-      dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
-    };
-    const uint16_t* kbase = reinterpret_cast<const uint16_t*>(g.c.k) + kvh * g.c.stride_head;
-    const uint16_t* vbase = reinterpret_cast<const uint16_t*>(g.c.v) + kvh * g.c.stride_head;
-    auto fetch = [&](int t) {
-      const uint32_t st = ring_at + (t & 1) * 2 * TILE;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = i * RPI + lane / CH, ch = lane % CH;
-        const int j = first_key(t) + r, page = divide(j, p.page), id = ids[(t & 3) * 64 + r];
-        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token;
-        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
-        const int ck = (ch ^ k_swz<DP>(r)) * 8, cv = (ch ^ v_swz<DP>(r)) * 8;
-        const void* ks = in && !good             ? (const void*)kNans
-                         : in && ck < D          ? (const void*)(kbase + at + ck)
-                                                 : (const void*)kZeros;
-        const void* vs = in && good && cv < D ? (const void*)(vbase + at + cv) : (const void*)kZeros;
-        dma16(ks, st + i * 1024);
-        dma16(vs, st + TILE + i * 1024);
-      }
-    };
-    // in the order of issue: data(t), ids(t + 2), data(t + 1), ids(t + 3), ...: a wait that leaves the
-    // newest data in flight covers the tile before it and the page numbers of the one after it
-    if (mine > 0) {
-      fetch_ids(0);
-      if (mine > 1) fetch_ids(1);
+  // in the order of issue: data(t), ids(t + 2), data(t + 1), ids(t + 3), ...: a wait that leaves the
+  // newest data in flight covers the tile before it and the page numbers of the one after it
+  if (mine > 0) {
+    wait_vm<0>();
+    fetch(0);
+    if (mine > 2) fetch_ids(2);
+    if (mine > 1) fetch(1);
+  }
+  for (int t = 0; t < mine; ++t) {
+    if (t + 1 < mine)
+      wait_vm<2 * NI>();
+    else
       wait_vm<0>();
-      fetch(0);
-      if (mine > 2) fetch_ids(2);
-      if (mine > 1) fetch(1);
-    }
-    for (int t = 0; t < mine; ++t) {
-      if (t + 1 < mine)
-        wait_vm<2 * NI>();
-      else
-        wait_vm<0>();
-      compute(t, ring + (t & 1) * 2 * TILE);
-      if (t + 2 < mine) {
-        wait_lds();  // the stage has been read
-        if (t + 3 < mine) fetch_ids(t + 3);
-        fetch(t + 2);
-      }
-    }
-  } else {
-    constexpr int CH = DP / 16, RPI = 64 / CH, NI = KT / RPI;  // chunks of 16 codes
-    const uint8_t* kbase = reinterpret_cast<const uint8_t*>(g.c.k) + kvh * g.c.stride_head;
-    const uint8_t* vbase = reinterpret_cast<const uint8_t*>(g.c.v) + kvh * g.c.stride_head;
-    u32x4 kr[NI], vr[NI];
-    auto page_id = [&](int t) { return table[divide(min(first_key(t) + (lane & 31), k1 - 1), p.page)]; };
-    auto load = [&](int t, int ids) {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = i * RPI + lane / CH, d = lane % CH * 16;
-        const int j = first_key(t) + r, page = divide(j, p.page), id = __shfl(ids, r);
-        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token + d;
-        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
-        const uint32_t fill = in && !good ? 0x7f7f7f7fu : 0u;
-        kr[i] = {fill, fill, fill, fill};
-        vr[i] = {0, 0, 0, 0};
-        if (in && good && d < D) {
-          kr[i] = *reinterpret_cast<const u32x4*>(kbase + at);
-          vr[i] = *reinterpret_cast<const u32x4*>(vbase + at);
-        }
-      }
-    };
-    auto store = [&]() {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = i * RPI + lane / CH, ch = lane % CH * 2;
-        f16x8 h[2];
-        widen(kr[i], h);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<f16x8*>(ring + r * DP * 2 + ((ch + e) ^ k_swz<DP>(r)) * 16) = h[e];
-        widen(vr[i], h);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<f16x8*>(ring + TILE + r * DP * 2 + ((ch + e) ^ v_swz<DP>(r)) * 16) = h[e];
-      }
-    };
-    int ids = 0;
-    if (mine > 0) {
-      load(0, page_id(0));
-      if (mine > 1) ids = page_id(1);
-    }
-    for (int t = 0; t < mine; ++t) {
-      store();
-      if (t + 1 < mine) {
-        load(t + 1, ids);
-        if (t + 2 < mine) ids = page_id(t + 2);
-      }
-      compute(t, ring);
+    compute(t, ring + (t & 1) * 2 * TILE);
+    if (t + 2 < mine) {
+      wait_lds();  // the stage has been read
+      if (t + 3 < mine) fetch_ids(t + 3);
+      fetch(t + 2);
     }
   }
 
   // join the waves: each leaves (m, l) and its sums in LDS
   l = across<true>(l, add2);
-  float* sums = reinterpret_cast<float*>(ring);  // [16][DP + 4]
+  float* sums = reinterpret_cast<float*>(lds + wave * RING);  // [16][DP + 4]
   constexpr int LD = DP + 4;
   static_assert(16 * LD * 4 <= RING, "a wave's sums fit in its ring");
   wait_lds();
@@ -441,9 +544,6 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
   for (int i = 0; i < DB; ++i) *reinterpret_cast<f32x4*>(&sums[row * LD + 16 * i + 4 * grp]) = acc[i];
   if (grp == 0) join[wave][row][0] = m, join[wave][row][1] = l;
   __syncthreads();
-  const int64_t part = ((int64_t)item * p.splits + split) * kFewRows;
-  float* sums_out = p.part + part * D;
-  float* ml_out = p.part + (int64_t)g.B * g.c.heads * p.splits * kFewRows * D + part * 2;
   const float vs = FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f;
   for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * NW) {
     const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
@@ -457,9 +557,12 @@ __global__ __launch_bounds__(64 * few_waves<DP>()) void attention_few_kernel(Pla
       lt += join[w][r][1] * f;
       o += *reinterpret_cast<const f32x4*>(lds + w * RING + (r * LD + d) * 4) * f;
     }
-    if (k.act > 1) {
-      *reinterpret_cast<f32x4*>(&sums_out[r * D + d]) = o;
-      if (d == 0) ml_out[2 * r] = mt, ml_out[2 * r + 1] = lt;
+    if (count > 1) {
+      if (r < p.part_rows) {
+        float* to = part_row(p, part, kvh, r);
+        *reinterpret_cast<f32x4*>(to + d) = o;
+        if (d == 0) to[D] = mt, to[D + 1] = lt;
+      }
     } else {
       const int tk = divide(r, p.group);
       const float f = lt == 0.f ? 0.f : vs / lt;
@@ -526,11 +629,15 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   const int split = rest % p.splits, slot = p.tiles - 1 - rest / p.splits;
   int b, tile;
   locate(p, slot, b, tile);
-  if (b < 0) return;
+  if (b < 0) {
+    if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {0, 0, 0, 0};
+    return;
+  }
   const Seq s = sequence(g, b);
   const int D = g.c.dim, all_rows = s.n * p.G, r0 = tile * kManyRows, r1 = min(all_rows, r0 + kManyRows);
   const Keys k = keys_of(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT);
   if (split >= k.act) return;
+  if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {slot * p.splits, k.act, b, tile};
   const int k0 = k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
   const int tiles = (k1 - k0 + KT - 1) / KT;
   const int32_t* table = g.table + (int64_t)b * g.ldt;
@@ -822,9 +929,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   // acc[i][e]: dim 32 i + 8 (e / 4) + 4 h + e % 4 of this lane's row
   if (wr0 + (lane & 31) >= r1) return;
   l = across<false>(l, add2);
-  const int64_t part = (((int64_t)slot * g.c.heads + kvh) * p.splits + split) * kManyRows + (row - r0);
-  float* sums = p.part + part * D;
-  float* ml = p.part + (int64_t)p.tiles * g.c.heads * p.splits * kManyRows * D + part * 2;
+  float* sums = k.act > 1 ? part_row(p, (int64_t)slot * p.splits + split, kvh, row - r0) : nullptr;
   const float f = l == 0.f ? 0.f : (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
   uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D;
 #pragma unroll
@@ -845,77 +950,91 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
         *reinterpret_cast<f16x4*>(out + d) = o;
       }
     }
-  if (k.act > 1 && h == 0) ml[0] = m, ml[1] = l;
+  if (k.act > 1 && h == 0) sums[D] = m, sums[D + 1] = l;
 }
 
 // ------------------------------------------------------------------------------- the parts
-// out of a row whose keys were in several parts: with M = max m,  sum_s 2^(m_s - M) (sums_s, l_s), in the
-// order of the parts.  A wave per row, or (wide) the four waves of a workgroup on one row, a
-// quarter of the parts each.
-template <bool FEW, int EL>
-__global__ __launch_bounds__(256) void attention_join_kernel(Plan p, int wide) {
+// A row whose keys were in several parts: with M = max m, the sum of 2^(m_s - M) (sums_s, l_s).  Parts come
+// in batches, running as in the kernels above, so that a batch's loads are in flight together.  Bound:
+// latency (head, then the parts).  A workgroup of four waves takes one row, a quarter of the parts
+// each (WIDE), or four rows per wave.
+template <bool FEW, bool WIDE, int EL>
+__global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
+  constexpr int RW = WIDE ? 1 : 4, BATCH = WIDE ? 8 : 4;
   __shared__ float sums[4][64 * EL];
-  __shared__ float ls[4];
+  __shared__ float mls[4][2];
   const AttnArgs& g = p.a;
-  constexpr int ROWS = FEW ? kFewRows : kManyRows;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = g.c.dim;
-  const int per_item = wide ? ROWS : ROWS / 4;
-  const int item = blockIdx.x / per_item, r = wide ? blockIdx.x % per_item : blockIdx.x % per_item * 4 + wave;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = g.c.dim, d = lane * EL;
+  const int blocks = WIDE ? p.part_rows : (p.part_rows + 15) / 16;  // of an item
+  const int item = blockIdx.x / blocks, in = blockIdx.x - item * blocks;
   const int kvh = item % g.c.heads;
-  int b = item / g.c.heads, tile = 0;
-  const int64_t items = (int64_t)(FEW ? g.B : p.tiles) * g.c.heads;
-  Keys k;
-  Seq s;
-  int row;
-  if constexpr (FEW) {
-    s = sequence(g, b);
-    const int n = min(s.n, kFewRows / p.G);
-    if (s.n == 0 || (p.skip_short && s.n * p.G > kFewRows) || r >= n * p.G) return;
-    k = keys_of(p, s, 0, n - 1, 1, kFewKeys, kMinSplit);
-    row = r;
-  } else {
-    locate(p, item / g.c.heads, b, tile);
-    if (b < 0) return;
-    s = sequence(g, b);
-    row = tile * kManyRows + r;
-    if (row >= s.n * p.G) return;
-    const int last = min(s.n * p.G, (tile + 1) * kManyRows) - 1;
-    const int kt = p.keys;
-    k = keys_of(p, s, divide(tile * kManyRows, p.group), divide(last, p.group), kt, kt, 2 * kt);
-  }
-  if (k.act <= 1) return;  // written already
-  const float* part = p.part + ((int64_t)item * p.splits * ROWS + r) * D;
-  const float* ml = p.part + items * p.splits * ROWS * D + ((int64_t)item * p.splits * ROWS + r) * 2;
-  float top = -INFINITY;
-  for (int x = lane; x < k.act; x += 64) top = fmaxf(top, ml[(int64_t)x * ROWS * 2]);
-  for (int x = 32; x; x >>= 1) top = fmaxf(top, __shfl_xor(top, x));
-  const int step = wide ? 4 : 1, d = lane * EL;
-  float o[EL] = {}, l = 0.f;
-#pragma unroll 4
-  for (int x = wide ? wave : 0; x < k.act; x += step) {
-    const float mx = ml[(int64_t)x * ROWS * 2], f = mx == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mx - top);
-    l += ml[(int64_t)x * ROWS * 2 + 1] * f;
-    if (d < D) {
+  const int4 head = p.head[item / g.c.heads];
+  const int b = FEW ? item / g.c.heads : head.z, r0 = FEW ? 0 : head.w * kManyRows;
+  const int count = head.y, first = head.x;
+  if (!FEW && count <= 1) return;  // no such tile, or written already
+  const Seq s = sequence(g, b);
+  const int all_rows = s.n * p.G;
+  if (FEW && (s.n == 0 || (p.skip_short && all_rows > kFewRows) || count <= 1)) return;
+  const int rows = min(all_rows - r0, p.part_rows);
+  for (int i = 0; i < RW; ++i) {
+    const int r = WIDE ? in : in * 16 + wave * RW + i;
+    if (r >= rows) return;
+    float o[EL] = {}, l = 0.f, m = -INFINITY;
+    for (int x0 = WIDE ? wave : 0; x0 < count; x0 += BATCH * (WIDE ? 4 : 1)) {
+      float om[BATCH], ol[BATCH], ov[BATCH][EL];
 #pragma unroll
-      for (int e = 0; e < EL; ++e) o[e] += part[(int64_t)x * ROWS * D + d + e] * f;
+      for (int y = 0; y < BATCH; ++y) {
+        const int x = x0 + y * (WIDE ? 4 : 1);
+        const float* from = part_row(p, first + min(x, count - 1), kvh, r);
+        om[y] = x < count ? from[D] : -INFINITY;
+        ol[y] = from[D + 1];
+#pragma unroll
+        for (int e = 0; e < EL; ++e) ov[y][e] = d < D ? from[d + e] : 0.f;
+      }
+      float top = m;
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) top = fmaxf(top, om[y]);
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) o[e] *= f;
+#pragma unroll
+      for (int y = 0; y < BATCH; ++y) {
+        const float fy = om[y] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(om[y] - top);
+        const bool there = x0 + y * (WIDE ? 4 : 1) < count;
+        l += there ? ol[y] * fy : 0.f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[e] += there ? ov[y][e] * fy : 0.f;
+      }
+      m = top;
     }
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int e = 0; e < EL; ++e) sums[wave][d + e] = o[e];
+      if (lane == 0) mls[wave][0] = m, mls[wave][1] = l;
+      __syncthreads();
+      if (wave != 0) return;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, mls[w][0]);
+      l = 0.f;
+#pragma unroll
+      for (int e = 0; e < EL; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = mls[w][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mls[w][0] - top);
+        l += mls[w][1] * f;
+#pragma unroll
+        for (int e = 0; e < EL; ++e) o[e] += sums[w][d + e] * f;
+      }
+    }
+    if (d >= D) continue;
+    const int row = r0 + r, tok = divide(row, p.group);
+    const float f = l == 0.f ? 0.f : (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+    uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
+#pragma unroll
+    for (int e = 0; e < EL; ++e) out[e] = __builtin_bit_cast(uint16_t, (f16)(o[e] * f));
   }
-  if (wide) {
-#pragma unroll
-    for (int e = 0; e < EL; ++e) sums[wave][d + e] = o[e];
-    if (lane == 0) ls[wave] = l;
-    __syncthreads();
-    if (wave != 0) return;
-    l = ls[0] + ls[1] + ls[2] + ls[3];
-#pragma unroll
-    for (int e = 0; e < EL; ++e) o[e] = sums[0][d + e] + sums[1][d + e] + sums[2][d + e] + sums[3][d + e];
-  }
-  if (d >= D) return;
-  const int tok = divide(row, p.group);
-  const float f = l == 0.f ? 0.f : (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
-  uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
-#pragma unroll
-  for (int e = 0; e < EL; ++e) out[e] = __builtin_bit_cast(uint16_t, (f16)(o[e] * f));
 }
 
 // ------------------------------------------------------------------------------- the launch
@@ -924,11 +1043,20 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p, int wide) {
 // they may differ.
 struct Launch {
   bool few, many;
-  int few_splits, many_splits, tiles;
+  int few_splits, few_parts, few_rows;  // few_parts 0: one workgroup per (sequence, kv head), no parts
+  int many_splits, tiles;
   size_t few_bytes, many_bytes;
 };
 
 constexpr int kCus = 256;
+constexpr int kWorkgroups = 1024;  // of the kernel for many rows, about: two rounds of two per CU
+
+// Workgroups of the decode kernel that a CU holds, by its LDS (join and deal's own come to less than 1 KB).
+int few_per_cu(const AttnArgs& a) {
+  const int d = a.c.dim, lds = a.c.e4m3 ? d <= 64 ? few_lds<64, true>() : d <= 128 ? few_lds<128, true>() : few_lds<256, true>()
+                                        : d <= 64 ? few_lds<64, false>() : d <= 128 ? few_lds<128, false>() : few_lds<256, false>();
+  return 163840 / (lds + 1024);
+}
 
 Launch plan(const AttnArgs& a) {
   Launch x{};
@@ -937,19 +1065,27 @@ Launch plan(const AttnArgs& a) {
   x.few = (int64_t)a.max_q * G <= kFewRows;
   x.many = !x.few;
   if (x.many && a.B > 1 && G <= kFewRows && (int64_t)a.B * a.max_q != a.T) x.few = true;
-  const size_t row = (size_t)(a.c.dim + 2) * sizeof(float);
+  const size_t row = (size_t)(a.c.dim + 4) * sizeof(float);
   if (x.few) {
-    const int64_t items = (int64_t)a.B * a.c.heads;
     const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kFewRows) : most;
-    x.few_splits = (int)std::max<int64_t>(1, std::min((keys + kMinSplit - 1) / kMinSplit, (2 * kCus + items - 1) / items));
-    if (x.few_splits > 1) x.few_bytes = items * x.few_splits * kFewRows * row;
+    x.few_rows = (int)std::min<int64_t>(kFewRows, (int64_t)a.max_q * G);
+    if (keys > kMinPart) {
+      // one round of the workgroups that the CUs hold, in parts of equal length (their number exceeds
+      // few_splits by at most one per sequence); with more sequences than that, two parts each, for balance
+      const int slots = kCus * few_per_cu(a) / a.c.heads;
+      x.few_splits = std::max(slots - a.B, a.B);
+      // (keys + per - 1) / per parts of each sequence at most
+      x.few_parts = (int)std::min<int64_t>((int64_t)x.few_splits + a.B, a.B * ((keys + kMinPart - 1) / kMinPart));
+      x.few_bytes = (size_t)a.B * sizeof(int4) + (size_t)x.few_parts * a.c.heads * x.few_rows * row;
+    }
   }
   if (x.many) {
     x.tiles = (int)((int64_t)a.T * G / kManyRows + std::min(a.B, a.T));
     const int64_t items = (int64_t)x.tiles * a.c.heads;
     const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kManyRows) : most;
-    x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (2 * kCus + items - 1) / items));
-    if (x.many_splits > 1) x.many_bytes = items * x.many_splits * kManyRows * row;
+    x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (kWorkgroups + items - 1) / items));
+    if (x.many_splits > 1)
+      x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)items * x.many_splits * kManyRows * row;
   }
   return x;
 }
@@ -961,7 +1097,7 @@ void launch_few(const Plan& p, int items, hipStream_t st) {
     (void)hipFuncSetAttribute(reinterpret_cast<const void*>(attention_few_kernel<DP, FP8>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, few_lds<DP, FP8>());
   });
-  attention_few_kernel<DP, FP8><<<items * p.splits, 64 * few_waves<DP>(), few_lds<DP, FP8>(), st>>>(p);
+  attention_few_kernel<DP, FP8><<<items, 64 * few_waves<DP, FP8>(), few_lds<DP, FP8>(), st>>>(p);
 }
 
 template <int DP, bool FP8>
@@ -974,38 +1110,43 @@ void launch_many(const Plan& p, int items, hipStream_t st) {
   attention_many_kernel<DP, FP8><<<items * p.splits, 64 * kManyWaves, many_lds<DP>(), st>>>(p);
 }
 
-template <bool FEW>
+template <bool FEW, bool WIDE>
 void launch_join(const Plan& p, int items, hipStream_t st) {
-  const int wide = p.splits >= 8, D = p.a.c.dim;
-  const int grid = items * (FEW ? kFewRows : kManyRows) / (wide ? 1 : 4);
+  const int D = p.a.c.dim, grid = items * (WIDE ? p.part_rows : (p.part_rows + 15) / 16);
   if (D <= 64)
-    attention_join_kernel<FEW, 1><<<grid, 256, 0, st>>>(p, wide);
+    attention_join_kernel<FEW, WIDE, 1><<<grid, 256, 0, st>>>(p);
   else if (D <= 128)
-    attention_join_kernel<FEW, 2><<<grid, 256, 0, st>>>(p, wide);
+    attention_join_kernel<FEW, WIDE, 2><<<grid, 256, 0, st>>>(p);
   else
-    attention_join_kernel<FEW, 4><<<grid, 256, 0, st>>>(p, wide);
+    attention_join_kernel<FEW, WIDE, 4><<<grid, 256, 0, st>>>(p);
 }
 
 template <bool FP8>
-void launch_dims(const Launch& x, Plan p, void* ws, hipStream_t st) {
-  const int D = p.a.c.dim;
+void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
+  const int D = p.a.c.dim, heads = p.a.c.heads;
   if (x.few) {
-    p.splits = x.few_splits, p.part = reinterpret_cast<float*>(ws);
-    const int items = p.a.B * p.a.c.heads;
+    p.splits = x.few_splits, p.part_rows = x.few_rows;
+    p.head = reinterpret_cast<int4*>(ws);
+    p.part = x.few_parts ? reinterpret_cast<float*>(ws + (size_t)p.a.B * sizeof(int4)) : nullptr;
+    const int items = (x.few_parts ? x.few_parts : p.a.B) * heads;
     if (D <= 64) launch_few<64, FP8>(p, items, st);
     else if (D <= 128) launch_few<128, FP8>(p, items, st);
     else launch_few<256, FP8>(p, items, st);
-    if (p.splits > 1) launch_join<true>(p, items, st);
+    if (x.few_parts) launch_join<true, true>(p, p.a.B * heads, st);
   }
   if (x.many) {
-    p.splits = x.many_splits, p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + x.few_bytes);
-    const int items = x.tiles * p.a.c.heads;
-    p.tiles = x.tiles;
-    p.keys = D <= 128 ? 64 : 32;
+    ws += x.few_bytes;
+    p.splits = x.many_splits, p.part_rows = kManyRows;
+    p.tiles = x.tiles, p.keys = D <= 128 ? 64 : 32;
+    p.head = reinterpret_cast<int4*>(ws);
+    p.part = x.many_splits > 1 ? reinterpret_cast<float*>(ws + (size_t)x.tiles * sizeof(int4)) : nullptr;
+    const int items = x.tiles * heads;
     if (D <= 64) launch_many<64, FP8>(p, items, st);
     else if (D <= 128) launch_many<128, FP8>(p, items, st);
     else launch_many<256, FP8>(p, items, st);
-    if (p.splits > 1) launch_join<false>(p, items, st);
+    // many parts: a workgroup per row
+    if (p.splits >= 16) launch_join<false, true>(p, items, st);
+    else if (p.splits > 1) launch_join<false, false>(p, items, st);
   }
 }
 
@@ -1022,9 +1163,9 @@ void launch_attention(const AttnArgs& a, void* ws, hipStream_t st) {
   p.a = a, p.G = a.Hq / a.c.heads, p.page = divider(a.c.page_size), p.group = divider(p.G);
   p.skip_short = x.few && x.many, p.c = a.scale * kLog2e;
   if (a.c.e4m3)
-    launch_dims<true>(x, p, ws, st);
+    launch_dims<true>(x, p, reinterpret_cast<char*>(ws), st);
   else
-    launch_dims<false>(x, p, ws, st);
+    launch_dims<false>(x, p, reinterpret_cast<char*>(ws), st);
 }
 
 }  // namespace w4
