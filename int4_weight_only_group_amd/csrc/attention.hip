@@ -203,20 +203,22 @@ __device__ __forceinline__ float special_of(f16 v) {  // v if it is not finite, 
 // ------------------------------------------------------------------------- few rows (decode)
 // At most 16 rows of a (sequence, kv head): decode, short drafts.  Bound: HBM, by the cache's bytes.
 // A workgroup takes a part of one sequence's keys for one kv head; its waves take 32-key tiles in
-// turn, each with a ring of two tiles in LDS of its own and no barrier until the waves' sums are
-// joined.  Tile t + 1 is in flight while t is computed; the page numbers run one tile further ahead,
-// through LDS too (in registers, the compiler's wait for them would be a wait for all tiles in
-// flight).  e4m3 tiles stay e4m3 in LDS and are widened to f16, exactly, as fragments are read.
+// turn, each with LDS of its own for one tile and no barrier until the waves' sums are joined.  K of
+// tile t + 1 is fetched as soon as K of t has been multiplied, V of t + 1 after V of t, so a wave always
+// has half a tile or more in flight; the page numbers run a tile further ahead, through LDS too (in
+// registers, the compiler's wait for them would be a wait for everything in flight).  e4m3 tiles stay
+// e4m3 in LDS and are widened to f16, exactly, as fragments are read.
 constexpr int kFewKeys = 32;
 constexpr int kMinPart = 128;  // keys of a part at least
 template <int DP, bool FP8>
-constexpr int few_ring() { return 2 * 2 * kFewKeys * DP * (FP8 ? 1 : 2); }  // bytes per wave
-// waves of a workgroup: two workgroups of them, at least, share a CU (160 KB of LDS), so that one starts or ends
-// while the other streams
+constexpr int few_tile() { return kFewKeys * DP * (FP8 ? 1 : 2); }  // bytes of K, and of V
 template <int DP, bool FP8>
-constexpr int few_waves() { return few_ring<DP, FP8>() <= 16384 ? 4 : few_ring<DP, FP8>() <= 32768 ? 2 : 1; }
+constexpr int few_waves() { return few_tile<DP, FP8>() > 8192 ? 2 : 4; }
 template <int DP, bool FP8>
-constexpr int few_lds() { return few_waves<DP, FP8>() * (few_ring<DP, FP8>() + 1024); }
+constexpr int few_lds() { return few_waves<DP, FP8>() * (2 * few_tile<DP, FP8>() + 512); }
+// Workgroups of a CU: two at least, so that one starts or ends while the other streams.
+template <int DP, bool FP8>
+constexpr int few_per_cu() { return few_lds<DP, FP8>() > 40960 ? 2 : 4; }
 
 // Tile rows of ROWB bytes, as above (k_swz, v_swz are for f16: ROWB = 2 DP); the transposing 8-byte
 // reads of e4m3 take the 16-byte chunk of 16 rows, {0-3, 16-19} + 4 group for two groups at a time.
@@ -232,7 +234,8 @@ __device__ __forceinline__ int v_swz_few(int r) {
                        : (r & 7) | ((r >> 4) & 1) << 3;
 }
 
-// The keys [lo, hi) that a sequence's rows see; n < 0: not this kernel's sequence.
+// The keys [lo, hi) that a sequence's rows see (lo rounded down to 16, for whole pages); n < 0: not this
+// kernel's sequence.
 struct FewKeys {
   int n, lo, hi;
 };
@@ -241,12 +244,17 @@ __device__ __forceinline__ FewKeys few_keys(const Plan& p, const Seq& s) {
   if (s.n == 0 || (p.skip_short && s.n * p.G > kFewRows)) return {-1, 0, 0};
   k.n = min(s.n, kFewRows / p.G);
   k.hi = max(0, s.len - s.n + k.n);
-  k.lo = p.a.window ? min(max(0, s.len - s.n + 1 - p.a.window), k.hi) : 0;
+  k.lo = p.a.window ? min(max(0, s.len - s.n + 1 - p.a.window) & ~15, k.hi) : 0;
   return k;
 }
 // Parts of a sequence when parts should have about `per` keys.
 __device__ __forceinline__ int few_parts(const FewKeys& k, int per) {
   return k.n < 0 ? 0 : max(1, (k.hi - k.lo + per - 1) / per);
+}
+
+// Keys of a part, about, where all sequences have `all`.
+__device__ __forceinline__ int part_keys(const Plan& p, int64_t all) {
+  return (int)min((int64_t)1 << 30, max((int64_t)kMinPart, (all + p.splits - 1) / p.splits + kFewKeys - 1)) & ~(kFewKeys - 1);
 }
 
 // Sum over the workgroup, and over the threads before this one.
@@ -289,6 +297,12 @@ __device__ __forceinline__ Dealt deal(const Plan& p, int part) {
   __shared__ int64_t sums[2][NW];
   __shared__ Dealt found;
   const int B = p.a.B, each = (B + 64 * NW - 1) / (64 * NW);
+  if (B == 1) {
+    const Seq s = sequence(p.a, 0);
+    const FewKeys k = few_keys(p, s);
+    const int n = few_parts(k, part_keys(p, k.hi - k.lo));
+    return {part < n ? 0 : -1, part, n, s};
+  }
   const int b0 = min(B, (int)threadIdx.x * each), b1 = min(B, b0 + each);
   if (threadIdx.x == 0) found.b = -1;
   int64_t mine = 0, before = 0;
@@ -299,8 +313,7 @@ __device__ __forceinline__ Dealt deal(const Plan& p, int part) {
     mine += k.hi - k.lo;
   }
   const int64_t all = block_scan<NW>(mine, before, sums[0]);
-  const int per = (int)min((int64_t)1 << 30, max((int64_t)kMinPart, (all + p.splits - 1) / p.splits + kFewKeys - 1)) &
-                  ~(kFewKeys - 1);
+  const int per = part_keys(p, all);
   auto parts = [&](int b) { return few_parts(few_keys(p, each == 1 ? one : sequence(p.a, b)), per); };
   mine = 0;
   for (int b = b0; b < b1; ++b) mine += parts(b);
@@ -321,9 +334,9 @@ __device__ __forceinline__ Dealt deal(const Plan& p, int part) {
 }
 
 template <int DP, bool FP8>
-__global__ __launch_bounds__((64 * few_waves<DP, FP8>())) void attention_few_kernel(Plan p) {
+__global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>())) void attention_few_kernel(Plan p) {
   constexpr int NW = few_waves<DP, FP8>(), KT = kFewKeys, ES = FP8 ? 1 : 2, ROWB = DP * ES;
-  constexpr int TILE = KT * ROWB, RING = few_ring<DP, FP8>();
+  constexpr int TILE = few_tile<DP, FP8>();
   constexpr int STEPS = DP / 32, DB = DP / 16;
   extern __shared__ __align__(16) unsigned char lds[];
   __shared__ float join[NW][16][2];
@@ -350,39 +363,67 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>())) void attention_few_ker
   const int D = g.c.dim;
   if (p.part && kvh == 0 && index == 0 && threadIdx.x == 0) p.head[b] = {part, count, 0, 0};
 
-  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
-  const uint32_t ring = lds_at + wave * RING;
+  const uint32_t kt = (uint32_t)(uintptr_t)(lds_void_t*)lds + wave * 2 * TILE, vt = kt + TILE;  // this wave's tiles
   const int32_t* table = g.table + (int64_t)b * g.ldt;
   auto first_key = [&](int t) { return k0 + (t * NW + wave) * KT; };
 
   constexpr int CH = ROWB / 16, RPI = 64 / CH, NI = KT / RPI;  // chunks of a row; rows and count of a DMA instruction
-  const int* ids = reinterpret_cast<const int*>(lds + NW * RING + wave * 1024);  // 4 tiles' page numbers
+  const int* ids = reinterpret_cast<const int*>(lds + NW * 2 * TILE + wave * 512);  // two tiles' page numbers
   const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
   auto fetch_ids = [&](int t) {
     const int j = min(first_key(t) + (lane & 31), k1 - 1);
-    dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
+    dma4(table + divide(j, p.page), ids_at + (t & 1) * 256);
   };
-  const char* kbase = reinterpret_cast<const char*>(g.c.k) + kvh * g.c.stride_head * ES;
-  const char* vbase = reinterpret_cast<const char*>(g.c.v) + kvh * g.c.stride_head * ES;
-  auto fetch = [&](int t) {
-    const uint32_t st = ring + (t & 1) * 2 * TILE;
+  const char* bases[2] = {reinterpret_cast<const char*>(g.c.k) + kvh * g.c.stride_head * ES,
+                          reinterpret_cast<const char*>(g.c.v) + kvh * g.c.stride_head * ES};
+  // Whole tiles of pages of 16 n tokens: half a tile lies in one page, whose address is scalar; a lane adds its
+  // row and chunk.
+  const bool plain = D == DP && g.c.page_size % 16 == 0 && (k0 & 15) == 0 && g.c.stride_token < (1 << 20);
+  const uint32_t token_bytes = (uint32_t)g.c.stride_token * ES;
+  auto fetch = [&](int t, auto of_v) {
+    constexpr bool V = decltype(of_v)::value;
+    const uint32_t st = V ? vt : kt;
+    const int j0 = first_key(t);
+    int lane_here = lane;  // opaque, or the lanes' offsets move out of the loop and fill registers
+    asm volatile("" : "+v"(lane_here));
+    auto chunk = [&](int r) {
+      const int ch = lane_here % CH;
+      return (V ? ch ^ v_swz_few<ROWB, FP8>(r) : ch ^ k_swz_few<ROWB>(r)) * 16;
+    };
+    if (plain && j0 + KT <= k1) {
+      const int id0 = __builtin_amdgcn_readfirstlane(ids[(t & 1) * 64]);
+      const int id1 = __builtin_amdgcn_readfirstlane(ids[(t & 1) * 64 + 16]);
+      if ((uint32_t)id0 < (uint32_t)g.c.pages && (uint32_t)id1 < (uint32_t)g.c.pages) {
 #pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int j = j0 + 16 * half, id = half ? id1 : id0;
+          const int64_t at = id * g.c.stride_page + (j - divide(j, p.page) * g.c.page_size) * g.c.stride_token;
+          const char* base = bases[V] + at * ES;
+#pragma unroll
+          for (int i = 0; i < NI / 2; ++i) {
+            const int in = i * RPI + lane_here / CH;
+            dma16(base + (int64_t)i * RPI * token_bytes, (uint32_t)(lane_here / CH) * token_bytes + chunk(16 * half + in),
+                  st + (half * NI / 2 + i) * 1024);
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll 1
     for (int i = 0; i < NI; ++i) {
-      const int r = i * RPI + lane / CH, ch = lane % CH;
-      const int j = first_key(t) + r, page = divide(j, p.page), id = ids[(t & 3) * 64 + r];
+      const int r = i * RPI + lane_here / CH, at_chunk = chunk(r);
+      const int j = j0 + r, page = divide(j, p.page), id = ids[(t & 1) * 64 + r];
       const int64_t at = (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES;
       const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
-      const int ck = (ch ^ k_swz_few<ROWB>(r)) * 16, cv = (ch ^ v_swz_few<ROWB, FP8>(r)) * 16;
-      const void* ks = in && !good         ? (const void*)(FP8 ? kNans8 : kNans)
-                       : in && ck < D * ES ? (const void*)(kbase + at + ck)
-                                           : (const void*)kZeros;
-      const void* vs = in && good && cv < D * ES ? (const void*)(vbase + at + cv) : (const void*)kZeros;
-      dma16(ks, st + i * 1024);
-      dma16(vs, st + TILE + i * 1024);
+      const void* from = in && !good && !V                   ? (const void*)(FP8 ? kNans8 : kNans)
+                         : in && good && at_chunk < D * ES ? (const void*)(bases[V] + at + at_chunk)
+                                                           : (const void*)kZeros;
+      dma16(from, st + i * 1024);
     }
   };
-  if (mine > 0) fetch_ids(0);
-  if (mine > 1) fetch_ids(1);
+  constexpr std::false_type K_{};
+  constexpr std::true_type V_{};
+  if (mine > 0) fetch_ids(0), fetch_ids(1);
 
   // Q^T operand: lane (row = lane % 16, grp = lane / 16), step t.  f16: dims 32 t + 8 grp ..; e4m3: a
   // 16-byte chunk of K feeds two steps, so dims 16 (4 (t / 2) + grp) + 8 (t % 2) ..
@@ -408,27 +449,60 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>())) void attention_few_ker
 #pragma unroll
   for (int i = 0; i < DB; ++i) acc[i] = {0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int t, uint32_t kt) {  // kt: LDS address of the K tile, V's behind it
-    const uint32_t vt = kt + TILE;
+  // LDS offsets of a lane's fragments: the swizzles fold into the lane's part
+  constexpr int KA = ROWB / 64;  // 64-byte blocks of a row: chunks 4 x + grp
+  uint32_t k_at[KA];
+#pragma unroll
+  for (int x = 0; x < KA; ++x) k_at[x] = kt + row * ROWB + (((4 * x + grp) ^ k_swz_few<ROWB>(row)) * 16);
+  uint32_t v_row, v_chunk;
+  if constexpr (FP8) {  // 8 rows x 16 codes: lane L of 16 points at row L / 2, half L % 2
+    const int x = (lane & 15) >> 1, r = (x & 4) * 4 + 4 * grp + (x & 3);
+    v_row = vt + r * ROWB + (lane & 1) * 8, v_chunk = v_swz_few<ROWB, FP8>(r);
+  } else {
+    const int r = 4 * grp + ((lane & 15) >> 2);
+    v_row = vt + r * ROWB + (lane & 1) * 8, v_chunk = ((lane & 3) >> 1) ^ v_swz_few<ROWB, FP8>(r);
+  }
+  // V^T operand: dims 16 i + lane % 16, keys 4 grp .. + 3 and 16 + 4 grp .. + 3
+  auto v_frag = [&](int i) {
+    if constexpr (FP8) {
+      const auto v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_i32x2*>(v_row + (i ^ v_chunk) * 16));
+      return widen8(v[0], v[1]);
+    } else {
+      const uint32_t at = v_row + ((2 * i) ^ v_chunk) * 16;
+      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
+      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 16 * ROWB));
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  };
+
+  if (mine > 0) {
+    wait_vm<0>();
+    fetch(0, K_);
+    fetch(0, V_);
+  }
+  for (int t = 0; t < mine; ++t) {
     const int j0 = first_key(t);
+    wait_vm<NI>();  // V of this tile may be in flight
     f32x4 sc[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       sc[kb] = {0.f, 0.f, 0.f, 0.f};
-      const int r = 16 * kb + row;
 #pragma unroll
-      for (int st = 0; st < STEPS; st += ES == 1 ? 2 : 1) {
-        const uint32_t at = kt + r * ROWB + ((((FP8 ? 2 * st : 4 * st) + grp) ^ k_swz_few<ROWB>(r)) * 16);
+      for (int x = 0; x < KA; ++x) {
+        const uint32_t at = k_at[x] + 16 * kb * ROWB;
         if constexpr (FP8) {
-          f16x8 a[2];
-          const u32x4 x = *reinterpret_cast<const lds_u32x4*>(at);
-          widen(x, a);
-          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[0], q[st], sc[kb], 0, 0, 0);
-          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a[1], q[st + 1], sc[kb], 0, 0, 0);
+          const u32x4 codes = *reinterpret_cast<const lds_u32x4*>(at);
+          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(codes[0], codes[1]), q[2 * x], sc[kb], 0, 0, 0);
+          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(codes[2], codes[3]), q[2 * x + 1], sc[kb], 0, 0, 0);
         } else {
-          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const lds_f16x8*>(at), q[st], sc[kb], 0, 0, 0);
+          sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(*reinterpret_cast<const lds_f16x8*>(at), q[x], sc[kb], 0, 0, 0);
         }
       }
+    }
+    if (t + 1 < mine) {
+      wait_lds();  // K has been read
+      fetch_ids(t + 2);
+      fetch(t + 1, K_);
     }
     // sc[kb][e]: key j0 + 16 kb + 4 grp + e of this lane's row
     const bool edge = j0 + KT > all1 || j0 < all0;
@@ -463,85 +537,54 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>())) void attention_few_ker
         l += x;
         w[4 * kb + e] = (f16)x;
       }
-    // V^T operand: dims 16 i + lane % 16, keys 4 grp .. + 3 and 16 + 4 grp .. + 3
-    auto v_frag = [&](int i) {
-      if constexpr (FP8) {  // 8 rows x 16 codes: lane L of 16 points at row L / 2, half L % 2
-        const int x = (lane & 15) >> 1, r = (x & 4) * 4 + 4 * grp + (x & 3);
-        const auto v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_i32x2*>(
-            vt + r * ROWB + ((i ^ v_swz_few<ROWB, FP8>(r)) * 16) + (lane & 1) * 8));
-        return widen8(v[0], v[1]);
-      } else {
-        s16x4 v[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int r = 16 * u + 4 * grp + ((lane & 15) >> 2), ch = 2 * i + ((lane & 3) >> 1);
-          v[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(
-              vt + r * ROWB + ((ch ^ v_swz_few<ROWB, FP8>(r)) * 16) + (lane & 1) * 8));
-        }
-        return __builtin_bit_cast(f16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-      }
-    };
-    if (!edge || n == 1) {  // one token: no row sees less of the tile than another
-#pragma unroll
-      for (int i = 0; i < DB; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_frag(i), w, acc[i], 0, 0, 0);
-      return;
-    }
-    uint32_t odd = 0;
-#pragma unroll
-    for (int i = 0; i < DB; ++i)
-      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(finite(v_frag(i), odd), w, acc[i], 0, 0, 0);
-    if (__any(odd != 0)) {
-#pragma unroll 1
-      for (int r = 0; r < KT; ++r) {
-        const int j = j0 + r;
-        const bool see = j >= see0 && j < see1;
-#pragma unroll
-        for (int i = 0; i < DB; ++i) {
-          const int byte = (16 * i + 4 * grp) * ES;
-          const uint32_t at = vt + r * ROWB + ((byte / 16) ^ v_swz_few<ROWB, FP8>(r)) * 16 + byte % 16;
-          f16x4 v;
-          if constexpr (FP8) {
-            const f16x8 x = widen8(*reinterpret_cast<const lds_i32*>(at), 0);
-            v = __builtin_shufflevector(x, x, 0, 1, 2, 3);
-          } else {
-            v = *reinterpret_cast<const lds_f16x4*>(at);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][e] += see ? special_of(v[e]) : 0.f;
-        }
-      }
-    }
-  };
-
-  // in the order of issue: data(t), ids(t + 2), data(t + 1), ids(t + 3), ...: a wait that leaves the
-  // newest data in flight covers the tile before it and the page numbers of the one after it
-  if (mine > 0) {
-    wait_vm<0>();
-    fetch(0);
-    if (mine > 2) fetch_ids(2);
-    if (mine > 1) fetch(1);
-  }
-  for (int t = 0; t < mine; ++t) {
     if (t + 1 < mine)
-      wait_vm<2 * NI>();
+      wait_vm<NI + 1>();  // K and the page numbers of the next tiles may be in flight
     else
       wait_vm<0>();
-    compute(t, ring + (t & 1) * 2 * TILE);
-    if (t + 2 < mine) {
-      wait_lds();  // the stage has been read
-      if (t + 3 < mine) fetch_ids(t + 3);
-      fetch(t + 2);
+    if (!edge || (n == 1 && j0 >= all0)) {  // no row sees less of the tile's keys (past k1: zeros) than another
+#pragma unroll
+      for (int i = 0; i < DB; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_frag(i), w, acc[i], 0, 0, 0);
+    } else {
+      uint32_t odd = 0;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(finite(v_frag(i), odd), w, acc[i], 0, 0, 0);
+      if (__any(odd != 0)) {
+#pragma unroll 1
+        for (int r = 0; r < KT; ++r) {
+          const int j = j0 + r;
+          const bool see = j >= see0 && j < see1;
+#pragma unroll
+          for (int i = 0; i < DB; ++i) {
+            const int byte = (16 * i + 4 * grp) * ES;
+            const uint32_t at = vt + r * ROWB + ((byte / 16) ^ v_swz_few<ROWB, FP8>(r)) * 16 + byte % 16;
+            f16x4 v;
+            if constexpr (FP8) {
+              const f16x8 x = widen8(*reinterpret_cast<const lds_i32*>(at), 0);
+              v = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+            } else {
+              v = *reinterpret_cast<const lds_f16x4*>(at);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] += see ? special_of(v[e]) : 0.f;
+          }
+        }
+      }
+    }
+    if (t + 1 < mine) {
+      wait_lds();  // V has been read
+      fetch(t + 1, V_);
     }
   }
 
   // join the waves: each leaves (m, l) and its sums in LDS
   l = across<true>(l, add2);
-  float* sums = reinterpret_cast<float*>(lds + wave * RING);  // [16][DP + 4]
-  constexpr int LD = DP + 4;
-  static_assert(16 * LD * 4 <= RING, "a wave's sums fit in its ring");
+  // sums f32 [16][DP], four dims x of row r at x ^ r (rows of one column would share a bank)
+  static_assert(16 * DP * 4 <= 2 * TILE, "a wave's sums fit where its tiles were");
+  auto sums_of = [&](int w, int r, int x) { return reinterpret_cast<f32x4*>(lds + w * 2 * TILE + r * DP * 4 + (x ^ r) * 16); };
   wait_lds();
 #pragma unroll
-  for (int i = 0; i < DB; ++i) *reinterpret_cast<f32x4*>(&sums[row * LD + 16 * i + 4 * grp]) = acc[i];
+  for (int i = 0; i < DB; ++i) *sums_of(wave, row, 4 * i + grp) = acc[i];
   if (grp == 0) join[wave][row][0] = m, join[wave][row][1] = l;
   __syncthreads();
   const float vs = FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f;
@@ -555,7 +598,7 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>())) void attention_few_ker
     for (int w = 0; w < NW; ++w) {
       const float mw = join[w][r][0], f = mw == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mw - mt);
       lt += join[w][r][1] * f;
-      o += *reinterpret_cast<const f32x4*>(lds + w * RING + (r * LD + d) * 4) * f;
+      o += *sums_of(w, r, d / 4) * f;
     }
     if (count > 1) {
       if (r < p.part_rows) {
@@ -1051,11 +1094,11 @@ struct Launch {
 constexpr int kCus = 256;
 constexpr int kWorkgroups = 1024;  // of the kernel for many rows, about: two rounds of two per CU
 
-// Workgroups of the decode kernel that a CU holds, by its LDS (join and deal's own come to less than 1 KB).
-int few_per_cu(const AttnArgs& a) {
-  const int d = a.c.dim, lds = a.c.e4m3 ? d <= 64 ? few_lds<64, true>() : d <= 128 ? few_lds<128, true>() : few_lds<256, true>()
-                                        : d <= 64 ? few_lds<64, false>() : d <= 128 ? few_lds<128, false>() : few_lds<256, false>();
-  return 163840 / (lds + 1024);
+// Workgroups of the decode kernel that a CU holds.
+int few_slots(const AttnArgs& a) {
+  const int d = a.c.dim;
+  return a.c.e4m3 ? d <= 64 ? few_per_cu<64, true>() : d <= 128 ? few_per_cu<128, true>() : few_per_cu<256, true>()
+                  : d <= 64 ? few_per_cu<64, false>() : d <= 128 ? few_per_cu<128, false>() : few_per_cu<256, false>();
 }
 
 Launch plan(const AttnArgs& a) {
@@ -1072,8 +1115,8 @@ Launch plan(const AttnArgs& a) {
     if (keys > kMinPart) {
       // one round of the workgroups that the CUs hold, in parts of equal length (their number exceeds
       // few_splits by at most one per sequence); with more sequences than that, two parts each, for balance
-      const int slots = kCus * few_per_cu(a) / a.c.heads;
-      x.few_splits = std::max(slots - a.B, a.B);
+      const int slots = kCus * few_slots(a) / a.c.heads;
+      x.few_splits = std::max(slots - a.B, 2 * a.B);
       // (keys + per - 1) / per parts of each sequence at most
       x.few_parts = (int)std::min<int64_t>((int64_t)x.few_splits + a.B, a.B * ((keys + kMinPart - 1) / kMinPart));
       x.few_bytes = (size_t)a.B * sizeof(int4) + (size_t)x.few_parts * a.c.heads * x.few_rows * row;
