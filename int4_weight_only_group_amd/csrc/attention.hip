@@ -702,8 +702,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   const int at0 = s.len - s.n + 1;  // keys before and at token 0's position
   const int see1 = at0 + tok, see0 = g.window ? see1 - g.window : 0;
   const int tok_a = divide(min(wr0, r1 - 1), p.group), tok_b = divide(max(wr0, wr1) - 1, p.group);
-  const int all1 = at0 + tok_a, all0 = g.window ? at0 + tok_b - g.window : 0;  // what all rows of the wave see
-  const int any1 = at0 + tok_b, any0 = g.window ? at0 + tok_a - g.window : 0;  // and what any does
+  const int any1 = at0 + tok_b, any0 = g.window ? at0 + tok_a - g.window : 0;  // keys that any row of the wave sees
   const float c = FP8 && g.c.k_scale ? p.c * g.c.k_scale[kvh] : p.c;
   float m = -INFINITY, l = 0.f;
   f32x16 acc[DB];
@@ -728,9 +727,23 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     v_at[i] = (uint32_t)(r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8);
   }
 
-  auto compute = [&](int t, uint32_t kt) {  // kt: LDS address of the K tile, V's behind it
+  // Tiles that all rows see whole come first, [f0, f0 + full), then those at the edges: the loop over the first
+  // knows no masks.  (One loop with branches kept two copies of the sums in registers.)
+  int f0 = 0, full;
+  {
+    const int end = at0 + divide(r0, p.group), beg = g.window ? at0 + divide(r1 - 1, p.group) - g.window : 0;
+    f0 = max(0, beg - k0 + KT - 1) / KT;
+    full = max(0, max(0, min(end, k1) - k0) / KT - f0);
+    if (full == 0) f0 = 0;
+  }
+  auto tile_at = [&](int i) { return i < full ? f0 + i : i - full < f0 ? i - full : i; };
+
+  // edges: this tile may hold keys that some row does not see
+  auto compute = [&](int t, uint32_t kt, auto edges) {  // kt: LDS address of the K tile, V's behind it
+    constexpr bool EDGES = decltype(edges)::value;
     const int j0 = k0 + t * KT;
-    if (!live || j0 >= any1 || j0 + KT <= any0) return;
+    if constexpr (EDGES)
+      if (j0 >= any1 || j0 + KT <= any0) return;
     // Fragments are read four at a time, a group ahead of the products that use them, and the compiler
     // is kept from moving more of them up (it would fill the register file with them and spill).
     auto k_frag = [&](int f) {  // step f / KB, key block f % KB
@@ -759,16 +772,14 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       __builtin_amdgcn_sched_barrier(0);
     }
     // sc[kb][e]: key j0 + 32 kb + 8 (e / 4) + 4 h + e % 4 of this lane's row
-    auto seen = [&](int kb, int e) {
-      const int j = j0 + 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3);
-      return j >= see0 && j < see1;
-    };
-    const bool edge = j0 + KT > all1 || j0 < all0;
-    if (edge) {
+    if constexpr (EDGES) {
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) sc[kb][e] = seen(kb, e) ? sc[kb][e] : -INFINITY;
+        for (int e = 0; e < 16; ++e) {
+          const int j = j0 + 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3);
+          sc[kb][e] = j >= see0 && j < see1 ? sc[kb][e] : -INFINITY;
+        }
     }
     float top = -INFINITY;
 #pragma unroll
@@ -804,35 +815,30 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
     };
     uint32_t odd = 0;
-    auto weigh = [&](auto clean) {  // O^T += V^T P^T: product x is keys block x % (2 KB), dims block x / (2 KB)
-      constexpr int N = DB * 2 * KB;
+    // product x: keys block x % (2 KB), dims block x / (2 KB)
+    constexpr int N = DB * 2 * KB;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) fr[0][f] = v_frag(f / (2 * KB), f % (2 * KB));
+    for (int f = 0; f < 4; ++f) fr[0][f] = v_frag(f / (2 * KB), f % (2 * KB));
 #pragma unroll
-      for (int gr = 0; gr < N / 4; ++gr) {
-        if (gr + 1 < N / 4) {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int x = 4 * (gr + 1) + f;
-            fr[(gr + 1) & 1][f] = v_frag(x / (2 * KB), x % (2 * KB));
-          }
-        }
+    for (int gr = 0; gr < N / 4; ++gr) {
+      if (gr + 1 < N / 4) {
 #pragma unroll
         for (int f = 0; f < 4; ++f) {
-          const int x = 4 * gr + f, i = x / (2 * KB);
-          f16x8 v = fr[gr & 1][f];
-          if constexpr (decltype(clean)::value) v = finite(v, odd);
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[x % (2 * KB)], acc[i], 0, 0, 0);
+          const int x = 4 * (gr + 1) + f;
+          fr[(gr + 1) & 1][f] = v_frag(x / (2 * KB), x % (2 * KB));
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
-    };
-    if (!edge) {
-      weigh(std::false_type{});
-      return;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const int x = 4 * gr + f, i = x / (2 * KB);
+        f16x8 v = fr[gr & 1][f];
+        if constexpr (EDGES) v = finite(v, odd);
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[x % (2 * KB)], acc[i], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
-    weigh(std::true_type{});
-    if (__any(odd != 0)) {
+    if constexpr (EDGES) {
+      if (!__any(odd != 0)) return;
 #pragma unroll 1
       for (int r = 0; r < KT; ++r) {
         const int j = j0 + r;
@@ -859,7 +865,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     const uint16_t* kbase = reinterpret_cast<const uint16_t*>(g.c.k) + kvh * g.c.stride_head;
     const uint16_t* vbase = reinterpret_cast<const uint16_t*>(g.c.v) + kvh * g.c.stride_head;
     auto fetch_ids = [&](int t) {
-      const int j = min(k0 + t * KT + RW * wave + lane % RW, k1 - 1);
+      const int j = min(k0 + tile_at(t) * KT + RW * wave + lane % RW, k1 - 1);
       dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
     };
     // A whole tile of whole pages: this wave's RW keys lie in one page, whose address is scalar; a lane adds
@@ -870,8 +876,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       int lane_here = lane;  // opaque, or the offsets below move out of the loop and cost 8 registers
       asm volatile("" : "+v"(lane_here));
       const uint32_t st = lds_at + (t & 1) * 2 * TILE + wave * (TILE / NW);
-      const int jw = k0 + t * KT + RW * wave;
-      if (plain && k0 + (t + 1) * KT <= k1) {
+      const int jt = k0 + tile_at(t) * KT, jw = jt + RW * wave;
+      if (plain && jt + KT <= k1) {
         const int id = __builtin_amdgcn_readfirstlane(ids[(t & 3) * 64]);
         if ((uint32_t)id < (uint32_t)g.c.pages) {
           const int64_t at = id * g.c.stride_page + (jw - divide(jw, p.page) * g.c.page_size) * g.c.stride_token;
@@ -906,13 +912,25 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       fetch(0);
       if (tiles > 1) fetch_ids(1);
     }
-    for (int t = 0; t < tiles; ++t) {
+    auto turn = [&](int i) {
       meet();
-      if (t + 1 < tiles) {
-        fetch(t + 1);
-        if (t + 2 < tiles) fetch_ids(t + 2);
+      if (i + 1 < tiles) {
+        fetch(i + 1);
+        if (i + 2 < tiles) fetch_ids(i + 2);
       }
-      compute(t, lds_at + (t & 1) * 2 * TILE);
+    };
+    int i = 0;
+    if (!live) {
+      for (; i < tiles; ++i) turn(i);
+    } else {
+      for (; i < full; ++i) {
+        turn(i);
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{});
+      }
+      for (; i < tiles; ++i) {
+        turn(i);
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{});
+      }
     }
   } else {
     constexpr int CH = DP / 16, RPI = 64 / CH, NI = (RW + RPI - 1) / RPI;
@@ -920,12 +938,12 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     const uint8_t* vbase = reinterpret_cast<const uint8_t*>(g.c.v) + kvh * g.c.stride_head;
     static_assert(RW % RPI == 0, "whole rows of a load");
     u32x4 kr[NI], vr[NI];
-    auto page_id = [&](int t) { return table[divide(min(k0 + t * KT + RW * wave + lane % RW, k1 - 1), p.page)]; };
+    auto page_id = [&](int t) { return table[divide(min(k0 + tile_at(t) * KT + RW * wave + lane % RW, k1 - 1), p.page)]; };
     auto load = [&](int t, int ids) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int rw = i * RPI + lane / CH, d = lane % CH * 16;
-        const int j = k0 + t * KT + RW * wave + rw, page = divide(j, p.page), id = __shfl(ids, rw);
+        const int j = k0 + tile_at(t) * KT + RW * wave + rw, page = divide(j, p.page), id = __shfl(ids, rw);
         const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token + d;
         const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
         const uint32_t fill = in && !good ? 0x7f7f7f7fu : 0u;
@@ -958,14 +976,30 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       if (tiles > 1) ids = page_id(1);
       store(lds);
     }
-    for (int t = 0; t < tiles; ++t) {
+    auto turn = [&](int i) {
       __syncthreads();
-      if (t + 1 < tiles) {
-        load(t + 1, ids);
-        if (t + 2 < tiles) ids = page_id(t + 2);
+      if (i + 1 < tiles) {
+        load(i + 1, ids);
+        if (i + 2 < tiles) ids = page_id(i + 2);
       }
-      compute(t, lds_at + (t & 1) * 2 * TILE);
-      if (t + 1 < tiles) store(lds + ((t + 1) & 1) * 2 * TILE);
+    };
+    auto land = [&](int i) {
+      if (i + 1 < tiles) store(lds + ((i + 1) & 1) * 2 * TILE);
+    };
+    int i = 0;
+    if (!live) {
+      for (; i < tiles; ++i) turn(i), land(i);
+    } else {
+      for (; i < full; ++i) {
+        turn(i);
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{});
+        land(i);
+      }
+      for (; i < tiles; ++i) {
+        turn(i);
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{});
+        land(i);
+      }
     }
   }
 
