@@ -30,6 +30,7 @@ namespace {
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
 typedef __attribute__((address_space(3))) f16x4 lds_f16x4;
 typedef int i32x2 __attribute__((ext_vector_type(2)));
@@ -739,16 +740,22 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   auto tile_at = [&](int i) { return i < full ? f0 + i : i - full < f0 ? i - full : i; };
 
   // edges: this tile may hold keys that some row does not see
-  auto compute = [&](int t, uint32_t kt, auto edges) {  // kt: LDS address of the K tile, V's behind it
+  // between(gr) is called after the gr-th group of the first product: the next tile's DMA goes there
+  auto compute = [&](int t, uint32_t kt, auto edges, auto between) {  // kt: LDS address of the K tile, V's behind it
     constexpr bool EDGES = decltype(edges)::value;
     const int j0 = k0 + t * KT;
     if constexpr (EDGES)
       if (j0 >= any1 || j0 + KT <= any0) return;
+    lds_char *kp[KA], *vp[VA];
+#pragma unroll
+    for (int x = 0; x < KA; ++x) kp[x] = reinterpret_cast<lds_char*>(kt + k_at[x]);
+#pragma unroll
+    for (int x = 0; x < VA; ++x) vp[x] = reinterpret_cast<lds_char*>(kt + v_at[x]);
     // Fragments are read four at a time, a group ahead of the products that use them, and the compiler
     // is kept from moving more of them up (it would fill the register file with them and spill).
     auto k_frag = [&](int f) {  // step f / KB, key block f % KB
       const int st = f / KB;
-      return *reinterpret_cast<const lds_f16x8*>(kt + k_at[st % KA] + (uint32_t)(st / KA * 256 + f % KB * 32 * DP * 2));
+      return *reinterpret_cast<const lds_f16x8*>(kp[st % KA] + (st / KA * 256 + f % KB * 32 * DP * 2));
     };
     f32x16 sc[KB];
 #pragma unroll
@@ -769,6 +776,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
         const int x = 4 * gr + f;
         sc[x % KB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[gr & 1][f], q[x / KB], sc[x % KB], 0, 0, 0);
       }
+      between(gr);
       __builtin_amdgcn_sched_barrier(0);
     }
     // sc[kb][e]: key j0 + 32 kb + 8 (e / 4) + 4 h + e % 4 of this lane's row
@@ -809,7 +817,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       }
     // V^T operand: dims 32 i + lane % 32, keys 16 ks + 4 h .. + 3 and 16 ks + 8 + 4 h .. + 3
     auto v_frag = [&](int i, int ks) {
-      const uint32_t at = kt + v_at[i % VA] + (uint32_t)(TILE + i / VA * 256 + 16 * ks * DP * 2);
+      lds_char* at = vp[i % VA] + (TILE + i / VA * 256 + 16 * ks * DP * 2);
       const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
       const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 8 * DP * 2));
       return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -872,23 +880,28 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     // its row and chunk.  (Per-lane addresses of every DMA cost more VALU work than the softmax.)
     const bool plain = D == DP && g.c.page_size % RW == 0 && g.c.stride_token < (1 << 20);
     const uint32_t lane_row = (uint32_t)(lane / CH) * (uint32_t)g.c.stride_token;
-    auto fetch = [&](int t) {
+    const char *next_k = nullptr, *next_v = nullptr;  // the next tile's rows of this wave, when they are plain
+    uint32_t next_at = 0;
+    // DMA instruction i of the tile that ready() found plain
+    auto fetch_one = [&](int i) {
       int lane_here = lane;  // opaque, or the offsets below move out of the loop and cost 8 registers
       asm volatile("" : "+v"(lane_here));
+      const int r = RW * wave + i * RPI + lane_here / CH, ch = lane_here % CH;
+      const int64_t step = (int64_t)i * RPI * g.c.stride_token * 2;
+      dma16(next_k + step, (lane_row + (ch ^ k_swz<DP>(r)) * 8) * 2, next_at + i * 1024);
+      dma16(next_v + step, (lane_row + (ch ^ v_swz<DP>(r)) * 8) * 2, next_at + TILE + i * 1024);
+    };
+    // Makes tile t ready for fetch_one(0 .. NI - 1), or fetches it whole and says false.
+    auto ready = [&](int t) {
       const uint32_t st = lds_at + (t & 1) * 2 * TILE + wave * (TILE / NW);
       const int jt = k0 + tile_at(t) * KT, jw = jt + RW * wave;
       if (plain && jt + KT <= k1) {
         const int id = __builtin_amdgcn_readfirstlane(ids[(t & 3) * 64]);
         if ((uint32_t)id < (uint32_t)g.c.pages) {
           const int64_t at = id * g.c.stride_page + (jw - divide(jw, p.page) * g.c.page_size) * g.c.stride_token;
-#pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            const int r = RW * wave + i * RPI + lane_here / CH, ch = lane_here % CH;
-            const int64_t ai = at + i * RPI * g.c.stride_token;
-            dma16(kbase + ai, (lane_row + (ch ^ k_swz<DP>(r)) * 8) * 2, st + i * 1024);
-            dma16(vbase + ai, (lane_row + (ch ^ v_swz<DP>(r)) * 8) * 2, st + TILE + i * 1024);
-          }
-          return;
+          next_k = reinterpret_cast<const char*>(kbase + at), next_v = reinterpret_cast<const char*>(vbase + at);
+          next_at = st;
+          return true;
         }
       }
 #pragma unroll 1
@@ -905,6 +918,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
         dma16(ks, st + i * 1024);
         dma16(vs, st + TILE + i * 1024);
       }
+      return false;
+    };
+    auto fetch = [&](int t) {
+      if (ready(t)) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) fetch_one(i);
+      }
     };
     if (tiles > 0) {
       fetch_ids(0);
@@ -912,25 +932,34 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       fetch(0);
       if (tiles > 1) fetch_ids(1);
     }
+    // tile i is there; the next one's DMA starts, but for what it leaves to fetch_one if that says true
     auto turn = [&](int i) {
       meet();
-      if (i + 1 < tiles) {
-        fetch(i + 1);
-        if (i + 2 < tiles) fetch_ids(i + 2);
-      }
+      if (i + 2 < tiles) fetch_ids(i + 2);
+      return i + 1 < tiles && ready(i + 1);
     };
     int i = 0;
-    if (!live) {
-      for (; i < tiles; ++i) turn(i);
-    } else {
+    if (live) {
+      constexpr int GROUPS = STEPS * KB / 4, EACH = (NI + GROUPS - 1) / GROUPS;
       for (; i < full; ++i) {
-        turn(i);
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{});
+        const bool more = turn(i);
+        // one or two DMA instructions behind each group of products: issued together, the waves' DMA queues
+        // up for the memory path while the matrix cores idle
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{}, [&](int gr) {
+          if (more) {
+#pragma unroll
+            for (int e = 0; e < EACH; ++e)
+              if (gr * EACH + e < NI) fetch_one(gr * EACH + e);
+          }
+        });
       }
-      for (; i < tiles; ++i) {
-        turn(i);
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{});
+    }
+    for (; i < tiles; ++i) {
+      if (turn(i)) {
+#pragma unroll
+        for (int e = 0; e < NI; ++e) fetch_one(e);
       }
+      if (live) compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{}, [](int) {});
     }
   } else {
     constexpr int CH = DP / 16, RPI = 64 / CH, NI = (RW + RPI - 1) / RPI;
@@ -992,12 +1021,12 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     } else {
       for (; i < full; ++i) {
         turn(i);
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{});
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{}, [](int) {});
         land(i);
       }
       for (; i < tiles; ++i) {
         turn(i);
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{});
+        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{}, [](int) {});
         land(i);
       }
     }
@@ -1126,7 +1155,7 @@ struct Launch {
 };
 
 constexpr int kCus = 256;
-constexpr int kWorkgroups = 1024;  // of the kernel for many rows, about: two rounds of two per CU
+constexpr int kWorkgroups = 512;  // of the kernel for many rows, about: two per CU
 
 // Workgroups of the decode kernel that a CU holds.
 int few_slots(const AttnArgs& a) {
