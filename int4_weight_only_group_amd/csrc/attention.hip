@@ -29,6 +29,7 @@ namespace {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) f16x8 lds_f16x8;
@@ -38,6 +39,9 @@ typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __attribute__((address_space(3))) int lds_i32;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+
+// for lambdas: one that is not inlined keeps what it captures in memory
+#define W4_INLINE __attribute__((always_inline))
 
 constexpr float kLog2e = 1.44269504088896340736f;
 // m moves only when a score exceeds it by more than this (in powers of two): weights stay below
@@ -664,7 +668,7 @@ __device__ __forceinline__ void locate(const Plan& p, int tile, int& b, int& at)
 template <int DP, bool FP8>
 __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_many_kernel(Plan p) {
   constexpr int NW = kManyWaves, KT = many_keys<DP>(), TILE = KT * DP * 2, RW = KT / NW;
-  constexpr int STEPS = DP / 16, DB = DP / 32, KB = KT / 32;
+  constexpr int STEPS = DP / 16, DB = DP / 32, SUB = KT / 32;
   extern __shared__ __align__(16) unsigned char lds[];
   const AttnArgs& g = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -712,24 +716,39 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
 
+  // LDS: two K tiles, two V tiles, the waves' page numbers.  Offsets of a lane's fragments within a tile:
+  // the swizzles fold into the lane's part, up to the chunk bits that count steps (K) or dims blocks (V)
+  // below 256 bytes.
   const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
-  // LDS offsets of a lane's fragments within a tile; the swizzles fold into the lane's part, up to the
-  // chunk bits that count steps (K) or dims blocks (V) below 256 bytes
+  auto k_tile = [](int i) { return (uint32_t)((i & 1) * TILE); };
+  auto v_tile = [](int i) { return (uint32_t)((2 + (i & 1)) * TILE); };
+  constexpr int HALF = 32 * DP * 2;  // bytes of 32 keys
   constexpr int KA = STEPS < 8 ? STEPS : 8, VA = DB < 4 ? DB : 4;
   uint32_t k_at[KA], v_at[VA];
 #pragma unroll
   for (int st = 0; st < KA; ++st) {
     const int r = lane & 31;
-    k_at[st] = (uint32_t)(r * DP * 2 + (((2 * st + h) ^ k_swz<DP>(r)) * 16));
+    k_at[st] = lds_at + (uint32_t)(r * DP * 2 + (((2 * st + h) ^ k_swz<DP>(r)) * 16));
   }
 #pragma unroll
   for (int i = 0; i < VA; ++i) {
     const int r = 4 * h + ((lane & 15) >> 2), ch = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    v_at[i] = (uint32_t)(r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8);
+    v_at[i] = lds_at + (uint32_t)(r * DP * 2 + ((ch ^ v_swz<DP>(r)) * 16) + (lane & 1) * 8);
   }
+  // K operand: key lane % 32 of 32 at LDS offset `at`, dims 16 st + 8 h ..
+  auto k_frag = [&](uint32_t at, int st) W4_INLINE {
+    return *reinterpret_cast<const lds_f16x8*>(reinterpret_cast<lds_char*>(k_at[st % KA]) + (at + st / KA * 256));
+  };
+  // V^T operand x of 32 keys at `at`: dims 32 (x / 2) + lane % 32, keys 16 (x % 2) + 4 h .. + 3 and + 8 ..
+  auto v_frag = [&](uint32_t at, int x) W4_INLINE {
+    lds_char* from = reinterpret_cast<lds_char*>(v_at[x / 2 % VA]) + (at + x / 2 / VA * 256 + 16 * (x & 1) * DP * 2);
+    const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from));
+    const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(from + 8 * DP * 2));
+    return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
 
-  // Tiles that all rows see whole come first, [f0, f0 + full), then those at the edges: the loop over the first
-  // knows no masks.  (One loop with branches kept two copies of the sums in registers.)
+  // ---- whole tiles: [f0, f0 + full) of this part are seen whole by all rows and come first, in a loop
+  // without masks; the tiles at the edges follow.  The i-th tile taken:
   int f0 = 0, full;
   {
     const int end = at0 + divide(r0, p.group), beg = g.window ? at0 + divide(r1 - 1, p.group) - g.window : 0;
@@ -739,297 +758,374 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   }
   auto tile_at = [&](int i) { return i < full ? f0 + i : i - full < f0 ? i - full : i; };
 
-  // edges: this tile may hold keys that some row does not see
-  // between(gr) is called after the gr-th group of the first product: the next tile's DMA goes there
-  auto compute = [&](int t, uint32_t kt, auto edges, auto between) {  // kt: LDS address of the K tile, V's behind it
-    constexpr bool EDGES = decltype(edges)::value;
-    const int j0 = k0 + t * KT;
-    if constexpr (EDGES)
-      if (j0 >= any1 || j0 + KT <= any0) return;
-    lds_char *kp[KA], *vp[VA];
+  // The loop over whole tiles goes by 32 keys and is pipelined: while the softmax of block u runs on the VALU,
+  // the matrix cores compute the scores of block u + 1 and the weighted sums of block u - 1.  `sc` are
+  // u's scores, `w` the weights of u - 1 (scaled by the m of then: when u moves m, the sums are rescaled
+  // after the products of u - 1).  Slices of four products carry their share of the VALU work, fragments
+  // are read a slice ahead, and between(x) follows slice x.  l sums the weights as rounded, which are the ones that
+  // multiply v.
+  f32x16 sc;
+  f16x8 w[2];
+  float ms = 0.f;  // m, or 0 before there is one
+  auto block = [&](auto with_qk, auto with_pv, uint32_t k_next, uint32_t v_last, auto between) W4_INLINE {
+    constexpr bool QK = decltype(with_qk)::value, PV = decltype(with_pv)::value;
+    constexpr int SLICES = STEPS / 2, EACH = 16 / SLICES;
+    f32x16 next;
+    f16x8 kf[2][2], vf[2][2];
+    u32x4 nw[2];
+    float y[16];
+    auto round_to = [&](int x) W4_INLINE {  // slice x's weights to f16, a slice after their exponentials
 #pragma unroll
-    for (int x = 0; x < KA; ++x) kp[x] = reinterpret_cast<lds_char*>(kt + k_at[x]);
-#pragma unroll
-    for (int x = 0; x < VA; ++x) vp[x] = reinterpret_cast<lds_char*>(kt + v_at[x]);
-    // Fragments are read four at a time, a group ahead of the products that use them, and the compiler
-    // is kept from moving more of them up (it would fill the register file with them and spill).
-    auto k_frag = [&](int f) {  // step f / KB, key block f % KB
-      const int st = f / KB;
-      return *reinterpret_cast<const lds_f16x8*>(kp[st % KA] + (st / KA * 256 + f % KB * 32 * DP * 2));
+      for (int e = EACH * x; e < EACH * (x + 1); e += 2) {
+        const f16x2 pair = {(f16)y[e], (f16)y[e + 1]};
+        nw[e >> 3][e >> 1 & 3] = __builtin_bit_cast(uint32_t, pair);
+      }
     };
-    f32x16 sc[KB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+    for (int e = 0; e < 16; ++e) next[e] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) sc[kb][e] = 0.f;
-    f16x8 fr[2][4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) fr[0][f] = k_frag(f);
-#pragma unroll
-    for (int gr = 0; gr < STEPS * KB / 4; ++gr) {
-      if (gr + 1 < STEPS * KB / 4) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) fr[(gr + 1) & 1][f] = k_frag(4 * (gr + 1) + f);
-      }
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int x = 4 * gr + f;
-        sc[x % KB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr[gr & 1][f], q[x / KB], sc[x % KB], 0, 0, 0);
-      }
-      between(gr);
-      __builtin_amdgcn_sched_barrier(0);
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (QK) kf[0][e] = k_frag(k_next, e);
+      if constexpr (PV) vf[0][e] = v_frag(v_last, e);
     }
-    // sc[kb][e]: key j0 + 32 kb + 8 (e / 4) + 4 h + e % 4 of this lane's row
-    if constexpr (EDGES) {
+    float top[6];
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int j = j0 + 32 * kb + 8 * (e >> 2) + 4 * h + (e & 3);
-          sc[kb][e] = j >= see0 && j < see1 ? sc[kb][e] : -INFINITY;
-        }
-    }
-    float top = -INFINITY;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, sc[kb][e]);
-    top *= c;
-    if (__any(top > m + kSlack)) {
-      const float mn = fmaxf(m, across<false>(top, fmax2));
-      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+    for (int e = 0; e < 5; ++e) top[e] = fmaxf(fmaxf(sc[3 * e], sc[3 * e + 1]), sc[3 * e + 2]);
+    top[0] = fmaxf(fmaxf(top[0], top[1]), sc[15]);
+    top[2] = fmaxf(fmaxf(top[2], top[3]), top[4]);
+    top[0] = fmaxf(top[0], top[2]) * c;
+    const bool move = __any(top[0] > m + kSlack);
+    float f = 1.f;
+    if (move) {
+      const float mn = fmaxf(m, across<false>(top[0], fmax2));
+      f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      m = mn;
+      ms = m == -INFINITY ? 0.f : m;
       l *= f;
+    }
+#pragma unroll
+    for (int x = 0; x < SLICES; ++x) {
+      if (x + 1 < SLICES) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (QK) kf[(x + 1) & 1][e] = k_frag(k_next, 2 * (x + 1) + e);
+          if constexpr (PV) vf[(x + 1) & 1][e] = v_frag(v_last, 2 * (x + 1) + e);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if constexpr (QK) next = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[x & 1][e], q[2 * x + e], next, 0, 0, 0);
+        if constexpr (PV) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[x & 1][e], w[e], acc[x], 0, 0, 0);
+      }
+      if (x > 0) round_to(x - 1);
+#pragma unroll
+      for (int e = EACH * x; e < EACH * (x + 1); ++e) {
+        y[e] = __builtin_amdgcn_exp2f(sc[e] * c - ms);
+        asm volatile("" : "+v"(y[e]));  // in this slice: the compiler would move it behind the last branch
+      }
+#pragma unroll
+      for (int e = 0; e < 2 * (QK + PV); ++e) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
+        __builtin_amdgcn_sched_group_barrier(0x402, EACH + 1, 0);  // VALU work
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      between(x);
+    }
+    round_to(SLICES - 1);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t bits = nw[e >> 2][e & 3];
+      const hf16x2 ones = {(__fp16)1.f, (__fp16)1.f};
+      l = __builtin_amdgcn_fdot2(__builtin_bit_cast(hf16x2, bits), ones, l, false);
+    }
+    if (move) {
 #pragma unroll
       for (int i = 0; i < DB; ++i)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][e] *= f;
-      m = mn;
     }
-    const float ms = m == -INFINITY ? 0.f : m;
-    f16x8 w[2 * KB];  // 16 keys each
+    w[0] = __builtin_bit_cast(f16x8, nw[0]), w[1] = __builtin_bit_cast(f16x8, nw[1]);
+    sc = next;
+  };
+
+  // ---- a tile that some row does not see whole, 32 keys at a time
+  auto edge = [&](int i) W4_INLINE {
+#pragma unroll 1
+    for (int u = 0; u < SUB; ++u) {
+      const int j0 = k0 + tile_at(i) * KT + 32 * u;
+      if (j0 >= any1 || j0 + 32 <= any0) continue;
+      const uint32_t kt = k_tile(i) + u * HALF, vt = v_tile(i) + u * HALF;
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb)
+      for (int e = 0; e < 16; ++e) sc[e] = 0.f;
+#pragma unroll
+      for (int st = 0; st < STEPS; ++st)
+        sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_frag(kt, st), q[st], sc, 0, 0, 0);
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {  // key j0 + 8 (e / 4) + 4 h + e % 4 of this lane's row
+        const int j = j0 + 8 * (e >> 2) + 4 * h + (e & 3);
+        sc[e] = j >= see0 && j < see1 ? sc[e] : -INFINITY;
+        top = fmaxf(top, sc[e]);
+      }
+      top = across<false>(top, fmax2) * c;
+      if (__any(top > m + kSlack)) {
+        const float mn = fmaxf(m, top), f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+        l *= f;
+#pragma unroll
+        for (int x = 0; x < DB; ++x)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[x][e] *= f;
+        m = mn;
+        ms = m == -INFINITY ? 0.f : m;
+      }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float x = __builtin_amdgcn_exp2f(sc[kb][e] * c - ms);
-        l += x;
-        w[2 * kb + (e >> 3)][e & 7] = (f16)x;
+        w[e >> 3][e & 7] = (f16)__builtin_amdgcn_exp2f(sc[e] * c - ms);
+        l += (float)w[e >> 3][e & 7];
       }
-    // V^T operand: dims 32 i + lane % 32, keys 16 ks + 4 h .. + 3 and 16 ks + 8 + 4 h .. + 3
-    auto v_frag = [&](int i, int ks) {
-      lds_char* at = vp[i % VA] + (TILE + i / VA * 256 + 16 * ks * DP * 2);
-      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
-      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 8 * DP * 2));
-      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
-    uint32_t odd = 0;
-    // product x: keys block x % (2 KB), dims block x / (2 KB)
-    constexpr int N = DB * 2 * KB;
+      uint32_t odd = 0;
 #pragma unroll
-    for (int f = 0; f < 4; ++f) fr[0][f] = v_frag(f / (2 * KB), f % (2 * KB));
-#pragma unroll
-    for (int gr = 0; gr < N / 4; ++gr) {
-      if (gr + 1 < N / 4) {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int x = 4 * (gr + 1) + f;
-          fr[(gr + 1) & 1][f] = v_frag(x / (2 * KB), x % (2 * KB));
-        }
-      }
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int x = 4 * gr + f, i = x / (2 * KB);
-        f16x8 v = fr[gr & 1][f];
-        if constexpr (EDGES) v = finite(v, odd);
-        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, w[x % (2 * KB)], acc[i], 0, 0, 0);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if constexpr (EDGES) {
-      if (!__any(odd != 0)) return;
+      for (int x = 0; x < 2 * DB; ++x)
+        acc[x / 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(finite(v_frag(vt, x), odd), w[x & 1], acc[x / 2], 0, 0, 0);
+      if (!__any(odd != 0)) continue;
 #pragma unroll 1
-      for (int r = 0; r < KT; ++r) {
+      for (int r = 0; r < 32; ++r) {
         const int j = j0 + r;
         const bool see = j >= see0 && j < see1;
 #pragma unroll
-        for (int i = 0; i < DB; ++i)
+        for (int x = 0; x < DB; ++x)
 #pragma unroll
           for (int a = 0; a < 4; ++a) {
             const f16x4 v = *reinterpret_cast<const lds_f16x4*>(
-                  kt + (uint32_t)(TILE + r * DP * 2 + ((4 * i + a) ^ v_swz<DP>(r)) * 16 + 8 * h));
+                lds_at + vt + (uint32_t)(r * DP * 2 + ((4 * x + a) ^ v_swz<DP>(r)) * 16 + 8 * h));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][4 * a + e] += see ? special_of(v[e]) : 0.f;
+            for (int e = 0; e < 4; ++e) acc[x][4 * a + e] += see ? special_of(v[e]) : 0.f;
           }
       }
     }
   };
-  // every wave's part of a stage is there, and the other stage has been read
-  auto meet = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
-  if constexpr (!FP8) {
-    constexpr int CH = DP / 8, RPI = 64 / CH, NI = RW / RPI;
-    const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);
-    const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
-    const uint16_t* kbase = reinterpret_cast<const uint16_t*>(g.c.k) + kvh * g.c.stride_head;
-    const uint16_t* vbase = reinterpret_cast<const uint16_t*>(g.c.v) + kvh * g.c.stride_head;
-    auto fetch_ids = [&](int t) {
-      const int j = min(k0 + tile_at(t) * KT + RW * wave + lane % RW, k1 - 1);
-      dma4(table + divide(j, p.page), ids_at + (t & 3) * 256);
-    };
-    // A whole tile of whole pages: this wave's RW keys lie in one page, whose address is scalar; a lane adds
-    // its row and chunk.  (Per-lane addresses of every DMA cost more VALU work than the softmax.)
-    const bool plain = D == DP && g.c.page_size % RW == 0 && g.c.stride_token < (1 << 20);
-    const uint32_t lane_row = (uint32_t)(lane / CH) * (uint32_t)g.c.stride_token;
-    const char *next_k = nullptr, *next_v = nullptr;  // the next tile's rows of this wave, when they are plain
-    uint32_t next_at = 0;
-    // DMA instruction i of the tile that ready() found plain
-    auto fetch_one = [&](int i) {
-      int lane_here = lane;  // opaque, or the offsets below move out of the loop and cost 8 registers
-      asm volatile("" : "+v"(lane_here));
-      const int r = RW * wave + i * RPI + lane_here / CH, ch = lane_here % CH;
-      const int64_t step = (int64_t)i * RPI * g.c.stride_token * 2;
-      dma16(next_k + step, (lane_row + (ch ^ k_swz<DP>(r)) * 8) * 2, next_at + i * 1024);
-      dma16(next_v + step, (lane_row + (ch ^ v_swz<DP>(r)) * 8) * 2, next_at + TILE + i * 1024);
-    };
-    // Makes tile t ready for fetch_one(0 .. NI - 1), or fetches it whole and says false.
-    auto ready = [&](int t) {
-      const uint32_t st = lds_at + (t & 1) * 2 * TILE + wave * (TILE / NW);
-      const int jt = k0 + tile_at(t) * KT, jw = jt + RW * wave;
-      if (plain && jt + KT <= k1) {
-        const int id = __builtin_amdgcn_readfirstlane(ids[(t & 3) * 64]);
-        if ((uint32_t)id < (uint32_t)g.c.pages) {
-          const int64_t at = id * g.c.stride_page + (jw - divide(jw, p.page) * g.c.page_size) * g.c.stride_token;
-          next_k = reinterpret_cast<const char*>(kbase + at), next_v = reinterpret_cast<const char*>(vbase + at);
-          next_at = st;
-          return true;
-        }
-      }
-#pragma unroll 1
-      for (int i = 0; i < NI; ++i) {
-        const int rw = i * RPI + lane / CH, r = RW * wave + rw, ch = lane % CH;
-        const int j = jw + rw, page = divide(j, p.page), id = ids[(t & 3) * 64 + rw];
-        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token;
-        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
-        const int ck = (ch ^ k_swz<DP>(r)) * 8, cv = (ch ^ v_swz<DP>(r)) * 8;
-        const void* ks = in && !good             ? (const void*)kNans
-                         : in && ck < D          ? (const void*)(kbase + at + ck)
-                                                 : (const void*)kZeros;
-        const void* vs = in && good && cv < D ? (const void*)(vbase + at + cv) : (const void*)kZeros;
-        dma16(ks, st + i * 1024);
-        dma16(vs, st + TILE + i * 1024);
-      }
-      return false;
-    };
-    auto fetch = [&](int t) {
-      if (ready(t)) {
-#pragma unroll
-        for (int i = 0; i < NI; ++i) fetch_one(i);
-      }
-    };
-    if (tiles > 0) {
-      fetch_ids(0);
-      wait_vm<0>();
-      fetch(0);
-      if (tiles > 1) fetch_ids(1);
-    }
-    // tile i is there; the next one's DMA starts, but for what it leaves to fetch_one if that says true
-    auto turn = [&](int i) {
-      meet();
-      if (i + 2 < tiles) fetch_ids(i + 2);
-      return i + 1 < tiles && ready(i + 1);
-    };
-    int i = 0;
-    if (live) {
-      constexpr int GROUPS = STEPS * KB / 4, EACH = (NI + GROUPS - 1) / GROUPS;
-      for (; i < full; ++i) {
-        const bool more = turn(i);
-        // one or two DMA instructions behind each group of products: issued together, the waves' DMA queues
-        // up for the memory path while the matrix cores idle
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{}, [&](int gr) {
-          if (more) {
-#pragma unroll
-            for (int e = 0; e < EACH; ++e)
-              if (gr * EACH + e < NI) fetch_one(gr * EACH + e);
-          }
-        });
+  // ---- fetching: this wave's RW rows of a tile
+  const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);  // 4 tiles' page numbers
+  const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
+  auto fetch_ids = [&](int i) W4_INLINE {
+    const int j = min(k0 + tile_at(i) * KT + RW * wave + lane % RW, k1 - 1);
+    dma4(table + divide(j, p.page), ids_at + (i & 3) * 256);
+  };
+  constexpr int ES = FP8 ? 1 : 2, CH = DP * ES / 16, RPI = 64 / CH, NI = RW / RPI;  // chunks of a row; rows and count of a load
+  static_assert(RW % RPI == 0, "whole rows of a load");
+  const char* bases[2] = {reinterpret_cast<const char*>(g.c.k) + kvh * g.c.stride_head * ES,
+                          reinterpret_cast<const char*>(g.c.v) + kvh * g.c.stride_head * ES};
+  // A whole tile of whole pages: this wave's rows lie in one page, whose address is scalar; a lane adds
+  // its row and chunk.  (Per-lane addresses cost more VALU work than the softmax.)
+  const bool plain = D == DP && g.c.page_size % RW == 0 && g.c.stride_token < (1 << 20);
+  const uint32_t lane_row = (uint32_t)(lane / CH) * (uint32_t)g.c.stride_token * ES;
+  const int64_t step_bytes = (int64_t)RPI * g.c.stride_token * ES;  // between the rows of two loads
+  u32x4 held[2][NI];  // e4m3: tiles on their way to LDS
+  const char* from[2] = {nullptr, nullptr};  // this wave's rows of the plain K and V tiles that ready() found, and where
+  uint32_t to[2] = {0, 0};                   // they go
+  auto chunk = [&](auto of_v, int r, int ln) W4_INLINE {  // byte of row r that lane's 16 bytes are fetched from
+    constexpr bool V = decltype(of_v)::value;
+    const int ch = ln % CH;
+    return FP8 ? ch * 16 : (V ? ch ^ v_swz<DP>(r) : ch ^ k_swz<DP>(r)) * 16;
+  };
+  auto fetch_one = [&](auto of_v, int x) W4_INLINE {  // load x of a plain tile
+    constexpr bool V = decltype(of_v)::value;
+    const uint32_t off = lane_row + chunk(of_v, RW * wave + x * RPI + lane / CH, lane);
+    const char* row0 = from[V] + x * step_bytes;
+    if constexpr (FP8)
+      held[V][x] = *reinterpret_cast<const u32x4*>(row0 + off);
+    else
+      dma16(row0, off, to[V] + x * 1024);
+  };
+  // Makes tile i ready for fetch_one(0 .. NI - 1), or fetches it whole and says false.
+  auto ready = [&](int i, auto of_v) W4_INLINE {
+    constexpr bool V = decltype(of_v)::value;
+    const uint32_t st = lds_at + (V ? v_tile(i) : k_tile(i)) + wave * (TILE / NW);
+    const int jt = k0 + tile_at(i) * KT, jw = jt + RW * wave;
+    if (plain && jt + KT <= k1) {
+      const int id = __builtin_amdgcn_readfirstlane(ids[(i & 3) * 64]);
+      if ((uint32_t)id < (uint32_t)g.c.pages) {
+        from[V] = bases[V] + (id * g.c.stride_page + (jw - divide(jw, p.page) * g.c.page_size) * g.c.stride_token) * ES;
+        to[V] = st;
+        return true;
       }
     }
-    for (; i < tiles; ++i) {
-      if (turn(i)) {
 #pragma unroll
-        for (int e = 0; e < NI; ++e) fetch_one(e);
-      }
-      if (live) compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{}, [](int) {});
+    for (int x = 0; x < NI; ++x) {
+      const int rw = x * RPI + lane / CH, at_chunk = chunk(of_v, RW * wave + rw, lane);
+      const int j = jw + rw, page = divide(j, p.page), id = ids[(i & 3) * 64 + rw];
+      const int64_t at = (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES;
+      const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+      const void* src = in && !good && !V                 ? (const void*)(FP8 ? kNans8 : kNans)
+                        : in && good && at_chunk < D * ES ? (const void*)(bases[V] + at + at_chunk)
+                                                          : (const void*)kZeros;
+      if constexpr (FP8)
+        held[V][x] = *reinterpret_cast<const u32x4*>(src);
+      else
+        dma16(src, st + x * 1024);
     }
-  } else {
-    constexpr int CH = DP / 16, RPI = 64 / CH, NI = (RW + RPI - 1) / RPI;
-    const uint8_t* kbase = reinterpret_cast<const uint8_t*>(g.c.k) + kvh * g.c.stride_head;
-    const uint8_t* vbase = reinterpret_cast<const uint8_t*>(g.c.v) + kvh * g.c.stride_head;
-    static_assert(RW % RPI == 0, "whole rows of a load");
-    u32x4 kr[NI], vr[NI];
-    auto page_id = [&](int t) { return table[divide(min(k0 + tile_at(t) * KT + RW * wave + lane % RW, k1 - 1), p.page)]; };
-    auto load = [&](int t, int ids) {
+    return false;
+  };
+  // e4m3: what fetch() holds of tile i, widened, to LDS
+  auto land = [&](int i, auto of_v) W4_INLINE {
+    constexpr bool V = decltype(of_v)::value;
+    unsigned char* st = lds + ((V ? 2 : 0) + (i & 1)) * TILE;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int rw = i * RPI + lane / CH, d = lane % CH * 16;
-        const int j = k0 + tile_at(t) * KT + RW * wave + rw, page = divide(j, p.page), id = __shfl(ids, rw);
-        const int64_t at = id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token + d;
-        const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
-        const uint32_t fill = in && !good ? 0x7f7f7f7fu : 0u;
-        kr[i] = {fill, fill, fill, fill};
-        vr[i] = {0, 0, 0, 0};
-        if (in && good && d < D) {
-          kr[i] = *reinterpret_cast<const u32x4*>(kbase + at);
-          vr[i] = *reinterpret_cast<const u32x4*>(vbase + at);
-        }
-      }
-    };
-    auto store = [&](unsigned char* st) {
+    for (int x = 0; x < NI; ++x) {
+      const int r = RW * wave + x * RPI + lane / CH, ch = lane % CH * 2;
+      const int swz = V ? v_swz<DP>(r) : k_swz<DP>(r);
+      f16x8 y[2];
+      widen(held[V][x], y);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = RW * wave + i * RPI + lane / CH, ch = lane % CH * 2;
-        f16x8 x[2];
-        widen(kr[i], x);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<f16x8*>(st + r * DP * 2 + ((ch + e) ^ k_swz<DP>(r)) * 16) = x[e];
-        widen(vr[i], x);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<f16x8*>(st + TILE + r * DP * 2 + ((ch + e) ^ v_swz<DP>(r)) * 16) = x[e];
-      }
-    };
-    int ids = 0;
-    if (tiles > 0) {
-      load(0, page_id(0));
-      if (tiles > 1) ids = page_id(1);
-      store(lds);
+      for (int e = 0; e < 2; ++e) *reinterpret_cast<f16x8*>(st + r * DP * 2 + ((ch + e) ^ swz) * 16) = y[e];
     }
-    auto turn = [&](int i) {
-      __syncthreads();
-      if (i + 1 < tiles) {
-        load(i + 1, ids);
-        if (i + 2 < tiles) ids = page_id(i + 2);
+  };
+  constexpr std::false_type K_{};
+  constexpr std::true_type V_{};
+  // every wave's part of what was fetched is there, and what was read before has been read
+  auto meet = [&]() { asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
+  int held_k = -1, held_v = -1;  // e4m3: the tiles in `held`
+  auto put_down = [&]() W4_INLINE {
+    if constexpr (FP8) {
+      if (held_k >= 0) land(held_k, K_);
+      if (held_v >= 0) land(held_v, V_);
+      held_k = held_v = -1;
+    }
+  };
+  auto start_k = [&](int i) W4_INLINE {  // says whether fetch_one is to do the rest
+    if (i >= tiles) return false;
+    held_k = i;
+    return ready(i, K_);
+  };
+  auto start_v = [&](int i) W4_INLINE {
+    if (i >= tiles) return false;
+    held_v = i;
+    return ready(i, V_);
+  };
+  auto get_k = [&](int i) W4_INLINE {
+    if (start_k(i)) {
+#pragma unroll
+      for (int x = 0; x < NI; ++x) fetch_one(K_, x);
+    }
+  };
+  auto get_v = [&](int i) W4_INLINE {
+    if (start_v(i)) {
+#pragma unroll
+      for (int x = 0; x < NI; ++x) fetch_one(V_, x);
+    }
+  };
+  // Between the block that reads K of tile t last and the one that reads K of t + 1: K of t is not read any
+  // more, nor V of t + SUB - 3, so K of t + 2 and V of t + SUB - 1 may follow, all of them now, or the plain ones
+  // behind the slices of the next block(s).  (Issued together, the waves' DMA queues up for the memory path
+  // while the matrix cores idle.)
+  bool more_k = false, more_v = false;
+  auto turn = [&](int t) W4_INLINE {
+    put_down();
+    meet();
+    fetch_ids(t + 3);
+    more_k = start_k(t + 2);
+    more_v = start_v(t + SUB - 1);
+  };
+  constexpr int PER = (NI + DB - 1) / DB;  // loads behind a slice
+  auto rest_k = [&](int x) W4_INLINE {
+    if (more_k) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (x * PER + e < NI) fetch_one(K_, x * PER + e);
+    }
+  };
+  auto rest_v = [&](int x) W4_INLINE {
+    if (more_v) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e)
+        if (x * PER + e < NI) fetch_one(V_, x * PER + e);
+    }
+  };
+  auto rest_kv = [&](int x) W4_INLINE { rest_k(x), rest_v(x); };
+  auto none = [](int) {};
+  auto turn_whole = [&](int t) W4_INLINE {
+    turn(t);
+#pragma unroll
+    for (int x = 0; x < DB; ++x) rest_kv(x);
+  };
+  if (tiles > 0) {
+    fetch_ids(0), fetch_ids(1), fetch_ids(2);
+    wait_vm<0>();
+    get_k(0);
+    if constexpr (SUB == 2) get_v(0);
+    put_down();
+    get_k(1);
+  }
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  if (live && full > 0) {
+    if constexpr (FP8) put_down();
+    meet();  // K of tile 0 (and 1)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sc[e] = 0.f;
+#pragma unroll
+    for (int st = 0; st < STEPS; ++st)
+      sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_frag(k_tile(0), st), q[st], sc, 0, 0, 0);
+    if constexpr (SUB == 2) {
+      block(yes, no, k_tile(0) + HALF, 0, none);
+      // two tiles a round, so that LDS addresses are a lane's base and a constant
+      auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
+        turn(t);
+        block(yes, yes, kt, vt, rest_k);
+        block(yes, yes, kt + HALF, vt + HALF, rest_v);
+      };
+      int t = 0;
+      for (; t + 2 < full; t += 2) {
+        step(t, TILE, 2 * TILE);
+        step(t + 1, 0, 3 * TILE);
       }
-    };
-    auto land = [&](int i) {
-      if (i + 1 < tiles) store(lds + ((i + 1) & 1) * 2 * TILE);
-    };
-    int i = 0;
-    if (!live) {
-      for (; i < tiles; ++i) turn(i), land(i);
+      if (t + 1 < full) step(t, TILE, 2 * TILE);
+      turn_whole(full - 1);
+      block(no, yes, 0, v_tile(full - 1), none);
     } else {
-      for (; i < full; ++i) {
-        turn(i);
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::false_type{}, [](int) {});
-        land(i);
+      turn_whole(0);
+      if (full == 1) {
+        block(no, no, 0, 0, none);
+      } else {
+        block(yes, no, k_tile(1), 0, none);
+        auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
+          turn(t);
+          block(yes, yes, kt, vt, rest_kv);
+        };
+        int t = 1;
+        for (; t + 2 < full; t += 2) {
+          step(t, 0, 2 * TILE);
+          step(t + 1, TILE, 3 * TILE);
+        }
+        if (t + 1 < full) step(t, 0, 2 * TILE);
+        turn_whole(full - 1);
+        block(no, yes, 0, v_tile(full - 2), none);
       }
-      for (; i < tiles; ++i) {
-        turn(i);
-        compute(tile_at(i), lds_at + (i & 1) * 2 * TILE, std::true_type{}, [](int) {});
-        land(i);
-      }
+      put_down();
+      meet();  // V of the last
     }
+#pragma unroll
+    for (int x = 0; x < 2 * DB; ++x)
+      acc[x / 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v_frag(v_tile(full - 1) + (SUB - 1) * HALF, x), w[x & 1],
+                                                         acc[x / 2], 0, 0, 0);
+  } else if (full > 0) {  // a wave of no rows: the same barriers and fetches
+    put_down();
+    meet();
+    for (int t = 0; t < full; ++t) turn_whole(t);
+    put_down();
+    if constexpr (SUB == 1) meet();
+  }
+  // fetched so far: K to tile full + 1 (1 when full is 0), V to full + SUB - 2
+  for (int i = full; i < tiles; ++i) {
+    if (SUB == 1 && i == full) get_v(i);
+    put_down();
+    meet();
+    if (i > full) get_k(i + 1);
+    get_v(i + 1);
+    fetch_ids(i + 2);
+    if (live) edge(i);
   }
 
   // acc[i][e]: dim 32 i + 8 (e / 4) + 4 h + e % 4 of this lane's row
