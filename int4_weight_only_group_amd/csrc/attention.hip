@@ -907,21 +907,39 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   };
 
   // ---- fetching: this wave's RW rows of a tile
-  const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);  // 4 tiles' page numbers
-  const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
-  auto fetch_ids = [&](int i) W4_INLINE {
-    const int j = min(k0 + tile_at(i) * KT + RW * wave + lane % RW, k1 - 1);
-    dma4(table + divide(j, p.page), ids_at + (i & 3) * 256);
-  };
   constexpr int ES = FP8 ? 1 : 2, CH = DP * ES / 16, RPI = 64 / CH, NI = RW / RPI;  // chunks of a row; rows and count of a load
   static_assert(RW % RPI == 0, "whole rows of a load");
   const char* bases[2] = {reinterpret_cast<const char*>(g.c.k) + kvh * g.c.stride_head * ES,
                           reinterpret_cast<const char*>(g.c.v) + kvh * g.c.stride_head * ES};
-  // A whole tile of whole pages: this wave's rows lie in one page, whose address is scalar; a lane adds
-  // its row and chunk.  (Per-lane addresses cost more VALU work than the softmax.)
+  // Pages of whole RW rows (and no padded dims): this wave's rows of a tile lie in one page, so their offset
+  // from the base is scalar and a lane adds its row and chunk.  64 tiles' offsets are computed at once, one
+  // per lane; the turn between two tiles then takes two lane reads.  (Scalar address arithmetic at every
+  // turn, and per-lane addresses the more so, cost more issue slots than the softmax.)
   const bool plain = D == DP && g.c.page_size % RW == 0 && g.c.stride_token < (1 << 20);
   const uint32_t lane_row = (uint32_t)(lane / CH) * (uint32_t)g.c.stride_token * ES;
   const int64_t step_bytes = (int64_t)RPI * g.c.stride_token * ES;  // between the rows of two loads
+  int64_t offsets = 0;  // lane i: of tile batch + i; -1: a page outside the cache
+  int batch = -64;
+  auto offset_of = [&](int i) W4_INLINE {
+    if ((i & ~63) != batch) {
+      batch = i & ~63;
+      const int jw = k0 + tile_at(batch + lane) * KT + RW * wave, j = min(jw, k1 - 1);
+      const int page = divide(j, p.page), id = table[page];
+      offsets = (uint32_t)id < (uint32_t)g.c.pages
+                    ? (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES
+                    : -1;
+    }
+    return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(offsets >> 32), i & 63) << 32 |
+                     (uint32_t)__builtin_amdgcn_readlane((int)offsets, i & 63));
+  };
+  // any other page size: page numbers of a tile's rows, through LDS, four tiles of them
+  const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);
+  const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
+  auto fetch_ids = [&](int i) W4_INLINE {
+    if (plain) return;
+    const int j = min(k0 + tile_at(i) * KT + RW * wave + lane % RW, k1 - 1);
+    dma4(table + divide(j, p.page), ids_at + (i & 3) * 256);
+  };
   u32x4 held[2][NI];  // e4m3: tiles on their way to LDS
   const char* from[2] = {nullptr, nullptr};  // this wave's rows of the plain K and V tiles that ready() found, and where
   uint32_t to[2] = {0, 0};                   // they go
@@ -939,25 +957,27 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     else
       dma16(row0, off, to[V] + x * 1024);
   };
-  // Makes tile i ready for fetch_one(0 .. NI - 1), or fetches it whole and says false.
-  auto ready = [&](int i, auto of_v) W4_INLINE {
+  // Makes tile i, `off` from the base if plain, ready for fetch_one(0 .. NI - 1), or fetches it whole and says false.
+  auto ready = [&](int i, auto of_v, int64_t off) W4_INLINE {
     constexpr bool V = decltype(of_v)::value;
     const uint32_t st = lds_at + (V ? v_tile(i) : k_tile(i)) + wave * (TILE / NW);
     const int jt = k0 + tile_at(i) * KT, jw = jt + RW * wave;
-    if (plain && jt + KT <= k1) {
-      const int id = __builtin_amdgcn_readfirstlane(ids[(i & 3) * 64]);
-      if ((uint32_t)id < (uint32_t)g.c.pages) {
-        from[V] = bases[V] + (id * g.c.stride_page + (jw - divide(jw, p.page) * g.c.page_size) * g.c.stride_token) * ES;
-        to[V] = st;
-        return true;
-      }
+    if (plain && off >= 0 && jt + KT <= k1) {
+      from[V] = bases[V] + off;
+      to[V] = st;
+      return true;
     }
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
-      const int rw = x * RPI + lane / CH, at_chunk = chunk(of_v, RW * wave + rw, lane);
-      const int j = jw + rw, page = divide(j, p.page), id = ids[(i & 3) * 64 + rw];
-      const int64_t at = (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES;
-      const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
+      const int rw = x * RPI + lane / CH, at_chunk = chunk(of_v, RW * wave + rw, lane), j = jw + rw;
+      int64_t at = off + (int64_t)rw * g.c.stride_token * ES;
+      bool good = off >= 0;
+      if (!plain) {
+        const int page = divide(j, p.page), id = ids[(i & 3) * 64 + rw];
+        at = (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES;
+        good = (uint32_t)id < (uint32_t)g.c.pages;
+      }
+      const bool in = j < k1;
       const void* src = in && !good && !V                 ? (const void*)(FP8 ? kNans8 : kNans)
                         : in && good && at_chunk < D * ES ? (const void*)(bases[V] + at + at_chunk)
                                                           : (const void*)kZeros;
@@ -994,24 +1014,24 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       held_k = held_v = -1;
     }
   };
-  auto start_k = [&](int i) W4_INLINE {  // says whether fetch_one is to do the rest
+  auto start_k = [&](int i, int64_t off) W4_INLINE {  // says whether fetch_one is to do the rest
     if (i >= tiles) return false;
     held_k = i;
-    return ready(i, K_);
+    return ready(i, K_, off);
   };
-  auto start_v = [&](int i) W4_INLINE {
+  auto start_v = [&](int i, int64_t off) W4_INLINE {
     if (i >= tiles) return false;
     held_v = i;
-    return ready(i, V_);
+    return ready(i, V_, off);
   };
   auto get_k = [&](int i) W4_INLINE {
-    if (start_k(i)) {
+    if (start_k(i, plain ? offset_of(i) : 0)) {
 #pragma unroll
       for (int x = 0; x < NI; ++x) fetch_one(K_, x);
     }
   };
   auto get_v = [&](int i) W4_INLINE {
-    if (start_v(i)) {
+    if (start_v(i, plain ? offset_of(i) : 0)) {
 #pragma unroll
       for (int x = 0; x < NI; ++x) fetch_one(V_, x);
     }
@@ -1021,12 +1041,16 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   // behind the slices of the next block(s).  (Issued together, the waves' DMA queues up for the memory path
   // while the matrix cores idle.)
   bool more_k = false, more_v = false;
+  int64_t off_v[2] = {0, 0};  // offsets of V tiles t + SUB - 1 and (SUB = 1) t + 1
   auto turn = [&](int t) W4_INLINE {
     put_down();
     meet();
     fetch_ids(t + 3);
-    more_k = start_k(t + 2);
-    more_v = start_v(t + SUB - 1);
+    const int64_t off = plain ? offset_of(t + 2) : 0;
+    more_k = start_k(t + 2, off);
+    more_v = start_v(t + SUB - 1, off_v[0]);
+    if constexpr (SUB == 1) off_v[0] = off_v[1];
+    off_v[SUB == 1] = off;
   };
   constexpr int PER = (NI + DB - 1) / DB;  // loads behind a slice
   auto rest_k = [&](int x) W4_INLINE {
@@ -1057,6 +1081,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     if constexpr (SUB == 2) get_v(0);
     put_down();
     get_k(1);
+    if (plain) off_v[0] = offset_of(SUB - 1), off_v[1] = offset_of(1);
   }
   constexpr std::true_type yes{};
   constexpr std::false_type no{};
