@@ -759,21 +759,42 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   auto tile_at = [&](int i) { return i < full ? f0 + i : i - full < f0 ? i - full : i; };
 
   // The loop over whole tiles goes by 32 keys and is pipelined: while the softmax of block u runs on the VALU,
-  // the matrix cores compute the scores of block u + 1 and the weighted sums of block u - 1.  `sc` are
-  // u's scores, `w` the weights of u - 1 (scaled by the m of then: when u moves m, the sums are rescaled
-  // after the products of u - 1).  Slices of four products carry their share of the VALU work, fragments
-  // are read a slice ahead, and between(x) follows slice x.  l sums the weights as rounded, which are the ones that
-  // multiply v.
+  // the matrix cores compute the scores of block u + 1, then the weighted sums of block u - 1.  `sc` are
+  // u's scores and `top` their largest of this lane, `w` the weights of u - 1 (scaled by the m of then: when u moves m,
+  // the sums are rescaled after the products of u - 1).  Slices of four products carry their share of
+  // the VALU work, fragments are read two slices ahead, and between(x) follows slice x.  l sums the
+  // weights as rounded, which are the ones that multiply v.
   f32x16 sc;
   f16x8 w[2];
-  float ms = 0.f;  // m, or 0 before there is one
-  auto block = [&](auto with_qk, auto with_pv, uint32_t k_next, uint32_t v_last, auto between) W4_INLINE {
+  float ms = 0.f, top = 0.f;  // ms: m, or 0 before there is one
+  auto top_of = [&](const f32x16& x) W4_INLINE {
+    float y[6];
+#pragma unroll
+    for (int e = 0; e < 5; ++e) y[e] = fmaxf(fmaxf(x[3 * e], x[3 * e + 1]), x[3 * e + 2]);
+    y[0] = fmaxf(fmaxf(y[0], y[1]), x[15]);
+    y[2] = fmaxf(fmaxf(y[2], y[3]), y[4]);
+    return fmaxf(y[0], y[2]) * c;
+  };
+  constexpr int SLICES = STEPS / 2, EACH = 16 / SLICES;
+  f16x8 frags[3][4];  // of three slices in turn
+  // of: which of two blocks whose tiles follow each other in LDS this is: 0 reads ahead into 1; -1: alone
+  auto block = [&](auto with_qk, auto with_pv, uint32_t k_next, uint32_t v_last, auto between, auto of) W4_INLINE {
     constexpr bool QK = decltype(with_qk)::value, PV = decltype(with_pv)::value;
-    constexpr int SLICES = STEPS / 2, EACH = 16 / SLICES;
+    constexpr int OF = decltype(of)::value, FROM = OF == 1 ? SLICES : 0;
+    auto read = [&](int x) W4_INLINE {  // the fragments of slice x; past the last: of the block that follows
+      const uint32_t on = x / SLICES * HALF;
+      const int y = x % SLICES;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (QK)
+          if (y < SLICES / 2) frags[(FROM + x) % 3][e] = k_frag(k_next + on, 4 * y + e);
+        if constexpr (PV)
+          if (y >= SLICES / 2) frags[(FROM + x) % 3][e] = v_frag(v_last + on, 4 * (y - SLICES / 2) + e);
+      }
+    };
     f32x16 next;
-    f16x8 kf[2][2], vf[2][2];
     u32x4 nw[2];
-    float y[16];
+    float y[16], f = 1.f;
     auto round_to = [&](int x) W4_INLINE {  // slice x's weights to f16, a slice after their exponentials
 #pragma unroll
       for (int e = EACH * x; e < EACH * (x + 1); e += 2) {
@@ -783,21 +804,10 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     };
 #pragma unroll
     for (int e = 0; e < 16; ++e) next[e] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if constexpr (QK) kf[0][e] = k_frag(k_next, e);
-      if constexpr (PV) vf[0][e] = v_frag(v_last, e);
-    }
-    float top[6];
-#pragma unroll
-    for (int e = 0; e < 5; ++e) top[e] = fmaxf(fmaxf(sc[3 * e], sc[3 * e + 1]), sc[3 * e + 2]);
-    top[0] = fmaxf(fmaxf(top[0], top[1]), sc[15]);
-    top[2] = fmaxf(fmaxf(top[2], top[3]), top[4]);
-    top[0] = fmaxf(top[0], top[2]) * c;
-    const bool move = __any(top[0] > m + kSlack);
-    float f = 1.f;
+    if constexpr (OF != 1) read(0), read(1);
+    const bool move = __any(top > m + kSlack);
     if (move) {
-      const float mn = fmaxf(m, across<false>(top[0], fmax2));
+      const float mn = fmaxf(m, across<false>(top, fmax2));
       f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
       m = mn;
       ms = m == -INFINITY ? 0.f : m;
@@ -805,17 +815,15 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     }
 #pragma unroll
     for (int x = 0; x < SLICES; ++x) {
-      if (x + 1 < SLICES) {
+      if (x + 2 < SLICES || OF == 0) read(x + 2);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if constexpr (QK) kf[(x + 1) & 1][e] = k_frag(k_next, 2 * (x + 1) + e);
-          if constexpr (PV) vf[(x + 1) & 1][e] = v_frag(v_last, 2 * (x + 1) + e);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if constexpr (QK) next = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf[x & 1][e], q[2 * x + e], next, 0, 0, 0);
-        if constexpr (PV) acc[x] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf[x & 1][e], w[e], acc[x], 0, 0, 0);
+      for (int e = 0; e < 4; ++e) {
+        const int z = 4 * (x % (SLICES / 2)) + e;
+        const f16x8& fr = frags[(FROM + x) % 3][e];
+        if constexpr (QK)
+          if (x < SLICES / 2) next = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr, q[z], next, 0, 0, 0);
+        if constexpr (PV)
+          if (x >= SLICES / 2) acc[z / 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fr, w[z & 1], acc[z / 2], 0, 0, 0);
       }
       if (x > 0) round_to(x - 1);
 #pragma unroll
@@ -823,8 +831,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
         y[e] = __builtin_amdgcn_exp2f(sc[e] * c - ms);
         asm volatile("" : "+v"(y[e]));  // in this slice: the compiler would move it behind the last branch
       }
+      if constexpr (QK)
+        if (x == SLICES - 1) {
+          top = top_of(next);
+          asm volatile("" : "+v"(top));
+        }
 #pragma unroll
-      for (int e = 0; e < 2 * (QK + PV); ++e) {
+      for (int e = 0; e < 4; ++e) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // a product
         __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);  // LDS reads
         __builtin_amdgcn_sched_group_barrier(0x402, EACH + 1, 0);  // VALU work
@@ -861,7 +874,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
 #pragma unroll
       for (int st = 0; st < STEPS; ++st)
         sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_frag(kt, st), q[st], sc, 0, 0, 0);
-      float top = -INFINITY;
+      top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 16; ++e) {  // key j0 + 8 (e / 4) + 4 h + e % 4 of this lane's row
         const int j = j0 + 8 * (e >> 2) + 4 * h + (e & 3);
@@ -1085,6 +1098,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   }
   constexpr std::true_type yes{};
   constexpr std::false_type no{};
+  constexpr std::integral_constant<int, -1> alone{};
   if (live && full > 0) {
     if constexpr (FP8) put_down();
     meet();  // K of tile 0 (and 1)
@@ -1093,13 +1107,14 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
 #pragma unroll
     for (int st = 0; st < STEPS; ++st)
       sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_frag(k_tile(0), st), q[st], sc, 0, 0, 0);
+    top = top_of(sc);
     if constexpr (SUB == 2) {
-      block(yes, no, k_tile(0) + HALF, 0, none);
+      block(yes, no, k_tile(0) + HALF, 0, none, alone);
       // two tiles a round, so that LDS addresses are a lane's base and a constant
       auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
         turn(t);
-        block(yes, yes, kt, vt, rest_k);
-        block(yes, yes, kt + HALF, vt + HALF, rest_v);
+        block(yes, yes, kt, vt, rest_k, std::integral_constant<int, 0>{});
+        block(yes, yes, kt + HALF, vt + HALF, rest_v, std::integral_constant<int, 1>{});
       };
       int t = 0;
       for (; t + 2 < full; t += 2) {
@@ -1108,16 +1123,16 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       }
       if (t + 1 < full) step(t, TILE, 2 * TILE);
       turn_whole(full - 1);
-      block(no, yes, 0, v_tile(full - 1), none);
+      block(no, yes, 0, v_tile(full - 1), none, alone);
     } else {
       turn_whole(0);
       if (full == 1) {
-        block(no, no, 0, 0, none);
+        block(no, no, 0, 0, none, alone);
       } else {
-        block(yes, no, k_tile(1), 0, none);
+        block(yes, no, k_tile(1), 0, none, alone);
         auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
           turn(t);
-          block(yes, yes, kt, vt, rest_kv);
+          block(yes, yes, kt, vt, rest_kv, alone);
         };
         int t = 1;
         for (; t + 2 < full; t += 2) {
@@ -1126,7 +1141,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
         }
         if (t + 1 < full) step(t, 0, 2 * TILE);
         turn_whole(full - 1);
-        block(no, yes, 0, v_tile(full - 2), none);
+        block(no, yes, 0, v_tile(full - 2), none, alone);
       }
       put_down();
       meet();  // V of the last
