@@ -26,7 +26,7 @@ __all__ = [
     "rope_frequencies", "rope_f16", "kv_append_rope", "attention_paged", "attention_workspace_bytes",
 ]
 
-W4_OK = 0
+W4_OK, W4_ERR_WORKSPACE = 0, -4
 
 
 class W4Error(RuntimeError):
@@ -46,6 +46,9 @@ def _check(fn: str, status: int) -> None:
 
 def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # of a device, as an address
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype) -> None:
@@ -486,11 +489,18 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
     return freq.float().to(device), mscale
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> int:
+# These calls run once or twice per layer and token, so their checks are kept short: _need() looks at a
+# tensor once and leaves the wording of a refusal to _dev().
+
+
+def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _dev(t, name, dtype)
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
     """Elements between the tokens of a [tokens][heads][dim] tensor with contiguous heads."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    _dev(t, name, t.dtype if dtype is None else dtype)
+    _need(t, name, dtype, dev)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens][heads][dim]")
     n, h, d = t.shape
@@ -500,48 +510,55 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> int:
     return s0 if n > 1 else max(s0, h * d)
 
 
-def _row_type(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.float32:
-        return _F32
-    if t.dtype == torch.float16:
-        return _F16
-    raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+def _row_dtype(t: torch.Tensor, name: str) -> torch.dtype:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.float32, torch.float16):
+        raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
+    return t.dtype
 
 
-def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int) -> int:
-    _dev(t, name, dtype)
+def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
+    _need(t, name, dtype, dev)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and hold {n} elements")
     return t.data_ptr()
 
 
-def _kv_cache(k_cache, v_cache, k_scale, v_scale) -> KvCache:
-    _dev(k_cache, "k_cache", k_cache.dtype if isinstance(k_cache, torch.Tensor) else torch.float16)
-    _dev(v_cache, "v_cache", k_cache.dtype)
-    if k_cache.dtype == torch.float16:
+def _freq(t: torch.Tensor, dev: int) -> tuple[int | None, int]:
+    """(address, dims that it rotates) of a vector of frequencies"""
+    _need(t, "freq", torch.float32, dev)
+    if not t.is_contiguous():
+        raise ValueError("freq must be contiguous")
+    n = t.numel()
+    return (t.data_ptr() if n else None), 2 * n
+
+
+def _kv_cache(k_cache, v_cache, k_scale, v_scale, dev: int) -> KvCache:
+    if not isinstance(k_cache, torch.Tensor):
+        raise TypeError("k_cache must be a torch.Tensor")
+    dtype = k_cache.dtype
+    if dtype is torch.float16:
         kind = _F16
         if k_scale is not None or v_scale is not None:
             raise ValueError("a float16 cache takes no scales")
-    elif k_cache.dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         kind = _E4M3
     else:
-        raise TypeError(f"the caches must be torch.float16 or torch.float8_e4m3fn, got {k_cache.dtype}")
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise TypeError(f"the caches must be torch.float16 or torch.float8_e4m3fn, got {dtype}")
+    _need(k_cache, "k_cache", dtype, dev)
+    _need(v_cache, "v_cache", dtype, dev)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must both be [pages][kv heads][page size][dim]")
-    shape, st = k_cache.shape, k_cache.stride()
-    stv = v_cache.stride()
-    if (st[3] != 1 and shape[3] > 1) or any(a != b and n > 1 for a, b, n in zip(st, stv, shape)):
+    st, stv = k_cache.stride(), v_cache.stride()
+    if (st[3] != 1 and shape[3] > 1) or (st != stv and any(a != b and n > 1 for a, b, n in zip(st, stv, shape))):
         raise ValueError("k_cache and v_cache must have the same strides and a contiguous dim")
-    c = KvCache()
-    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
-    if k_scale is not None:
-        c.k_scale = _vec(k_scale, "k_scale", torch.float32, shape[1])
-    if v_scale is not None:
-        c.v_scale = _vec(v_scale, "v_scale", torch.float32, shape[1])
-    c.pages, c.heads, c.page_size, c.dim = shape
-    c.stride_page, c.stride_head, c.stride_token = (s if n > 1 else 0 for s, n in zip(st, shape[:3]))
-    c.type = kind
-    return c
+    pages, heads, size, dim = shape
+    ks = None if k_scale is None else _vec(k_scale, "k_scale", torch.float32, heads, dev)
+    vs = None if v_scale is None else _vec(v_scale, "v_scale", torch.float32, heads, dev)
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, pages, size, heads, dim,
+                   st[0] if pages > 1 else 0, st[1] if heads > 1 else 0, st[2] if size > 1 else 0, kind)
 
 
 def rope_f16(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, interleaved: bool = False,
@@ -550,18 +567,21 @@ def rope_f16(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, in
     freq float32 [R/2] (see rope_frequencies) -> float16 [T][H][D] with the first R dims of every
     head rotated by positions * freq, times mscale.  Pairs are (i, i + R/2), or (2i, 2i + 1) if
     interleaved.  inverse rotates back: the gradient of the rotation.  out may be x (float16)."""
-    ldx = _rows(x, "x")
-    kind = _row_type(x, "x")
+    dev = torch.cuda.current_device()
+    dtype = _row_dtype(x, "x")
+    ldx = _rows(x, "x", dtype, dev)
     t, h, d = x.shape
     if out is None:
         out = torch.empty((t, h, d), dtype=torch.float16, device=x.device)
-    ldy = _rows(out, "out", torch.float16)
-    if out.shape != x.shape:
-        raise ValueError("out must have x's shape")
-    rot = 2 * freq.numel()
-    _check("rope_f16", lib().rope_f16(x.data_ptr(), kind, ldx, _vec(positions, "positions", torch.int32, t),
-                                      _vec(freq, "freq", torch.float32, rot // 2) if rot else None, out.data_ptr(),
-                                      ldy, t, h, d, rot, interleaved, inverse, mscale, _stream()))
+        ldy = h * d
+    else:
+        ldy = _rows(out, "out", torch.float16, dev)
+        if out.shape != x.shape:
+            raise ValueError("out must have x's shape")
+    f, rot = _freq(freq, dev)
+    _check("rope_f16", lib().rope_f16(x.data_ptr(), _F32 if dtype is torch.float32 else _F16, ldx,
+                                      _vec(positions, "positions", torch.int32, t, dev), f, out.data_ptr(), ldy, t, h,
+                                      d, rot, interleaved, inverse, mscale, _raw_stream(dev)))
     return out
 
 
@@ -577,32 +597,35 @@ def kv_append_rope(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     contiguous dim, float16 or float8_e4m3fn (value = code * scale[head], scales float32 [kv heads]);
     slots int64 [T] = page * page size + token of the page, distinct, -1: not written.
     Returns the rotated queries, float16 (None without q)."""
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    ldk = _rows(k, "k")
-    kind = _row_type(k, "k")
-    ldv = _rows(v, "v", k.dtype)
+    dev = torch.cuda.current_device()
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    dtype = _row_dtype(k, "k")
+    ldk, ldv = _rows(k, "k", dtype, dev), _rows(v, "v", dtype, dev)
     t, heads, d = k.shape
     if v.shape != k.shape or heads != c.heads or d != c.dim:
         raise ValueError("k and v must be [T][kv heads][dim] of the cache")
     ldq = ldqo = hq = 0
+    pq = pqo = None
     if q is not None:
-        ldq = _rows(q, "q", k.dtype)
-        hq = q.shape[1]
-        if q.shape[0] != t or q.shape[2] != d:
+        ldq = _rows(q, "q", dtype, dev)
+        n, hq, dq = q.shape
+        if n != t or dq != d:
             raise ValueError("q must be [T][heads][dim] with k's T and dim")
         if q_out is None:
             q_out = torch.empty((t, hq, d), dtype=torch.float16, device=q.device)
-        ldqo = _rows(q_out, "q_out", torch.float16)
-        if q_out.shape != q.shape:
-            raise ValueError("q_out must have q's shape")
+            ldqo = hq * d
+        else:
+            ldqo = _rows(q_out, "q_out", torch.float16, dev)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rot = 2 * freq.numel()
+    f, rot = _freq(freq, dev)
     _check("kv_append_rope", lib().kv_append_rope(
-        None if q is None else q.data_ptr(), ldq, None if q is None else q_out.data_ptr(), ldqo, hq, k.data_ptr(), ldk,
-        v.data_ptr(), ldv, kind, c, _vec(slots, "slots", torch.int64, t),
-        _vec(positions, "positions", torch.int32, t),
-        _vec(freq, "freq", torch.float32, rot // 2) if rot else None, t, rot, interleaved, mscale, _stream()))
+        pq, ldq, pqo, ldqo, hq, k.data_ptr(), ldk, v.data_ptr(), ldv, _F32 if dtype is torch.float32 else _F16, c,
+        _vec(slots, "slots", torch.int64, t, dev), _vec(positions, "positions", torch.int32, t, dev), f, t, rot,
+        interleaved, mscale, _raw_stream(dev)))
     return q_out
 
 
@@ -610,9 +633,9 @@ def attention_workspace_bytes(k_cache: torch.Tensor, b: int, t: int, max_q: int,
                               window: int = 0) -> int:
     """Workspace bytes attention_paged needs for t query rows of b sequences over this cache, with
     tables of pages_per_seq pages."""
-    c = _kv_cache(k_cache, k_cache, None, None)
+    c = _kv_cache(k_cache, k_cache, None, None, torch.cuda.current_device())
     need = ctypes.c_size_t(0)
-    p, ld = 16, heads * int(c.dim)
+    p, ld = 16, heads * c.dim
     _check("attention_paged", lib().attention_paged(p, ld, c, p, pages_per_seq, pages_per_seq, p, p, b, t, max_q,
                                                     heads, window, 1.0, p, ld, None, ctypes.byref(need), None))
     return int(need.value)
@@ -633,38 +656,43 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     decode: it chooses the kernel).  Returns float16 [T][heads][dim]; a row that sees no key is 0,
     rows past the last sequence are not written.  One is allocated for out and the workspace
     (attention_workspace_bytes) when not given or too small."""
-    c = _kv_cache(k_cache, v_cache, k_scale, v_scale)
-    ldq = _rows(q, "q", torch.float16)
+    dev = torch.cuda.current_device()
+    c = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    ldq = _rows(q, "q", torch.float16, dev)
     t, hq, d = q.shape
     if d != c.dim:
         raise ValueError("q must have the cache's dim")
     if out is None:
         out = torch.empty((t, hq, d), dtype=torch.float16, device=q.device)
-    ldo = _rows(out, "out", torch.float16)
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    _dev(table, "table", torch.int32)
+        ldo = hq * d
+    else:
+        ldo = _rows(out, "out", torch.float16, dev)
+        if out.shape != q.shape:
+            raise ValueError("out must have q's shape")
+    _need(table, "table", torch.int32, dev)
     ldt = _rowmajor(table, "table")
     b, width = table.shape
-    len_ptr = _vec(kv_len, "kv_len", torch.int32, b)
-    start_ptr = None
+    start = None
     if q_start is not None:
-        start_ptr = _vec(q_start, "q_start", torch.int32, b + 1)
+        start = _vec(q_start, "q_start", torch.int32, b + 1, dev)
         if max_q is None:
             max_q = t
     elif max_q is None:
         max_q = 1
     if scale is None:
         scale = d ** -0.5
-    args = (q.data_ptr(), ldq, c, table.data_ptr(), ldt, width, len_ptr, start_ptr, b, t, max_q, hq, window, scale,
-            out.data_ptr(), ldo)
-    size = ctypes.c_size_t(0)
-    fn = lib().attention_paged
-    _check("attention_paged", fn(*args, None, ctypes.byref(size), None))
-    ws_ptr = None
-    if size.value:
-        if workspace is None or workspace.numel() * workspace.element_size() < size.value:
-            workspace = torch.empty(size.value, dtype=torch.uint8, device=q.device)
-        ws_ptr = workspace.data_ptr()
-    _check("attention_paged", fn(*args, ws_ptr, ctypes.byref(size) if ws_ptr else None, _stream()))
+    args = (q.data_ptr(), ldq, c, table.data_ptr(), ldt, width, _vec(kv_len, "kv_len", torch.int32, b, dev), start, b,
+            t, max_q, hq, window, scale, out.data_ptr(), ldo)
+    fn, stream = lib().attention_paged, _raw_stream(dev)
+    status = W4_ERR_WORKSPACE
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the current device")
+        status = fn(*args, workspace.data_ptr(), ctypes.c_size_t(workspace.numel() * workspace.element_size()), stream)
+    if status == W4_ERR_WORKSPACE:
+        size = ctypes.c_size_t(0)
+        _check("attention_paged", fn(*args, None, size, None))
+        workspace = torch.empty(max(16, size.value), dtype=torch.uint8, device=q.device)
+        status = fn(*args, workspace.data_ptr(), size, stream)
+    _check("attention_paged", status)
     return out

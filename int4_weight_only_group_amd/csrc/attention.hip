@@ -1168,46 +1168,70 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     if (live) edge(i);
   }
 
-  // acc[i][e]: dim 32 i + 8 (e / 4) + 4 h + e % 4 of this lane's row
-  if (wr0 + (lane & 31) >= r1) return;
+  // The sums, acc[i][e]: dim 32 i + 8 (e / 4) + 4 h + e % 4 of this lane's row, go through LDS, 128 dims at a time, so
+  // that rows are written whole.  Four dims x of row r of the wave's 32 lie at x ^ r (mod what 128 dims hold).
   l = across<false>(l, add2);
-  float* sums = k.act > 1 ? part_row(p, (int64_t)slot * p.splits + split, kvh, row - r0) : nullptr;
+  constexpr int DW = DP < 128 ? DP : 128, XW = DW / 4;  // dims of a round, in fours
+  static_assert(4 * 32 * DW * 4 <= 4 * TILE, "the rows of four waves fit where the tiles were");
+  unsigned char* mine = lds + wave * 32 * DW * 4;
+  auto four_of = [&](int r, int x) W4_INLINE { return reinterpret_cast<f32x4*>(mine + r * DW * 4 + (x ^ (r % XW)) * 16); };
+  const int rows = live ? wr1 - wr0 : 0;
   const float f = l == 0.f ? 0.f : (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
-  uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D;
+  wait_vm<0>();     // no DMA is on its way to LDS any more
+  __syncthreads();  // the tiles have been read
 #pragma unroll
-  for (int i = 0; i < DB; ++i)
+  for (int d0 = 0; d0 < DP; d0 += DW) {
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const int d = 32 * i + 8 * a + 4 * h;
-      if (d >= D) break;
-      if (k.act > 1) {
+    for (int i = 0; i < DW / 32; ++i)
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
         f32x4 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = acc[i][4 * a + e];
-        *reinterpret_cast<f32x4*>(sums + d) = o;
-      } else {
-        f16x4 o;
+        for (int e = 0; e < 4; ++e) o[e] = acc[d0 / 32 + i][4 * a + e] * (k.act > 1 ? 1.f : f);
+        *four_of(lane & 31, 8 * i + 2 * a + h) = o;
+      }
+    wait_lds();
+    if (k.act > 1) {
+      for (int i = lane; i < rows * XW; i += 64) {
+        const int r = i / XW, x = i % XW;
+        if (d0 + 4 * x < D)
+          *reinterpret_cast<f32x4*>(part_row(p, (int64_t)slot * p.splits + split, kvh, wr0 - r0 + r) + d0 + 4 * x) = *four_of(r, x);
+      }
+    } else {
+      for (int i = lane; i < rows * XW / 2; i += 64) {
+        const int r = i / (XW / 2), x = i % (XW / 2) * 2, at = wr0 + r, tk = divide(at, p.group);
+        if (d0 + 4 * x < D) {
+          const f32x4 o0 = *four_of(r, x), o1 = *four_of(r, x + 1);
+          f16x8 o;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = (f16)(acc[i][4 * a + e] * f);
-        *reinterpret_cast<f16x4*>(out + d) = o;
+          for (int e = 0; e < 4; ++e) o[e] = (f16)o0[e], o[4 + e] = (f16)o1[e];
+          *reinterpret_cast<f16x8*>(g.out + (int64_t)(s.first + tk) * g.ldo + (int64_t)(kvh * p.G + at - tk * p.G) * D +
+                                    d0 + 4 * x) = o;
+        }
       }
     }
-  if (k.act > 1 && h == 0) sums[D] = m, sums[D + 1] = l;
+    wait_lds();
+  }
+  if (k.act > 1 && h == 0 && lane < rows) {
+    float* to_ml = part_row(p, (int64_t)slot * p.splits + split, kvh, wr0 - r0 + lane) + D;
+    to_ml[0] = m, to_ml[1] = l;
+  }
 }
 
 // ------------------------------------------------------------------------------- the parts
 // A row whose keys were in several parts: with M = max m, the sum of 2^(m_s - M) (sums_s, l_s).  Parts come
 // in batches, running as in the kernels above, so that a batch's loads are in flight together.  Bound:
 // latency (head, then the parts).  A workgroup of four waves takes one row, a quarter of the parts
-// each (WIDE), or four rows per wave.
+// each (WIDE), or a row per wave.
 template <bool FEW, bool WIDE, int EL>
 __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
-  constexpr int RW = WIDE ? 1 : 4, BATCH = WIDE ? 8 : 4;
-  __shared__ float sums[4][64 * EL];
+  typedef float vec __attribute__((ext_vector_type(EL)));
+  constexpr int BATCH = WIDE ? 8 : 4, STEP = WIDE ? 4 : 1;
+  __shared__ vec sums[4][64];
   __shared__ float mls[4][2];
   const AttnArgs& g = p.a;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, D = g.c.dim, d = lane * EL;
-  const int blocks = WIDE ? p.part_rows : (p.part_rows + 15) / 16;  // of an item
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), D = g.c.dim, d = lane * EL;
+  const int blocks = WIDE ? p.part_rows : (p.part_rows + 3) / 4;  // of an item
   const int item = blockIdx.x / blocks, in = blockIdx.x - item * blocks;
   const int kvh = item % g.c.heads;
   const int4 head = p.head[item / g.c.heads];
@@ -1217,66 +1241,62 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
   const Seq s = sequence(g, b);
   const int all_rows = s.n * p.G;
   if (FEW && (s.n == 0 || (p.skip_short && all_rows > kFewRows) || count <= 1)) return;
-  const int rows = min(all_rows - r0, p.part_rows);
-  for (int i = 0; i < RW; ++i) {
-    const int r = WIDE ? in : in * 16 + wave * RW + i;
-    if (r >= rows) return;
-    float o[EL] = {}, l = 0.f, m = -INFINITY;
-    for (int x0 = WIDE ? wave : 0; x0 < count; x0 += BATCH * (WIDE ? 4 : 1)) {
-      float om[BATCH], ol[BATCH], ov[BATCH][EL];
+  const int r = WIDE ? in : in * 4 + wave;
+  if (r >= min(all_rows - r0, p.part_rows)) return;  // whole workgroups if WIDE
+  vec o = 0.f;
+  float l = 0.f, m = -INFINITY;
+  for (int x0 = WIDE ? wave : 0; x0 < count; x0 += BATCH * STEP) {
+    float om[BATCH], ol[BATCH];
+    vec ov[BATCH];
 #pragma unroll
-      for (int y = 0; y < BATCH; ++y) {
-        const int x = x0 + y * (WIDE ? 4 : 1);
-        const float* from = part_row(p, first + min(x, count - 1), kvh, r);
-        om[y] = x < count ? from[D] : -INFINITY;
-        ol[y] = from[D + 1];
-#pragma unroll
-        for (int e = 0; e < EL; ++e) ov[y][e] = d < D ? from[d + e] : 0.f;
-      }
-      float top = m;
-#pragma unroll
-      for (int y = 0; y < BATCH; ++y) top = fmaxf(top, om[y]);
-      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
-      l *= f;
-#pragma unroll
-      for (int e = 0; e < EL; ++e) o[e] *= f;
-#pragma unroll
-      for (int y = 0; y < BATCH; ++y) {
-        const float fy = om[y] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(om[y] - top);
-        const bool there = x0 + y * (WIDE ? 4 : 1) < count;
-        l += there ? ol[y] * fy : 0.f;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) o[e] += there ? ov[y][e] * fy : 0.f;
-      }
-      m = top;
-    }
-    if constexpr (WIDE) {
-#pragma unroll
-      for (int e = 0; e < EL; ++e) sums[wave][d + e] = o[e];
-      if (lane == 0) mls[wave][0] = m, mls[wave][1] = l;
-      __syncthreads();
-      if (wave != 0) return;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) top = fmaxf(top, mls[w][0]);
-      l = 0.f;
-#pragma unroll
-      for (int e = 0; e < EL; ++e) o[e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float f = mls[w][0] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mls[w][0] - top);
-        l += mls[w][1] * f;
-#pragma unroll
-        for (int e = 0; e < EL; ++e) o[e] += sums[w][d + e] * f;
+    for (int y = 0; y < BATCH; ++y) {
+      const int x = x0 + y * STEP;
+      om[y] = -INFINITY, ol[y] = 0.f, ov[y] = 0.f;
+      if (x < count) {
+        const float* from = part_row(p, first + x, kvh, r);
+        om[y] = from[D], ol[y] = from[D + 1];
+        if (d < D) ov[y] = *reinterpret_cast<const vec*>(from + d);
       }
     }
-    if (d >= D) continue;
-    const int row = r0 + r, tok = divide(row, p.group);
-    const float f = l == 0.f ? 0.f : (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
-    uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
+    float top = m;
 #pragma unroll
-    for (int e = 0; e < EL; ++e) out[e] = __builtin_bit_cast(uint16_t, (f16)(o[e] * f));
+    for (int y = 0; y < BATCH; ++y) top = fmaxf(top, om[y]);
+    const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    l *= f, o *= f;
+#pragma unroll
+    for (int y = 0; y < BATCH; ++y) {
+      const float fy = om[y] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(om[y] - top);
+      // a part that saw none of the row's keys (m at -infinity) has l = 0 and sums of 0, or NaN from NaN keys
+      l += om[y] == -INFINITY ? ol[y] : ol[y] * fy;
+      o += om[y] == -INFINITY ? ov[y] : ov[y] * fy;
+    }
+    m = top;
   }
+  if constexpr (WIDE) {
+    sums[wave][lane] = o;
+    if (lane == 0) mls[wave][0] = m, mls[wave][1] = l;
+    __syncthreads();
+    if (wave != 0) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, mls[w][0]);
+    l = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float f = mls[w][0] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(mls[w][0] - top);
+      l += mls[w][1] * f;
+      o += sums[w][lane] * f;
+    }
+  }
+  if (d >= D) return;
+  const int row = r0 + r, tok = divide(row, p.group);
+  const float f = l == 0.f ? 0.f : (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+  uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
+  typedef uint16_t bits __attribute__((ext_vector_type(EL)));
+  bits h;
+#pragma unroll
+  for (int e = 0; e < EL; ++e) h[e] = __builtin_bit_cast(uint16_t, (f16)(o[e] * f));
+  *reinterpret_cast<bits*>(out) = h;
 }
 
 // ------------------------------------------------------------------------------- the launch
@@ -1291,7 +1311,6 @@ struct Launch {
 };
 
 constexpr int kCus = 256;
-constexpr int kWorkgroups = 512;  // of the kernel for many rows, about: two per CU
 
 // Workgroups of the decode kernel that a CU holds.
 int few_slots(const AttnArgs& a) {
@@ -1325,7 +1344,10 @@ Launch plan(const AttnArgs& a) {
     x.tiles = (int)((int64_t)a.T * G / kManyRows + std::min(a.B, a.T));
     const int64_t items = (int64_t)x.tiles * a.c.heads;
     const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kManyRows) : most;
-    x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (kWorkgroups + items - 1) / items));
+    // one round of the workgroups that the CUs hold (two of them, one at 256 dims, by their registers), where
+    // whole rows give less than two thirds of it: every part of a row costs its f32 sums once written and once read
+    const int64_t slots = kCus * (a.c.dim <= 128 ? 2 : 1);
+    x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (slots + items / 2) / items));
     if (x.many_splits > 1)
       x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)items * x.many_splits * kManyRows * row;
   }
@@ -1354,7 +1376,7 @@ void launch_many(const Plan& p, int items, hipStream_t st) {
 
 template <bool FEW, bool WIDE>
 void launch_join(const Plan& p, int items, hipStream_t st) {
-  const int D = p.a.c.dim, grid = items * (WIDE ? p.part_rows : (p.part_rows + 15) / 16);
+  const int D = p.a.c.dim, grid = items * (WIDE ? p.part_rows : (p.part_rows + 3) / 4);
   if (D <= 64)
     attention_join_kernel<FEW, WIDE, 1><<<grid, 256, 0, st>>>(p);
   else if (D <= 128)
