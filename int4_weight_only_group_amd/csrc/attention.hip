@@ -122,8 +122,8 @@ struct Plan {
   Divider page, group;
   int G;
   int splits;       // few rows: parts of the keys of all sequences, about; many rows: of a row tile, at most
-  int tiles, keys;  // many rows: row tiles at most, keys of a key tile
-  int part_rows;    // rows kept of a part
+  int tiles;        // many rows: row tiles at most
+  int part_rows;    // rows kept of a part; many rows: of a row tile
   bool skip_short;  // both kernels run: sequences of at most kFewRows rows are the first one's
   float c;          // scale * log2 e
   int4* head;       // of a sequence (few) or row tile (many): first part, parts, ...; see the kernels
@@ -624,18 +624,20 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
 }
 
 // ------------------------------------------------------------------------------ many rows
-// Chunks of prompts.  Bound: the matrix cores.  A workgroup takes 128 rows of a (sequence, kv head), 32 per
-// wave, and a part of their keys; the four waves share key tiles, double buffered in LDS: tile t + 1
-// is fetched while t is computed, one barrier per tile.
-constexpr int kManyRows = 128, kManyWaves = 4;
-template <int DP>
-constexpr int many_keys() { return DP == 256 ? 32 : 64; }
-template <int DP>
-constexpr int many_lds() { return 2 * 2 * many_keys<DP>() * DP * 2 + kManyWaves * 1024; }
+// Chunks of prompts.  Bound: the matrix cores.  A workgroup of four waves takes a tile of rows of a (sequence, kv
+// head), 32 per wave, and a part of their keys; K and V tiles are double buffered in LDS.  Either four row
+// blocks share the key tiles (KS = 1: 128 rows), or two do and two waves each take every other tile, their sums
+// being joined in LDS at the end (KS = 2: 64 rows; half the time per workgroup for twice as many, where
+// 128 rows leave CUs idle).
+constexpr int kManyWaves = 4;
+template <int DP, int KS>
+constexpr int many_keys() { return DP == 256 || KS == 2 ? 32 : 64; }  // of a key tile
+template <int DP, int KS>
+constexpr int many_lds() { return KS * 2 * 2 * many_keys<DP, KS>() * DP * 2 + kManyWaves * 1024; }
 
 __device__ __forceinline__ int tiles_of(const Plan& p, int n) {
   const int rows = n * p.G;
-  return p.skip_short && rows <= kFewRows ? 0 : (rows + kManyRows - 1) / kManyRows;
+  return p.skip_short && rows <= kFewRows ? 0 : (rows + p.part_rows - 1) / p.part_rows;
 }
 
 // The sequence and tile of the tile-th row tile of the batch; b = -1 past the last.  64 sequences at a
@@ -665,9 +667,10 @@ __device__ __forceinline__ void locate(const Plan& p, int tile, int& b, int& at)
   b = -1, at = 0;
 }
 
-template <int DP, bool FP8>
+template <int DP, bool FP8, int KS>
 __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_many_kernel(Plan p) {
-  constexpr int NW = kManyWaves, KT = many_keys<DP>(), TILE = KT * DP * 2, RW = KT / NW;
+  constexpr int NW = kManyWaves, RG = NW / KS, ROWS = 32 * RG;  // row blocks, rows
+  constexpr int KT = many_keys<DP, KS>(), TILE = KT * DP * 2, RW = KT / RG;  // RW: rows of a tile that a wave fetches
   constexpr int STEPS = DP / 16, DB = DP / 32, SUB = KT / 32;
   extern __shared__ __align__(16) unsigned char lds[];
   const AttnArgs& g = p.a;
@@ -682,8 +685,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     return;
   }
   const Seq s = sequence(g, b);
-  const int D = g.c.dim, all_rows = s.n * p.G, r0 = tile * kManyRows, r1 = min(all_rows, r0 + kManyRows);
-  const Keys k = keys_of(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT);
+  const int D = g.c.dim, all_rows = s.n * p.G, r0 = tile * ROWS, r1 = min(all_rows, r0 + ROWS);
+  const Keys k = keys_of(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT * KS);
   if (split >= k.act) return;
   if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {slot * p.splits, k.act, b, tile};
   const int k0 = k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
@@ -691,7 +694,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   const int32_t* table = g.table + (int64_t)b * g.ldt;
 
   // Q^T operand: lane (row = lane % 32, h = lane / 32), step t: dims 16 t + 8 h ..
-  const int h = lane >> 5, wr0 = r0 + 32 * wave, wr1 = min(r1, wr0 + 32);
+  const int rg = wave % RG, kg = wave / RG;  // row block; with KS = 2, which of every two key tiles
+  const int h = lane >> 5, wr0 = r0 + 32 * rg, wr1 = min(r1, wr0 + 32);
   const bool live = wr0 < r1;  // a wave of no rows helps to fetch
   const int row = min(wr0 + (lane & 31), r1 - 1), tok = divide(row, p.group);
   f16x8 q[STEPS];
@@ -716,10 +720,10 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
 
-  // LDS: two K tiles, two V tiles, the waves' page numbers.  Offsets of a lane's fragments within a tile:
+  // LDS: two K tiles, two V tiles (of each kg), the waves' page numbers.  Offsets of a lane's fragments within a tile:
   // the swizzles fold into the lane's part, up to the chunk bits that count steps (K) or dims blocks (V)
   // below 256 bytes.
-  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds;
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds + kg * 4 * TILE;
   auto k_tile = [](int i) { return (uint32_t)((i & 1) * TILE); };
   auto v_tile = [](int i) { return (uint32_t)((2 + (i & 1)) * TILE); };
   constexpr int HALF = 32 * DP * 2;  // bytes of 32 keys
@@ -747,16 +751,22 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
-  // ---- whole tiles: [f0, f0 + full) of this part are seen whole by all rows and come first, in a loop
-  // without masks; the tiles at the edges follow.  The i-th tile taken:
-  int f0 = 0, full;
+  // ---- whole tiles: [f0, f0 + whole) of this part are seen whole by all rows and come first, in a loop
+  // without masks; the tiles at the edges follow.
+  int f0 = 0, whole;
   {
     const int end = at0 + divide(r0, p.group), beg = g.window ? at0 + divide(r1 - 1, p.group) - g.window : 0;
     f0 = max(0, beg - k0 + KT - 1) / KT;
-    full = max(0, max(0, min(end, k1) - k0) / KT - f0);
-    if (full == 0) f0 = 0;
+    whole = max(0, max(0, min(end, k1) - k0) / KT - f0);
+    if (whole == 0) f0 = 0;
   }
-  auto tile_at = [&](int i) { return i < full ? f0 + i : i - full < f0 ? i - full : i; };
+  // in the order that they are taken; this wave takes kg, kg + KS, ...: `turns` of them, `full` in the first loop
+  auto tile_at = [&](int i) {
+    const int n = i * KS + kg;
+    return n < whole ? f0 + n : n - whole < f0 ? n - whole : n;
+  };
+  auto there = [&](int i) { return i * KS + kg < tiles; };
+  const int full = whole / KS, turns = (tiles + KS - 1) / KS;
 
   // The loop over whole tiles goes by 32 keys and is pipelined: while the softmax of block u runs on the VALU,
   // the matrix cores compute the scores of block u + 1, then the weighted sums of block u - 1.  `sc` are
@@ -936,7 +946,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   auto offset_of = [&](int i) W4_INLINE {
     if ((i & ~63) != batch) {
       batch = i & ~63;
-      const int jw = k0 + tile_at(batch + lane) * KT + RW * wave, j = min(jw, k1 - 1);
+      const int jw = k0 + tile_at(batch + lane) * KT + RW * rg, j = min(jw, k1 - 1);
       const int page = divide(j, p.page), id = table[page];
       offsets = (uint32_t)id < (uint32_t)g.c.pages
                     ? (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES
@@ -946,11 +956,11 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
                      (uint32_t)__builtin_amdgcn_readlane((int)offsets, i & 63));
   };
   // any other page size: page numbers of a tile's rows, through LDS, four tiles of them
-  const int* ids = reinterpret_cast<const int*>(lds + 4 * TILE + wave * 1024);
+  const int* ids = reinterpret_cast<const int*>(lds + KS * 4 * TILE + wave * 1024);
   const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
   auto fetch_ids = [&](int i) W4_INLINE {
     if (plain) return;
-    const int j = min(k0 + tile_at(i) * KT + RW * wave + lane % RW, k1 - 1);
+    const int j = min(k0 + tile_at(i) * KT + RW * rg + lane % RW, k1 - 1);
     dma4(table + divide(j, p.page), ids_at + (i & 3) * 256);
   };
   u32x4 held[2][NI];  // e4m3: tiles on their way to LDS
@@ -963,7 +973,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   };
   auto fetch_one = [&](auto of_v, int x) W4_INLINE {  // load x of a plain tile
     constexpr bool V = decltype(of_v)::value;
-    const uint32_t off = lane_row + chunk(of_v, RW * wave + x * RPI + lane / CH, lane);
+    const uint32_t off = lane_row + chunk(of_v, RW * rg + x * RPI + lane / CH, lane);
     const char* row0 = from[V] + x * step_bytes;
     if constexpr (FP8)
       held[V][x] = *reinterpret_cast<const u32x4*>(row0 + off);
@@ -973,8 +983,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   // Makes tile i, `off` from the base if plain, ready for fetch_one(0 .. NI - 1), or fetches it whole and says false.
   auto ready = [&](int i, auto of_v, int64_t off) W4_INLINE {
     constexpr bool V = decltype(of_v)::value;
-    const uint32_t st = lds_at + (V ? v_tile(i) : k_tile(i)) + wave * (TILE / NW);
-    const int jt = k0 + tile_at(i) * KT, jw = jt + RW * wave;
+    const uint32_t st = lds_at + (V ? v_tile(i) : k_tile(i)) + rg * (TILE / RG);
+    const int jt = k0 + tile_at(i) * KT, jw = jt + RW * rg;
     if (plain && off >= 0 && jt + KT <= k1) {
       from[V] = bases[V] + off;
       to[V] = st;
@@ -982,7 +992,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     }
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
-      const int rw = x * RPI + lane / CH, at_chunk = chunk(of_v, RW * wave + rw, lane), j = jw + rw;
+      const int rw = x * RPI + lane / CH, at_chunk = chunk(of_v, RW * rg + rw, lane), j = jw + rw;
       int64_t at = off + (int64_t)rw * g.c.stride_token * ES;
       bool good = off >= 0;
       if (!plain) {
@@ -1004,10 +1014,10 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   // e4m3: what fetch() holds of tile i, widened, to LDS
   auto land = [&](int i, auto of_v) W4_INLINE {
     constexpr bool V = decltype(of_v)::value;
-    unsigned char* st = lds + ((V ? 2 : 0) + (i & 1)) * TILE;
+    unsigned char* st = lds + (4 * kg + (V ? 2 : 0) + (i & 1)) * TILE;
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
-      const int r = RW * wave + x * RPI + lane / CH, ch = lane % CH * 2;
+      const int r = RW * rg + x * RPI + lane / CH, ch = lane % CH * 2;
       const int swz = V ? v_swz<DP>(r) : k_swz<DP>(r);
       f16x8 y[2];
       widen(held[V][x], y);
@@ -1028,12 +1038,12 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     }
   };
   auto start_k = [&](int i, int64_t off) W4_INLINE {  // says whether fetch_one is to do the rest
-    if (i >= tiles) return false;
+    if (!there(i)) return false;
     held_k = i;
     return ready(i, K_, off);
   };
   auto start_v = [&](int i, int64_t off) W4_INLINE {
-    if (i >= tiles) return false;
+    if (!there(i)) return false;
     held_v = i;
     return ready(i, V_, off);
   };
@@ -1065,7 +1075,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     if constexpr (SUB == 1) off_v[0] = off_v[1];
     off_v[SUB == 1] = off;
   };
-  constexpr int PER = (NI + DB - 1) / DB;  // loads behind a slice
+  constexpr int PER = (2 * NI + DB - 1) / DB;  // loads behind a slice
   auto rest_k = [&](int x) W4_INLINE {
     if (more_k) {
 #pragma unroll
@@ -1113,8 +1123,8 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
       // two tiles a round, so that LDS addresses are a lane's base and a constant
       auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
         turn(t);
-        block(yes, yes, kt, vt, rest_k, std::integral_constant<int, 0>{});
-        block(yes, yes, kt + HALF, vt + HALF, rest_v, std::integral_constant<int, 1>{});
+        block(yes, yes, kt, vt, rest_kv, std::integral_constant<int, 0>{});
+        block(yes, yes, kt + HALF, vt + HALF, none, std::integral_constant<int, 1>{});
       };
       int t = 0;
       for (; t + 2 < full; t += 2) {
@@ -1158,27 +1168,53 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     if constexpr (SUB == 1) meet();
   }
   // fetched so far: K to tile full + 1 (1 when full is 0), V to full + SUB - 2
-  for (int i = full; i < tiles; ++i) {
+  for (int i = full; i < turns; ++i) {
     if (SUB == 1 && i == full) get_v(i);
     put_down();
     meet();
     if (i > full) get_k(i + 1);
     get_v(i + 1);
     fetch_ids(i + 2);
-    if (live) edge(i);
+    if (live && there(i)) edge(i);
   }
 
   // The sums, acc[i][e]: dim 32 i + 8 (e / 4) + 4 h + e % 4 of this lane's row, go through LDS, 128 dims at a time, so
   // that rows are written whole.  Four dims x of row r of the wave's 32 lie at x ^ r (mod what 128 dims hold).
   l = across<false>(l, add2);
   constexpr int DW = DP < 128 ? DP : 128, XW = DW / 4;  // dims of a round, in fours
-  static_assert(4 * 32 * DW * 4 <= 4 * TILE, "the rows of four waves fit where the tiles were");
-  unsigned char* mine = lds + wave * 32 * DW * 4;
+  static_assert(ROWS * DW * 4 <= KS * 4 * TILE, "the rows fit where the tiles were");
+  unsigned char* mine = lds + rg * 32 * DW * 4;
   auto four_of = [&](int r, int x) W4_INLINE { return reinterpret_cast<f32x4*>(mine + r * DW * 4 + (x ^ (r % XW)) * 16); };
-  const int rows = live ? wr1 - wr0 : 0;
-  const float f = l == 0.f ? 0.f : (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+  const int rows = live && kg == 0 ? wr1 - wr0 : 0;
   wait_vm<0>();     // no DMA is on its way to LDS any more
   __syncthreads();  // the tiles have been read
+  if constexpr (KS == 2) {  // the second half of the keys' sums are handed over, lane by lane
+    static_assert(RG * (DB * 16 + 2) * 256 <= KS * 4 * TILE, "a wave's sums fit where its tiles were");
+    float* give = reinterpret_cast<float*>(lds + rg * (DB * 16 + 2) * 256) + lane;
+    if (kg == 1) {
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) give[(16 * i + e) * 64] = acc[i][e];
+      give[DB * 16 * 64] = m, give[(DB * 16 + 1) * 64] = l;
+    }
+    __syncthreads();
+    if (kg == 0) {
+      const float m1 = give[DB * 16 * 64], top1 = fmaxf(m, m1);
+      // a half that saw none of the row's keys has l = 0 and sums of 0, or NaN from NaN keys
+      const float f0 = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top1);
+      const float f1 = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m1 - top1);
+      l = l * f0 + give[(DB * 16 + 1) * 64] * f1;
+      m = top1;
+#pragma unroll
+      for (int i = 0; i < DB; ++i)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][e] = acc[i][e] * f0 + give[(16 * i + e) * 64] * f1;
+    }
+    __syncthreads();
+    if (kg == 1) return;
+  }
+  const float f = l == 0.f ? 0.f : (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
 #pragma unroll
   for (int d0 = 0; d0 < DP; d0 += DW) {
 #pragma unroll
@@ -1235,7 +1271,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
   const int item = blockIdx.x / blocks, in = blockIdx.x - item * blocks;
   const int kvh = item % g.c.heads;
   const int4 head = p.head[item / g.c.heads];
-  const int b = FEW ? item / g.c.heads : head.z, r0 = FEW ? 0 : head.w * kManyRows;
+  const int b = FEW ? item / g.c.heads : head.z, r0 = FEW ? 0 : head.w * p.part_rows;
   const int count = head.y, first = head.x;
   if (!FEW && count <= 1) return;  // no such tile, or written already
   const Seq s = sequence(g, b);
@@ -1306,7 +1342,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
 struct Launch {
   bool few, many;
   int few_splits, few_parts, few_rows;  // few_parts 0: one workgroup per (sequence, kv head), no parts
-  int many_splits, tiles;
+  int many_splits, many_rows, tiles;
   size_t few_bytes, many_bytes;
 };
 
@@ -1341,15 +1377,21 @@ Launch plan(const AttnArgs& a) {
     }
   }
   if (x.many) {
-    x.tiles = (int)((int64_t)a.T * G / kManyRows + std::min(a.B, a.T));
+    const int64_t slots = kCus * (a.c.dim <= 128 ? 2 : 1);  // workgroups that the CUs hold, by their registers
+    auto row_tiles = [&](int rows) {  // at most: by all rows, and by max_q
+      return std::min((int64_t)a.T * G / rows + std::min(a.B, a.T), a.B * (((int64_t)a.max_q * G + rows - 1) / rows));
+    };
+    // 64 rows take a little over half the time of 128, and are taken where that makes the rounds shorter
+    const int64_t r128 = (row_tiles(128) * a.c.heads + slots - 1) / slots, r64 = (row_tiles(64) * a.c.heads + slots - 1) / slots;
+    x.many_rows = 11 * r64 < 20 * r128 ? 64 : 128;
+    x.tiles = (int)row_tiles(x.many_rows);
     const int64_t items = (int64_t)x.tiles * a.c.heads;
-    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kManyRows) : most;
-    // one round of the workgroups that the CUs hold (two of them, one at 256 dims, by their registers), where
-    // whole rows give less than two thirds of it: every part of a row costs its f32 sums once written and once read
-    const int64_t slots = kCus * (a.c.dim <= 128 ? 2 : 1);
+    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + x.many_rows) : most;
+    // parts where whole rows give less than two thirds of a round: every part of a row costs its f32 sums once
+    // written and once read
     x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (slots + items / 2) / items));
     if (x.many_splits > 1)
-      x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)items * x.many_splits * kManyRows * row;
+      x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)items * x.many_splits * x.many_rows * row;
   }
   return x;
 }
@@ -1364,14 +1406,21 @@ void launch_few(const Plan& p, int items, hipStream_t st) {
   attention_few_kernel<DP, FP8><<<items, 64 * few_waves<DP, FP8>(), few_lds<DP, FP8>(), st>>>(p);
 }
 
-template <int DP, bool FP8>
-void launch_many(const Plan& p, int items, hipStream_t st) {
+template <int DP, bool FP8, int KS>
+void launch_many_ks(const Plan& p, int items, hipStream_t st) {
   static std::once_flag flags[kMaxDevices];
   once_per_device(flags, [] {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(attention_many_kernel<DP, FP8>),
-                              hipFuncAttributeMaxDynamicSharedMemorySize, many_lds<DP>());
+    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(attention_many_kernel<DP, FP8, KS>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, many_lds<DP, KS>());
   });
-  attention_many_kernel<DP, FP8><<<items * p.splits, 64 * kManyWaves, many_lds<DP>(), st>>>(p);
+  attention_many_kernel<DP, FP8, KS><<<items * p.splits, 64 * kManyWaves, many_lds<DP, KS>(), st>>>(p);
+}
+template <int DP, bool FP8>
+void launch_many(const Plan& p, int items, hipStream_t st) {
+  if (p.part_rows == 64)
+    launch_many_ks<DP, FP8, 2>(p, items, st);
+  else
+    launch_many_ks<DP, FP8, 1>(p, items, st);
 }
 
 template <bool FEW, bool WIDE>
@@ -1400,8 +1449,7 @@ void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
   }
   if (x.many) {
     ws += x.few_bytes;
-    p.splits = x.many_splits, p.part_rows = kManyRows;
-    p.tiles = x.tiles, p.keys = D <= 128 ? 64 : 32;
+    p.splits = x.many_splits, p.part_rows = x.many_rows, p.tiles = x.tiles;
     p.head = reinterpret_cast<int4*>(ws);
     p.part = x.many_splits > 1 ? reinterpret_cast<float*>(ws + (size_t)x.tiles * sizeof(int4)) : nullptr;
     const int items = x.tiles * heads;
