@@ -633,7 +633,11 @@ constexpr int kManyWaves = 4;
 template <int DP, int KS>
 constexpr int many_keys() { return DP == 256 || KS == 2 ? 32 : 64; }  // of a key tile
 template <int DP, int KS>
-constexpr int many_lds() { return KS * 2 * 2 * many_keys<DP, KS>() * DP * 2 + kManyWaves * 1024; }
+constexpr int many_lds() { return KS * 4 * many_keys<DP, KS>() * DP * 2 + kManyWaves * 1024; }
+// Workgroups of a CU: two by their LDS, and by their registers up to 128 dims.  (Three buffers at KS = 2 take the LDS of
+// one: a 1570-token prompt in 39 us against 31.7.)
+template <int DP>
+constexpr int many_per_cu() { return DP == 256 ? 1 : 2; }
 
 __device__ __forceinline__ int tiles_of(const Plan& p, int n) {
   const int rows = n * p.G;
@@ -642,11 +646,12 @@ __device__ __forceinline__ int tiles_of(const Plan& p, int n) {
 
 // The sequence and tile of the tile-th row tile of the batch; b = -1 past the last.  64 sequences at a
 // time, one per lane.
-__device__ __forceinline__ void locate(const Plan& p, int tile, int& b, int& at) {
+__device__ __forceinline__ Seq locate(const Plan& p, int tile, int& b, int& at) {
   const int lane = threadIdx.x & 63;
   int base = 0;
   for (int b0 = 0; b0 < p.a.B; b0 += 64) {
-    const int mine = b0 + lane < p.a.B ? tiles_of(p, sequence(p.a, b0 + lane).n) : 0;
+    const Seq s = sequence(p.a, min(b0 + lane, p.a.B - 1));
+    const int mine = b0 + lane < p.a.B ? tiles_of(p, s.n) : 0;
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -660,18 +665,20 @@ __device__ __forceinline__ void locate(const Plan& p, int tile, int& b, int& at)
       at = tile - base - (__shfl(incl, at_lane) - __shfl(mine, at_lane));
       b = __builtin_amdgcn_readfirstlane(b);
       at = __builtin_amdgcn_readfirstlane(at);
-      return;
+      return {__builtin_amdgcn_readlane(s.first, at_lane), __builtin_amdgcn_readlane(s.n, at_lane),
+              __builtin_amdgcn_readlane(s.len, at_lane)};
     }
     base += __shfl(incl, 63);
   }
   b = -1, at = 0;
+  return {0, 0, 0};
 }
 
 template <int DP, bool FP8, int KS>
-__global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_many_kernel(Plan p) {
+__global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attention_many_kernel(Plan p) {
   constexpr int NW = kManyWaves, RG = NW / KS, ROWS = 32 * RG;  // row blocks, rows
   constexpr int KT = many_keys<DP, KS>(), TILE = KT * DP * 2, RW = KT / RG;  // RW: rows of a tile that a wave fetches
-  constexpr int STEPS = DP / 16, DB = DP / 32, SUB = KT / 32;
+  constexpr int STEPS = DP / 16, DB = DP / 32, SUB = KT / 32, NB = 2;  // NB: buffers
   extern __shared__ __align__(16) unsigned char lds[];
   const AttnArgs& g = p.a;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -679,12 +686,11 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   const int kvh = blockIdx.x % g.c.heads, rest = blockIdx.x / g.c.heads;
   const int split = rest % p.splits, slot = p.tiles - 1 - rest / p.splits;
   int b, tile;
-  locate(p, slot, b, tile);
+  const Seq s = locate(p, slot, b, tile);
   if (b < 0) {
     if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {0, 0, 0, 0};
     return;
   }
-  const Seq s = sequence(g, b);
   const int D = g.c.dim, all_rows = s.n * p.G, r0 = tile * ROWS, r1 = min(all_rows, r0 + ROWS);
   const Keys k = keys_of(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT * KS);
   if (split >= k.act) return;
@@ -699,15 +705,6 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   const bool live = wr0 < r1;  // a wave of no rows helps to fetch
   const int row = min(wr0 + (lane & 31), r1 - 1), tok = divide(row, p.group);
   f16x8 q[STEPS];
-  {
-    const uint16_t* src = g.q + (int64_t)(s.first + tok) * g.ldq + (int64_t)(kvh * p.G + row - tok * p.G) * D;
-#pragma unroll
-    for (int t = 0; t < STEPS; ++t) {
-      const int d = 16 * t + 8 * h;
-      f16x8 z = {};
-      q[t] = d < D ? *reinterpret_cast<const f16x8*>(src + d) : z;
-    }
-  }
   const int at0 = s.len - s.n + 1;  // keys before and at token 0's position
   const int see1 = at0 + tok, see0 = g.window ? see1 - g.window : 0;
   const int tok_a = divide(min(wr0, r1 - 1), p.group), tok_b = divide(max(wr0, wr1) - 1, p.group);
@@ -720,12 +717,13 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
 
-  // LDS: two K tiles, two V tiles (of each kg), the waves' page numbers.  Offsets of a lane's fragments within a tile:
+  // LDS: NB K tiles, NB V tiles (of each kg), the waves' page numbers.  Offsets of a lane's fragments within a tile:
   // the swizzles fold into the lane's part, up to the chunk bits that count steps (K) or dims blocks (V)
   // below 256 bytes.
-  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds + kg * 4 * TILE;
-  auto k_tile = [](int i) { return (uint32_t)((i & 1) * TILE); };
-  auto v_tile = [](int i) { return (uint32_t)((2 + (i & 1)) * TILE); };
+  constexpr int SPACE = 2 * NB * TILE;  // of a kg
+  const uint32_t lds_at = (uint32_t)(uintptr_t)(lds_void_t*)lds + kg * SPACE;
+  auto k_tile = [](int i) { return (uint32_t)(i % NB * TILE); };
+  auto v_tile = [](int i) { return (uint32_t)((NB + i % NB) * TILE); };
   constexpr int HALF = 32 * DP * 2;  // bytes of 32 keys
   constexpr int KA = STEPS < 8 ? STEPS : 8, VA = DB < 4 ? DB : 4;
   uint32_t k_at[KA], v_at[VA];
@@ -956,7 +954,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
                      (uint32_t)__builtin_amdgcn_readlane((int)offsets, i & 63));
   };
   // any other page size: page numbers of a tile's rows, through LDS, four tiles of them
-  const int* ids = reinterpret_cast<const int*>(lds + KS * 4 * TILE + wave * 1024);
+  const int* ids = reinterpret_cast<const int*>(lds + KS * SPACE + wave * 1024);
   const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
   auto fetch_ids = [&](int i) W4_INLINE {
     if (plain) return;
@@ -1014,7 +1012,7 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   // e4m3: what fetch() holds of tile i, widened, to LDS
   auto land = [&](int i, auto of_v) W4_INLINE {
     constexpr bool V = decltype(of_v)::value;
-    unsigned char* st = lds + (4 * kg + (V ? 2 : 0) + (i & 1)) * TILE;
+    unsigned char* st = lds + kg * SPACE + (V ? v_tile(i) : k_tile(i));
 #pragma unroll
     for (int x = 0; x < NI; ++x) {
       const int r = RW * rg + x * RPI + lane / CH, ch = lane % CH * 2;
@@ -1060,20 +1058,34 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     }
   };
   // Between the block that reads K of tile t last and the one that reads K of t + 1: K of t is not read any
-  // more, nor V of t + SUB - 3, so K of t + 2 and V of t + SUB - 1 may follow, all of them now, or the plain ones
-  // behind the slices of the next block(s).  (Issued together, the waves' DMA queues up for the memory path
-  // while the matrix cores idle.)
+  // more, nor V of t - 1 (SUB = 2) or t - 2, so the tiles NB further may follow, all of them now, or the plain ones
+  // behind the first slices of the next block.  (Issued together, the waves' DMA queues up for the memory
+  // path while the matrix cores idle.)
+  constexpr int LAG = SUB == 2 ? 1 : 2;  // V is that far behind K
   bool more_k = false, more_v = false;
-  int64_t off_v[2] = {0, 0};  // offsets of V tiles t + SUB - 1 and (SUB = 1) t + 1
-  auto turn = [&](int t) W4_INLINE {
+  int64_t off_v[2] = {0, 0};  // offsets of the next V tiles
+  // inner: tile t + NB is a whole one, and phase is t % NB, a constant
+  auto turn = [&](int t, auto inner, int phase) W4_INLINE {
     put_down();
     meet();
-    fetch_ids(t + 3);
-    const int64_t off = plain ? offset_of(t + 2) : 0;
-    more_k = start_k(t + 2, off);
-    more_v = start_v(t + SUB - 1, off_v[0]);
-    if constexpr (SUB == 1) off_v[0] = off_v[1];
-    off_v[SUB == 1] = off;
+    if (!plain) {
+      fetch_ids(t + NB + 1);
+      more_k = start_k(t + NB, 0);
+      more_v = start_v(t + NB - LAG, 0);
+      return;
+    }
+    const int64_t off = offset_of(t + NB), now_v = off_v[0];
+    if constexpr (LAG == 2) off_v[0] = off_v[1];
+    off_v[LAG - 1] = off;
+    if (decltype(inner)::value && (off | now_v) >= 0) {
+      from[0] = bases[0] + off, from[1] = bases[1] + now_v;
+      to[0] = lds_at + k_tile(phase) + rg * (TILE / RG), to[1] = lds_at + v_tile(phase + NB - LAG) + rg * (TILE / RG);
+      held_k = t + NB, held_v = t + NB - LAG;
+      more_k = more_v = true;
+      return;
+    }
+    more_k = start_k(t + NB, off);
+    more_v = start_v(t + NB - LAG, now_v);
   };
   constexpr int PER = (2 * NI + DB - 1) / DB;  // loads behind a slice
   auto rest_k = [&](int x) W4_INLINE {
@@ -1093,18 +1105,29 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   auto rest_kv = [&](int x) W4_INLINE { rest_k(x), rest_v(x); };
   auto none = [](int) {};
   auto turn_whole = [&](int t) W4_INLINE {
-    turn(t);
+    turn(t, std::false_type{}, 0);
 #pragma unroll
     for (int x = 0; x < DB; ++x) rest_kv(x);
   };
   if (tiles > 0) {
-    fetch_ids(0), fetch_ids(1), fetch_ids(2);
-    wait_vm<0>();
+    if (!plain) {
+      for (int i = 0; i <= NB; ++i) fetch_ids(i);
+      wait_vm<0>();
+    }
     get_k(0);
-    if constexpr (SUB == 2) get_v(0);
+    if constexpr (NB > LAG) get_v(0);
     put_down();
     get_k(1);
-    if (plain) off_v[0] = offset_of(SUB - 1), off_v[1] = offset_of(1);
+    if (plain) off_v[0] = offset_of(NB - LAG), off_v[1] = offset_of(NB - 1);
+  }
+  {
+    const uint16_t* src = g.q + (int64_t)(s.first + tok) * g.ldq + (int64_t)(kvh * p.G + row - tok * p.G) * D;
+#pragma unroll
+    for (int t = 0; t < STEPS; ++t) {
+      const int d = 16 * t + 8 * h;
+      f16x8 z = {};
+      q[t] = d < D ? *reinterpret_cast<const f16x8*>(src + d) : z;
+    }
   }
   constexpr std::true_type yes{};
   constexpr std::false_type no{};
@@ -1120,18 +1143,21 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     top = top_of(sc);
     if constexpr (SUB == 2) {
       block(yes, no, k_tile(0) + HALF, 0, none, alone);
-      // two tiles a round, so that LDS addresses are a lane's base and a constant
-      auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
-        turn(t);
-        block(yes, yes, kt, vt, rest_kv, std::integral_constant<int, 0>{});
-        block(yes, yes, kt + HALF, vt + HALF, none, std::integral_constant<int, 1>{});
+      auto step = [&](int t, auto inner, int phase) W4_INLINE {  // phase: t % 2
+        turn(t, inner, phase);
+        block(yes, yes, k_tile(phase + 1), v_tile(phase), rest_kv, std::integral_constant<int, 0>{});
+        block(yes, yes, k_tile(phase + 1) + HALF, v_tile(phase) + HALF, none, std::integral_constant<int, 1>{});
       };
+      // as many tiles a round as buffers, so that LDS addresses are a lane's base and a constant
       int t = 0;
-      for (; t + 2 < full; t += 2) {
-        step(t, TILE, 2 * TILE);
-        step(t + 1, 0, 3 * TILE);
+      for (; t + 3 < full; t += 2) {
+        step(t, yes, 0);
+        step(t + 1, yes, 1);
       }
-      if (t + 1 < full) step(t, TILE, 2 * TILE);
+      while (t + 1 < full) {
+        step(t++, no, 0);
+        if (t + 1 < full) step(t++, no, 1);
+      }
       turn_whole(full - 1);
       block(no, yes, 0, v_tile(full - 1), none, alone);
     } else {
@@ -1140,21 +1166,25 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
         block(no, no, 0, 0, none, alone);
       } else {
         block(yes, no, k_tile(1), 0, none, alone);
-        auto step = [&](int t, uint32_t kt, uint32_t vt) W4_INLINE {
-          turn(t);
-          block(yes, yes, kt, vt, rest_kv, alone);
+        auto step = [&](int t, auto inner, int phase) W4_INLINE {  // phase: t % NB
+          turn(t, inner, phase);
+          block(yes, yes, k_tile(phase + 1), v_tile(phase + NB - 1), rest_kv, alone);
         };
         int t = 1;
-        for (; t + 2 < full; t += 2) {
-          step(t, 0, 2 * TILE);
-          step(t + 1, TILE, 3 * TILE);
+        for (; t + 2 * NB - 1 < full; t += NB) {
+          step(t, yes, 1);
+          step(t + 1, yes, 0);
         }
-        if (t + 1 < full) step(t, 0, 2 * TILE);
+        while (t + 1 < full) {
+          step(t++, no, 1);
+          if (t + 1 < full) step(t++, no, 0);
+        }
         turn_whole(full - 1);
         block(no, yes, 0, v_tile(full - 2), none, alone);
       }
       put_down();
       meet();  // V of the last
+      get_v(full);
     }
 #pragma unroll
     for (int x = 0; x < 2 * DB; ++x)
@@ -1165,16 +1195,20 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
     meet();
     for (int t = 0; t < full; ++t) turn_whole(t);
     put_down();
-    if constexpr (SUB == 1) meet();
+    if constexpr (SUB == 1) {
+      meet();
+      get_v(full);
+    }
+  } else if (LAG == NB) {
+    get_v(0);
   }
-  // fetched so far: K to tile full + 1 (1 when full is 0), V to full + SUB - 2
+  // on their way or there: K of tiles full .. full + NB - 1, V of full
   for (int i = full; i < turns; ++i) {
-    if (SUB == 1 && i == full) get_v(i);
     put_down();
     meet();
-    if (i > full) get_k(i + 1);
+    if (i > full) get_k(i + NB - 1);
     get_v(i + 1);
-    fetch_ids(i + 2);
+    fetch_ids(i + 3);
     if (live && there(i)) edge(i);
   }
 
@@ -1182,34 +1216,40 @@ __global__ __launch_bounds__(64 * kManyWaves, DP == 256 ? 1 : 2) void attention_
   // that rows are written whole.  Four dims x of row r of the wave's 32 lie at x ^ r (mod what 128 dims hold).
   l = across<false>(l, add2);
   constexpr int DW = DP < 128 ? DP : 128, XW = DW / 4;  // dims of a round, in fours
-  static_assert(ROWS * DW * 4 <= KS * 4 * TILE, "the rows fit where the tiles were");
+  static_assert(ROWS * DW * 4 <= KS * SPACE, "the rows fit where the tiles were");
   unsigned char* mine = lds + rg * 32 * DW * 4;
   auto four_of = [&](int r, int x) W4_INLINE { return reinterpret_cast<f32x4*>(mine + r * DW * 4 + (x ^ (r % XW)) * 16); };
   const int rows = live && kg == 0 ? wr1 - wr0 : 0;
   wait_vm<0>();     // no DMA is on its way to LDS any more
   __syncthreads();  // the tiles have been read
   if constexpr (KS == 2) {  // the second half of the keys' sums are handed over, lane by lane
-    static_assert(RG * (DB * 16 + 2) * 256 <= KS * 4 * TILE, "a wave's sums fit where its tiles were");
-    float* give = reinterpret_cast<float*>(lds + rg * (DB * 16 + 2) * 256) + lane;
+    static_assert(RG * (DB * 16 + 4) * 256 <= KS * SPACE, "a wave's sums fit where its tiles were");
+    f32x4* give = reinterpret_cast<f32x4*>(lds + rg * (DB * 16 + 4) * 256) + lane;
     if (kg == 1) {
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
+      for (int i = 0; i < DB * 4; ++i) {
+        f32x4 o;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) give[(16 * i + e) * 64] = acc[i][e];
-      give[DB * 16 * 64] = m, give[(DB * 16 + 1) * 64] = l;
+        for (int e = 0; e < 4; ++e) o[e] = acc[i / 4][i % 4 * 4 + e];
+        give[i * 64] = o;
+      }
+      give[DB * 4 * 64] = {m, l, 0.f, 0.f};
     }
     __syncthreads();
     if (kg == 0) {
-      const float m1 = give[DB * 16 * 64], top1 = fmaxf(m, m1);
+      const f32x4 ml = give[DB * 4 * 64];
+      const float top1 = fmaxf(m, ml[0]);
       // a half that saw none of the row's keys has l = 0 and sums of 0, or NaN from NaN keys
       const float f0 = m == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top1);
-      const float f1 = m1 == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m1 - top1);
-      l = l * f0 + give[(DB * 16 + 1) * 64] * f1;
+      const float f1 = ml[0] == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(ml[0] - top1);
+      l = l * f0 + ml[1] * f1;
       m = top1;
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
+      for (int i = 0; i < DB * 4; ++i) {
+        const f32x4 o = give[i * 64];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][e] = acc[i][e] * f0 + give[(16 * i + e) * 64] * f1;
+        for (int e = 0; e < 4; ++e) acc[i / 4][i % 4 * 4 + e] = acc[i / 4][i % 4 * 4 + e] * f0 + o[e] * f1;
+      }
     }
     __syncthreads();
     if (kg == 1) return;
@@ -1377,13 +1417,13 @@ Launch plan(const AttnArgs& a) {
     }
   }
   if (x.many) {
-    const int64_t slots = kCus * (a.c.dim <= 128 ? 2 : 1);  // workgroups that the CUs hold, by their registers
     auto row_tiles = [&](int rows) {  // at most: by all rows, and by max_q
       return std::min((int64_t)a.T * G / rows + std::min(a.B, a.T), a.B * (((int64_t)a.max_q * G + rows - 1) / rows));
     };
-    // 64 rows take a little over half the time of 128, and are taken where that makes the rounds shorter
+    // 64 rows take a little over half the time of 128, and are taken where that makes the rounds of workgroups shorter
+    const int64_t slots = kCus * (a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>());
     const int64_t r128 = (row_tiles(128) * a.c.heads + slots - 1) / slots, r64 = (row_tiles(64) * a.c.heads + slots - 1) / slots;
-    x.many_rows = 11 * r64 < 20 * r128 ? 64 : 128;
+    x.many_rows = r64 * 11 < r128 * 20 ? 64 : 128;
     x.tiles = (int)row_tiles(x.many_rows);
     const int64_t items = (int64_t)x.tiles * a.c.heads;
     const int64_t keys = a.window ? std::min(most, (int64_t)a.window + x.many_rows) : most;
