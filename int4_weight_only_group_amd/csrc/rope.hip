@@ -9,8 +9,9 @@
 // to 1e-10 turns at 10^6 positions, and only then goes to f32 for sincospif.  The f64 work is
 // one pair per thread (R/2 per token, shared by all heads through LDS), so it costs little.
 //
-// Bound: HBM for prompts (each element read once, written once), launch latency for a decode
-// step.
+// Bound: HBM for prompts (each element read once, written once), the launch and the chain of
+// loads for a decode step.  So a thread's first elements, its token's slot and its head's scale
+// are all on their way before the angles are formed.
 #include "w4_internal.h"
 #include "w4_kv.h"
 
@@ -18,8 +19,10 @@ namespace w4 {
 
 namespace {
 
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens of a workgroup
+constexpr int kMaxTokens = 4;  // tokens of a workgroup, at most
 
 struct RopeArgs {
   const void* src[3];  // q, k, v rows (heads of one token are contiguous)
@@ -33,6 +36,8 @@ struct RopeArgs {
   const float* freq;
   float mscale, sign;
   int T, D, R, tokens;  // tokens: of each workgroup
+  int per, n;           // items of a rotated head, of a token
+  float per_n, per_head, per_chunks;  // 1 / n, 1 / per, 1 / (D / 8)
 };
 
 // Where 8 (or 1) output values of a head go: f16 for q and an f16 cache, e4m3 with the head's
@@ -50,17 +55,12 @@ __device__ __forceinline__ float load1(const void* p, int64_t i) {
 }
 
 template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+__device__ __forceinline__ f32x8 load8(const void* p, int64_t i) {
   if constexpr (F32) {
     const f32x4* q = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(p) + i);
-    const f32x4 lo = q[0], hi = q[1];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = lo[e], v[4 + e] = hi[e];
-  } else {
-    const f16x8 h = *reinterpret_cast<const f16x8*>(reinterpret_cast<const f16*>(p) + i);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
+    return __builtin_shufflevector(q[0], q[1], 0, 1, 2, 3, 4, 5, 6, 7);
   }
+  return __builtin_convertvector(*reinterpret_cast<const f16x8*>(reinterpret_cast<const f16*>(p) + i), f32x8);
 }
 
 // RN to e4m3 of x / scale, saturated at 448 (NaN stays NaN)
@@ -70,7 +70,7 @@ __device__ __forceinline__ float e4m3_range(float x, float scale) {
   return x < -448.f ? -448.f : x;
 }
 
-__device__ __forceinline__ void store8(const Dst& d, int i, const float (&v)[8]) {
+__device__ __forceinline__ void store8(const Dst& d, int i, f32x8 v) {
   if (d.e4m3) {
     float s[8];
 #pragma unroll
@@ -84,10 +84,7 @@ __device__ __forceinline__ void store8(const Dst& d, int i, const float (&v)[8])
     }
     *reinterpret_cast<u32x2*>(reinterpret_cast<uint8_t*>(d.p) + i) = w;
   } else {
-    f16x8 h;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = (f16)v[e];
-    *reinterpret_cast<f16x8*>(reinterpret_cast<f16*>(d.p) + i) = h;
+    *reinterpret_cast<f16x8*>(reinterpret_cast<f16*>(d.p) + i) = __builtin_convertvector(v, f16x8);
   }
 }
 
@@ -99,20 +96,12 @@ __device__ __forceinline__ void store1(const Dst& d, int i, float v) {
     reinterpret_cast<f16*>(d.p)[i] = (f16)v;
 }
 
-// A token's head j (q heads, then k, then v): its source row and where it goes.
-__device__ __forceinline__ Dst head_of(const RopeArgs& g, int t, int j, int64_t slot, const void*& src, int64_t& at) {
-  const int w = j < g.heads[0] ? 0 : j < g.heads[0] + g.heads[1] ? 1 : 2;
-  const int h = j - (w > 0 ? g.heads[0] : 0) - (w > 1 ? g.heads[1] : 0);
-  src = w == 0 ? g.src[0] : w == 1 ? g.src[1] : g.src[2];
-  at = (int64_t)t * (w == 0 ? g.ld[0] : w == 1 ? g.ld[1] : g.ld[2]) + (int64_t)h * g.D;
-  if (w == 0) return {g.q_out + (int64_t)t * g.ldq_out + (int64_t)h * g.D, false, 1.f};
-  if (slot < 0 || slot >= (int64_t)g.c.pages * g.c.page_size) return {nullptr, false, 1.f};
-  const int page = (int)slot / g.c.page_size, off = (int)slot - page * g.c.page_size;
-  const int64_t e = page * g.c.stride_page + h * g.c.stride_head + off * g.c.stride_token;
-  void* base = w == 1 ? g.c.k : g.c.v;
-  if (!g.c.e4m3) return {reinterpret_cast<f16*>(base) + e, false, 1.f};
-  const float* sc = w == 1 ? g.c.k_scale : g.c.v_scale;
-  return {reinterpret_cast<uint8_t*>(base) + e, true, sc ? sc[h] : 1.f};
+// i / d for 0 <= i < 2^24 with r = 1 / d in f32: the product is off by less than one
+__device__ __forceinline__ int divide(int i, int d, float r) {
+  int q = (int)((float)i * r);
+  const int rest = i - q * d;
+  q += rest >= d;
+  return q - (rest < 0);
 }
 
 enum Mode { kHalf, kInterleaved, kHalfOdd };
@@ -121,78 +110,129 @@ enum Mode { kHalf, kInterleaved, kHalfOdd };
 // pairs in one thread, so y may be x), then the (D - R)/8 chunks that pass.  kInterleaved: D/8
 // chunks (a chunk that R ends in passes its tail).  kHalfOdd (any other R): R/2 pairs and
 // D - R single dims.  A v head is D/8 chunks that pass.
+int items_of(int mode, int D, int R) {
+  return mode == kHalf ? D / 8 - R / 16 : mode == kInterleaved ? D / 8 : D - R / 2;
+}
+
+struct Item {
+  Dst d;
+  int tl, item;  // token of the workgroup, item of the head
+  bool rot;      // of a head that turns
+  f32x8 a, b;
+};
+
+template <bool F32, int MODE>
+__device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x) {
+  const int half = g.R / 2, rot_heads = g.heads[0] + g.heads[1], n_rot = rot_heads * g.per;
+  x.tl = divide(i, g.n, g.per_n);
+  const int r = i - x.tl * g.n, t = t0 + x.tl;
+  const int64_t slot = g.slots ? g.slots[t] : -1;
+  x.rot = r < n_rot;
+  int j = x.rot ? divide(r, g.per, g.per_head) : divide(r - n_rot, g.D / 8, g.per_chunks);
+  x.item = x.rot ? r - j * g.per : r - n_rot - j * (g.D / 8);
+  j += x.rot ? 0 : rot_heads;
+  // the head: of q, k or v, where it is read and where it goes
+  const int w = j < g.heads[0] ? 0 : j < rot_heads ? 1 : 2;
+  const int h = j - (w > 0 ? g.heads[0] : 0) - (w > 1 ? g.heads[1] : 0);
+  const void *q = g.src[0], *k = g.src[1], *v = g.src[2];
+  const int64_t ldq = g.ld[0], ldk = g.ld[1], ldv = g.ld[2];
+  const void* src = w == 0 ? q : w == 1 ? k : v;
+  const int64_t at = (int64_t)t * (w == 0 ? ldq : w == 1 ? ldk : ldv) + (int64_t)h * g.D;
+  if (MODE == kHalfOdd && x.rot) {
+    if (x.item < half) x.a[0] = load1<F32>(src, at + x.item);
+    x.b[0] = load1<F32>(src, at + x.item + half);
+  } else {
+    const bool pair = MODE == kHalf && x.rot && x.item < g.R / 16;
+    if (MODE == kHalf && x.rot && !pair) x.item += g.R / 16;
+    x.a = load8<F32>(src, at + x.item * 8);
+    if (pair) x.b = load8<F32>(src, at + x.item * 8 + half);
+  }
+  x.d.e4m3 = w > 0 && g.c.e4m3;
+  x.d.scale = 1.f;
+  x.d.p = nullptr;
+  if (w == 0) {
+    x.d.p = g.q_out + (int64_t)t * g.ldq_out + (int64_t)h * g.D;
+  } else if (slot >= 0 && slot < (int64_t)g.c.pages * g.c.page_size) {
+    const int page = (int)slot / g.c.page_size, off = (int)slot - page * g.c.page_size;
+    const int64_t e = page * g.c.stride_page + h * g.c.stride_head + off * g.c.stride_token;
+    const float *ks = g.c.k_scale, *vs = g.c.v_scale, *sc = w == 1 ? ks : vs;
+    void *kc = g.c.k, *vc = g.c.v;
+    if (x.d.e4m3 && sc) x.d.scale = sc[h];
+    x.d.p = reinterpret_cast<uint8_t*>(w == 1 ? kc : vc) + (x.d.e4m3 ? e : 2 * e);
+  }
+}
+
+template <bool F32, int MODE>
+__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, Item& x) {
+  if (x.d.p == nullptr) return;
+  const int half = g.R / 2;
+  const float2* cs = turn + x.tl * half;
+  if (MODE == kHalfOdd && x.rot) {
+    if (x.item < half) {
+      const float2 w = cs[x.item];
+      store1(x.d, x.item, x.a[0] * w.x - x.b[0] * w.y);
+      store1(x.d, x.item + half, x.b[0] * w.x + x.a[0] * w.y);
+    } else {
+      store1(x.d, x.item + half, x.b[0]);
+    }
+    return;
+  }
+  const int c0 = x.item * 8;
+  if (MODE == kHalf && x.rot && x.item < g.R / 16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 w = cs[c0 + e];
+      const float a = x.a[e];
+      x.a[e] = a * w.x - x.b[e] * w.y;
+      x.b[e] = x.b[e] * w.x + a * w.y;
+    }
+    store8(x.d, c0 + half, x.b);
+  }
+  if (MODE == kInterleaved && x.rot) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (c0 + 2 * e >= g.R) break;
+      const float2 w = cs[c0 / 2 + e];
+      const float a = x.a[2 * e];
+      x.a[2 * e] = a * w.x - x.a[2 * e + 1] * w.y;
+      x.a[2 * e + 1] = x.a[2 * e + 1] * w.x + a * w.y;
+    }
+  }
+  store8(x.d, c0, x.a);
+}
+
 template <bool F32, int MODE>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
   __shared__ float2 turn[kMaxTokens * 128];  // [token][pair]: mscale (cos, sin)
-  const int t0 = blockIdx.x * g.tokens, nt = min(g.tokens, g.T - t0), half = g.R / 2;
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
-    const int tl = i / half, p = i - tl * half;
+  const int t0 = blockIdx.x * g.tokens, nt = min(g.tokens, g.T - t0), half = g.R / 2, n = nt * g.n;
+  Item x{};
+  int i = threadIdx.x;
+  if (i < n) fetch<F32, MODE>(g, i, t0, x);
+  for (int k = threadIdx.x; k < nt * half; k += kThreads) {
+    const int tl = k / half, p = k - tl * half;
     double a = (double)g.pos[t0 + tl] * (double)g.freq[p] * 0.15915494309189535;  // turns
     a -= rint(a);
     float s, c;
     sincospif(2.f * (float)a, &s, &c);
-    turn[tl * half + p] = make_float2(c * g.mscale, s * g.mscale * g.sign);
+    turn[k] = make_float2(c * g.mscale, s * g.mscale * g.sign);
   }
   __syncthreads();
-  const int rot_heads = g.heads[0] + g.heads[1];
-  const int per = MODE == kHalf ? g.D / 8 - g.R / 16 : MODE == kInterleaved ? g.D / 8 : g.D - half;
-  const int n_rot = rot_heads * per, n = n_rot + g.heads[2] * (g.D / 8);
-  for (int i = threadIdx.x; i < nt * n; i += kThreads) {
-    const int tl = i / n, r = i - tl * n, t = t0 + tl;
-    const bool rot = r < n_rot;
-    const int j = rot ? r / per : rot_heads + (r - n_rot) / (g.D / 8);
-    const int item = rot ? r - j * per : (r - n_rot) % (g.D / 8);
-    const void* src;
-    int64_t at;
-    const Dst d = head_of(g, t, j, g.slots ? g.slots[t] : -1, src, at);
-    if (d.p == nullptr) continue;
-    const float2* cs = turn + tl * half;
-    if (MODE == kHalfOdd && rot) {
-      if (item < half) {
-        const float a = load1<F32>(src, at + item), b = load1<F32>(src, at + item + half);
-        const float2 w = cs[item];
-        store1(d, item, a * w.x - b * w.y);
-        store1(d, item + half, b * w.x + a * w.y);
-      } else {
-        store1(d, item + half, load1<F32>(src, at + item + half));
-      }
-      continue;
-    }
-    if (MODE == kHalf && rot && item < g.R / 16) {
-      float a[8], b[8];
-      load8<F32>(src, at + item * 8, a);
-      load8<F32>(src, at + item * 8 + half, b);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 w = cs[item * 8 + e];
-        const float x = a[e];
-        a[e] = x * w.x - b[e] * w.y;
-        b[e] = b[e] * w.x + x * w.y;
-      }
-      store8(d, item * 8, a);
-      store8(d, item * 8 + half, b);
-      continue;
-    }
-    const int c0 = (MODE == kHalf && rot ? item + g.R / 16 : item) * 8;
-    float a[8];
-    load8<F32>(src, at + c0, a);
-    if (MODE == kInterleaved && rot) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (c0 + 2 * e >= g.R) break;
-        const float2 w = cs[c0 / 2 + e];
-        const float x = a[2 * e];
-        a[2 * e] = x * w.x - a[2 * e + 1] * w.y;
-        a[2 * e + 1] = a[2 * e + 1] * w.x + x * w.y;
-      }
-    }
-    store8(d, c0, a);
+  while (i < n) {
+    finish<F32, MODE>(g, turn, x);
+    i += kThreads;
+    if (i < n) fetch<F32, MODE>(g, i, t0, x);
   }
 }
 
 void launch(RopeArgs& g, bool f32, bool interleaved, hipStream_t st) {
   const int mode = interleaved ? kInterleaved : (g.R / 2) % 8 == 0 ? kHalf : kHalfOdd;
+  g.per = items_of(mode, g.D, g.R);
+  g.n = (g.heads[0] + g.heads[1]) * g.per + g.heads[2] * (g.D / 8);
+  g.per_n = 1.f / g.n, g.per_head = 1.f / g.per, g.per_chunks = 1.f / (g.D / 8);
+  // Narrow tokens share a workgroup once there are plenty (8 workgroups a CU stay): 8191 x 16 x 80 f16 take 10.6 us
+  // with four tokens against 13.5 with one; 64 tokens would wait for each other, 24 us against 6.
   g.tokens = 1;
+  while (g.tokens < kMaxTokens && g.n * g.tokens < 2 * kThreads && g.T / g.tokens > 8 * 256) g.tokens *= 2;
   const int grid = (g.T + g.tokens - 1) / g.tokens;
 #define W4_ROPE(F, M) rope_kernel<F, M><<<grid, kThreads, 0, st>>>(g)
   if (f32) {
