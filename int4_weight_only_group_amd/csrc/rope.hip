@@ -229,10 +229,11 @@ void launch(RopeArgs& g, bool f32, bool interleaved, hipStream_t st) {
   g.per = items_of(mode, g.D, g.R);
   g.n = (g.heads[0] + g.heads[1]) * g.per + g.heads[2] * (g.D / 8);
   g.per_n = 1.f / g.n, g.per_head = 1.f / g.per, g.per_chunks = 1.f / (g.D / 8);
-  // Narrow tokens share a workgroup once there are plenty (8 workgroups a CU stay): 8191 x 16 x 80 f16 take 10.6 us
-  // with four tokens against 13.5 with one; 64 tokens would wait for each other, 24 us against 6.
+  // Where tokens are plenty (8 workgroups a CU stay), narrow ones share a workgroup as long as its threads go about
+  // once over their items: 8191 x 16 x 80 of f16 (160 items a token) take 10.5 us two at a time, 12.5 one at a time;
+  // 8192 x 20 x 128 of f32 into the cache (176 items) 24.7 and 23.3.
   g.tokens = 1;
-  while (g.tokens < kMaxTokens && g.n * g.tokens < 2 * kThreads && g.T / g.tokens > 8 * 256) g.tokens *= 2;
+  while (g.tokens < kMaxTokens && g.n * g.tokens * 2 <= kThreads * 5 / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
   const int grid = (g.T + g.tokens - 1) / g.tokens;
 #define W4_ROPE(F, M) rope_kernel<F, M><<<grid, kThreads, 0, st>>>(g)
   if (f32) {
