@@ -1420,16 +1420,30 @@ Launch plan(const AttnArgs& a) {
     auto row_tiles = [&](int rows) {  // at most: by all rows, and by max_q
       return std::min((int64_t)a.T * G / rows + std::min(a.B, a.T), a.B * (((int64_t)a.max_q * G + rows - 1) / rows));
     };
-    // 64 rows take a little over half the time of 128, and are taken where that makes the rounds of workgroups shorter
-    const int64_t slots = kCus * (a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>());
-    const int64_t r128 = (row_tiles(128) * a.c.heads + slots - 1) / slots, r64 = (row_tiles(64) * a.c.heads + slots - 1) / slots;
-    x.many_rows = r64 * 11 < r128 * 20 ? 64 : 128;
-    x.tiles = (int)row_tiles(x.many_rows);
+    // Rows of a tile and parts of a row: what takes least by this sum, in us (its terms are measured; at 128 dims
+    // it is within a fifth of the whole).  A workgroup starts and ends in 5, and goes over 64 keys in `turn`, alone
+    // or two on its CU; f32 parts are written and read at 4 TB/s, by one more launch.  Parts fill a round of
+    // the workgroups that the CUs hold, or one for each CU: four sequences of 8 new tokens after 16384 (16 heads on 2)
+    // take 29 us in 64 parts and 26 in 32, 256 new tokens 55 in 8 and 67 in 4; 200 after 2048 (32 on 8), 36 in
+    // 5 that exceed the round, and 27 in 4.  64 rows: a prompt of 1570 tokens 31.6, in 128 rows 39.
+    constexpr float kTurn[2][2] = {{.87f, 1.2f}, {1.4f, 2.14f}};
+    const int per_cu = a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>();
+    float least = INFINITY;
+    for (int rows = 64; rows <= 128; rows *= 2) {
+      const int64_t tiles = row_tiles(rows), items = tiles * a.c.heads;
+      const int64_t keys = a.window ? std::min(most, (int64_t)a.window + rows) : most;
+      for (int fill = 0; fill <= per_cu; ++fill) {
+        const int64_t splits = std::max<int64_t>(1, std::min((keys + 127) / 128, fill * kCus / items));
+        const int64_t wgs = items * splits, round = per_cu * kCus;
+        const float turn = kTurn[rows / 128][wgs > kCus && per_cu > 1] * std::max(a.c.dim, 64) / 128;
+        const float us = (float)((wgs + round - 1) / round) * (5.f + (float)(keys / splits) / 64.f * turn) +
+                         (splits > 1 ? 2.f + (float)wgs * rows * (float)row * 2.f / 4e6f : 0.f);
+        if (us >= least) continue;
+        least = us;
+        x.many_rows = rows, x.tiles = (int)tiles, x.many_splits = (int)splits;
+      }
+    }
     const int64_t items = (int64_t)x.tiles * a.c.heads;
-    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + x.many_rows) : most;
-    // parts where whole rows give less than two thirds of a round: every part of a row costs its f32 sums once
-    // written and once read
-    x.many_splits = (int)std::max<int64_t>(1, std::min((keys + 127) / 128, (slots + items / 2) / items));
     if (x.many_splits > 1)
       x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)items * x.many_splits * x.many_rows * row;
   }
