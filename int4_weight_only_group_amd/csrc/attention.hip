@@ -1404,7 +1404,8 @@ Launch plan(const AttnArgs& a) {
   if (x.many && a.B > 1 && G <= kFewRows && (int64_t)a.B * a.max_q != a.T) x.few = true;
   const size_t row = (size_t)(a.c.dim + 4) * sizeof(float);
   if (x.few) {
-    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + kFewRows) : most;
+    // at most: 16 tokens' window, from a multiple of 16
+    const int64_t keys = a.window ? std::min(most, (int64_t)a.window + 2 * kFewRows) : most;
     x.few_rows = (int)std::min<int64_t>(kFewRows, (int64_t)a.max_q * G);
     if (keys > kMinPart) {
       // one round of the workgroups that the CUs hold, in parts of equal length (their number exceeds
