@@ -507,7 +507,7 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return s0 if n > 1 else max(s0, h * d)
+    return s0 if n > 1 else h * d
 
 
 def _row_dtype(t: torch.Tensor, name: str) -> torch.dtype:
