@@ -533,27 +533,33 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
       m = mn;
     }
     const float ms = m == -INFINITY ? 0.f : m;
-    f16x8 w;
+    // weights as the sum of two f16 (22 bits): the matrix cores have time for both products here
+    f16x8 w, w_low;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float x = __builtin_amdgcn_exp2f(sc[kb][e] * c - ms);
+        const f16 high = (f16)x;
         l += x;
-        w[4 * kb + e] = (f16)x;
+        w[4 * kb + e] = high;
+        w_low[4 * kb + e] = (f16)(x - (float)high);
       }
+    auto add = [&](int i, const f16x8& v) {
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w, acc[i], 0, 0, 0);
+      acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w_low, acc[i], 0, 0, 0);
+    };
     if (t + 1 < mine)
       wait_vm<NI + 1>();  // K and the page numbers of the next tiles may be in flight
     else
       wait_vm<0>();
     if (!edge || (n == 1 && j0 >= all0)) {  // no row sees less of the tile's keys (past k1: zeros) than another
 #pragma unroll
-      for (int i = 0; i < DB; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v_frag(i), w, acc[i], 0, 0, 0);
+      for (int i = 0; i < DB; ++i) add(i, v_frag(i));
     } else {
       uint32_t odd = 0;
 #pragma unroll
-      for (int i = 0; i < DB; ++i)
-        acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(finite(v_frag(i), odd), w, acc[i], 0, 0, 0);
+      for (int i = 0; i < DB; ++i) add(i, finite(v_frag(i), odd));
       if (__any(odd != 0)) {
 #pragma unroll 1
         for (int r = 0; r < KT; ++r) {
