@@ -213,8 +213,13 @@ __device__ __forceinline__ float special_of(f16 v) {  // v if it is not finite, 
 // has half a tile or more in flight; the page numbers run a tile further ahead, through LDS too (in
 // registers, the compiler's wait for them would be a wait for everything in flight).  e4m3 tiles stay
 // e4m3 in LDS and are widened to f16, exactly, as fragments are read.
+//
+// Measured: 8 sequences of 61001 to 65536 tokens (16 heads on 2 of 128 dims, 520 MB) 97 us, 5.4 TB/s of the 5.9 that a
+// bare DMA of such pages reaches; 64 of 1 to 8192 in e4m3 (16 on 8, 553 MB) 115 us, 4.8 TB/s; one of 1570, 6.4 us and
+// 3.5 for the join: the latencies of page number, K, V and sums one after another.  The kernel for many rows takes
+// 13.5 us for the last, and for 64 of 8192 in e4m3 278 against 195.
 constexpr int kFewKeys = 32;
-constexpr int kMinPart = 128;  // keys of a part at least
+constexpr int kMinPart = 128;  // keys of a part at least: 64 and 256 take 10.4 and 10.3 us for one of 1570 against 9.9
 template <int DP, bool FP8>
 constexpr int few_tile() { return kFewKeys * DP * (FP8 ? 1 : 2); }  // bytes of K, and of V
 template <int DP, bool FP8>
@@ -634,7 +639,13 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
 // head), 32 per wave, and a part of their keys; K and V tiles are double buffered in LDS.  Either four row
 // blocks share the key tiles (KS = 1: 128 rows), or two do and two waves each take every other tile, their sums
 // being joined in LDS at the end (KS = 2: 64 rows; half the time per workgroup for twice as many, where
-// 128 rows leave CUs idle).
+// 128 rows leave CUs idle).  32 rows a wave: its sums, queries and scores take 240 registers at 128 dims, so that two
+// waves of a SIMD cover each other's waits.  K's and V's fragments come from LDS at the rate that the products
+// take them.
+//
+// Measured, 16 heads on 2 of 128 dims: a chunk of 4096 tokens behind 12288, 480 us, 1.0 PFLOP/s (a library f16 product
+// of 8192^3: 1.1); a prompt of 1570, 29.6 us, of which the longest workgroup's 25 turns of 64 keys take 25.  8 heads
+// on 4 of 256 dims, 4096 tokens behind 4096: 267 us, 0.77 PFLOP/s, one wave a SIMD.
 constexpr int kManyWaves = 4;
 template <int DP, int KS>
 constexpr int many_keys() { return DP == 256 || KS == 2 ? 32 : 64; }  // of a key tile
@@ -1304,7 +1315,8 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
 // A row whose keys were in several parts: with M = max m, the sum of 2^(m_s - M) (sums_s, l_s).  Parts come
 // in batches, running as in the kernels above, so that a batch's loads are in flight together.  Bound:
 // latency (head, then the parts).  A workgroup of four waves takes one row, a quarter of the parts
-// each (WIDE), or a row per wave.
+// each (WIDE), or a row per wave.  3.5 us for 13 parts of one token's 16 rows of 128 dims, 5.2 for 32 parts of 512
+// rows.
 template <bool FEW, bool WIDE, int EL>
 __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
   typedef float vec __attribute__((ext_vector_type(EL)));
@@ -1394,11 +1406,16 @@ struct Launch {
 
 constexpr int kCus = 256;
 
-// Workgroups of the decode kernel that a CU holds.
-int few_slots(const AttnArgs& a) {
+// The decode kernel's workgroups that a CU holds, and their waves.
+struct FewShape {
+  int per_cu, waves;
+};
+template <int DP, bool FP8>
+FewShape few_shape() { return {few_per_cu<DP, FP8>(), few_waves<DP, FP8>()}; }
+FewShape few_shape_of(const AttnArgs& a) {
   const int d = a.c.dim;
-  return a.c.e4m3 ? d <= 64 ? few_per_cu<64, true>() : d <= 128 ? few_per_cu<128, true>() : few_per_cu<256, true>()
-                  : d <= 64 ? few_per_cu<64, false>() : d <= 128 ? few_per_cu<128, false>() : few_per_cu<256, false>();
+  return a.c.e4m3 ? d <= 64 ? few_shape<64, true>() : d <= 128 ? few_shape<128, true>() : few_shape<256, true>()
+                  : d <= 64 ? few_shape<64, false>() : d <= 128 ? few_shape<128, false>() : few_shape<256, false>();
 }
 
 Launch plan(const AttnArgs& a) {
@@ -1413,10 +1430,15 @@ Launch plan(const AttnArgs& a) {
     // at most: 16 tokens' window, from a multiple of 16
     const int64_t keys = a.window ? std::min(most, (int64_t)a.window + 2 * kFewRows) : most;
     x.few_rows = (int)std::min<int64_t>(kFewRows, (int64_t)a.max_q * G);
-    if (keys > kMinPart) {
+    // A workgroup per (sequence, kv head) and no join while its waves have three tiles each (250 keys of 2 kv heads:
+    // 8.1 us against 10.1, 500: 11.0 and 9.6), or 16 and there is a wave for every SIMD without parts (64 equal
+    // sequences of 1000 on 8 kv heads 49.5 us against 58.7; of 1 to 2000, 58.2 and 65.5).
+    const FewShape shape = few_shape_of(a);
+    const int alone = (int64_t)a.B * a.c.heads * shape.waves >= 4 * kCus ? 16 : 3;
+    if (keys > (int64_t)alone * kFewKeys * shape.waves) {
       // one round of the workgroups that the CUs hold, in parts of equal length (their number exceeds
       // few_splits by at most one per sequence); with more sequences than that, two parts each, for balance
-      const int slots = kCus * few_slots(a) / a.c.heads;
+      const int slots = kCus * shape.per_cu / a.c.heads;
       x.few_splits = std::max(slots - a.B, 2 * a.B);
       // (keys + per - 1) / per parts of each sequence at most
       x.few_parts = (int)std::min<int64_t>((int64_t)x.few_splits + a.B, a.B * ((keys + kMinPart - 1) / kMinPart));

@@ -149,3 +149,17 @@ def test_append_and_attention_on_another_stream(w4):  # noqa: F811
             got.append(run(*x))
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("hq,hkv,d,e4m3", [(4, 2, 64, False), (2, 1, 256, False), (2, 2, 128, True)])
+@pytest.mark.parametrize("b", [129, 300, 700])
+def test_many_sequences_and_long_ones(w4, b, hq, hkv, d, e4m3):  # noqa: F811
+    # the keys of all sequences are dealt out in parts, to workgroups that look at one or several sequences a thread
+    rng = np.random.default_rng(b + d)
+    kv = rng.integers(0, 40, b)
+    kv[[0, b // 2, b - 1]] = 300, 2500, 1100
+    s = Setup([(1, int(x)) for x in kv], hq, hkv, d, 16, e4m3, seed=b)
+    s.check(s.run(w4))
+    lens = [(int(a), int(a + x)) for a, x in zip(rng.integers(0, 3, b), kv)]
+    s = Setup(lens, hq, hkv, d, 16, e4m3, seed=b + 1)
+    s.check(s.run(w4))
