@@ -122,6 +122,7 @@ struct Plan {
   Divider page, group;
   int G;
   int splits;       // few rows: parts of the keys of all sequences, about; many rows: of a row tile, at most
+  int least;        // few rows: keys of a part at least
   int tiles;        // many rows: row tiles at most
   int part_rows;    // rows kept of a part; many rows: of a row tile
   bool skip_short;  // both kernels run: sequences of at most kFewRows rows are the first one's
@@ -264,7 +265,7 @@ __device__ __forceinline__ int few_parts(const FewKeys& k, int per) {
 
 // Keys of a part, about, where all sequences have `all`.
 __device__ __forceinline__ int part_keys(const Plan& p, int64_t all) {
-  return (int)min((int64_t)1 << 30, max((int64_t)kMinPart, (all + p.splits - 1) / p.splits + kFewKeys - 1)) & ~(kFewKeys - 1);
+  return (int)min((int64_t)1 << 30, max((int64_t)p.least, (all + p.splits - 1) / p.splits + kFewKeys - 1)) & ~(kFewKeys - 1);
 }
 
 // Sum over the workgroup, and over the threads before this one.
@@ -1399,7 +1400,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
 // they may differ.
 struct Launch {
   bool few, many;
-  int few_splits, few_parts, few_rows;  // few_parts 0: one workgroup per (sequence, kv head), no parts
+  int few_splits, few_parts, few_rows, few_least;  // few_parts 0: one workgroup per (sequence, kv head), no parts
   int many_splits, many_rows, tiles;
   size_t few_bytes, many_bytes;
 };
@@ -1441,7 +1442,11 @@ Launch plan(const AttnArgs& a) {
       const int slots = kCus * shape.per_cu / a.c.heads;
       x.few_splits = std::max(slots - a.B, 2 * a.B);
       // (keys + per - 1) / per parts of each sequence at most
-      x.few_parts = (int)std::min<int64_t>((int64_t)x.few_splits + a.B, a.B * ((keys + kMinPart - 1) / kMinPart));
+      // Two tiles of each of four waves where one would make more than a workgroup a CU: one sequence of 20000 on 2 kv
+      // heads 16.0 us against 20.0, 8 of 4096 with two rows each 15.8 and 17.3; with two waves (3 of 1500, 256 dims,
+      // 8 kv heads) 22.9 and 20.4.
+      x.few_least = shape.waves == 4 && a.B * ((keys + kMinPart - 1) / kMinPart) * a.c.heads > kCus ? 2 * kMinPart : kMinPart;
+      x.few_parts = (int)std::min<int64_t>((int64_t)x.few_splits + a.B, a.B * ((keys + x.few_least - 1) / x.few_least));
       x.few_bytes = (size_t)a.B * sizeof(int4) + (size_t)x.few_parts * a.c.heads * x.few_rows * row;
     }
   }
@@ -1521,7 +1526,7 @@ template <bool FP8>
 void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
   const int D = p.a.c.dim, heads = p.a.c.heads;
   if (x.few) {
-    p.splits = x.few_splits, p.part_rows = x.few_rows;
+    p.splits = x.few_splits, p.least = x.few_least, p.part_rows = x.few_rows;
     p.head = reinterpret_cast<int4*>(ws);
     p.part = x.few_parts ? reinterpret_cast<float*>(ws + (size_t)p.a.B * sizeof(int4)) : nullptr;
     const int items = (x.few_parts ? x.few_parts : p.a.B) * heads;
