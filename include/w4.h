@@ -332,10 +332,11 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
  * Scores, the softmax and its sums are f32; the weights are rounded before their product with v, to
  * 22 bits where max_q * Hq / heads <= 16, to f16 (or 22 bits) elsewhere; the result once to f16.
  * Requires B, W, max_q >= 1, T < 2^24, B <= 2^20, B <= T when q_start is NULL, max_q <= T,
- * 1 <= Hq <= 1024, Hq % heads == 0, T * Hq <= 2^30, W * page_size <= 2^30, ldt >= W, window >= 0, scale > 0 and finite,
+ * 1 <= Hq <= 1024, Hq % heads == 0, T * Hq <= 2^30, W * page_size <= 2^30, ldt >= W, window >= 0, 1e-30 <= scale <= 1e30,
  * ldq, ldo >= Hq * dim and multiples of 8; q, out 16-byte aligned, the int32 arrays 4-byte.  The cache:
  * see w4_kv_cache.  Workspace (query it): partial results where the keys of a row are split over
- * workgroups; contents need no initialisation.  Deterministic.
+ * workgroups; contents need no initialisation; calls that may run at the same time need one each.
+ * Deterministic.
  */
 int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
                     int64_t W, const int32_t* kv_len, const int32_t* q_start, int64_t B, int64_t T, int64_t max_q,

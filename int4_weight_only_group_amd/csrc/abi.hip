@@ -432,7 +432,8 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
     if (T < 1 || T >= kMaxTokens || B < 1 || B > ((int64_t)1 << 20) || max_q < 1 || max_q > T) return W4_ERR_SHAPE;
     if (!q_start && (B > T || max_q != 1)) return W4_ERR_SHAPE;
     if (W < 1 || W > ((int64_t)1 << 30) / c.page_size || ldt < W || ldt > kMaxDim) return W4_ERR_SHAPE;
-    if (Hq < 1 || Hq % c.heads != 0 || Hq > kMaxHeads || T * Hq > kMaxDim || window < 0 || !(scale > 0.f) || !std::isfinite(scale)) return W4_ERR_SHAPE;
+    if (Hq < 1 || Hq % c.heads != 0 || Hq > kMaxHeads || T * Hq > kMaxDim || window < 0) return W4_ERR_SHAPE;
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return W4_ERR_SHAPE;  // its product with log2 e and the scales stays normal
     if (int e = check_rows(q, ldq, Hq, c.dim)) return e;
     if (int e = check_rows(out, ldo, Hq, c.dim)) return e;
     if (!al4(table) || !al4(kv_len) || !al4(q_start)) return W4_ERR_ALIGN;

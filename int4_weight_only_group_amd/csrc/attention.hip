@@ -658,8 +658,8 @@ template <int DP>
 constexpr int many_per_cu() { return DP == 256 ? 1 : 2; }
 
 __device__ __forceinline__ int tiles_of(const Plan& p, int n) {
-  const int rows = n * p.G;
-  return p.skip_short && rows <= kFewRows ? 0 : (rows + p.part_rows - 1) / p.part_rows;
+  if (p.skip_short && n * p.G <= kFewRows) return 0;
+  return (min(n, p.a.max_q) * p.G + p.part_rows - 1) / p.part_rows;  // the launch has tiles for max_q tokens each
 }
 
 // The sequence and tile of the tile-th row tile of the batch; b = -1 past the last.  64 sequences at a

@@ -122,3 +122,10 @@ def test_no_device_is_an_error():
     assert append() == DEVICE
     assert append(q=None, qo=None, Hq=0, ldq=0, ldqo=0) == DEVICE
     assert append(c=cache(type=E4M3, k_scale=P, v_scale=P)) == DEVICE
+
+
+def test_attention_scale_keeps_its_products_normal():
+    for bad in (1e-31, 1e-45, 1e31, 3e38):
+        assert attend(scale=bad) == SHAPE, bad
+    n = ctypes.c_size_t(0)
+    assert attend(scale=1e-30, size=n) == OK and attend(scale=9.9e29, size=n) == OK

@@ -163,3 +163,15 @@ def test_many_sequences_and_long_ones(w4, b, hq, hkv, d, e4m3):  # noqa: F811
     lens = [(int(a), int(a + x)) for a, x in zip(rng.integers(0, 3, b), kv)]
     s = Setup(lens, hq, hkv, d, 16, e4m3, seed=b + 1)
     s.check(s.run(w4))
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (2, 2, 128), (16, 2, 256)])
+def test_a_sequence_longer_than_max_q_leaves_the_others_theirs(w4, hq, hkv, d):  # noqa: F811
+    # rows past max_q of a sequence are unspecified; the first max_q of each are right
+    for lens, max_q in (([(300, 300), (50, 70), (60, 60), (2, 90)], 60), ([(40, 900), (1, 700), (1, 3)], 1),
+                        ([(90, 95), (3, 40), (200, 210)], 3)):
+        s = Setup(lens, hq, hkv, d, 16, seed=d)
+        got = s.run(w4, max_q=max_q).cpu().numpy().astype(np.float64)
+        want, size, wobble = s.want()
+        keep = np.concatenate([a + np.arange(min(n, max_q)) for a, (n, _) in zip(s.starts, lens)])
+        assert (np.abs(got - want) <= s.bound(want, size, wobble))[keep].all()
