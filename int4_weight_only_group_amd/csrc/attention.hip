@@ -959,7 +959,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
   const int64_t step_bytes = (int64_t)RPI * g.c.stride_token * ES;  // between the rows of two loads
   int64_t offsets = 0;  // lane i: of tile batch + i; -1: a page outside the cache
   int batch = -64;
-  auto offset_of = [&](int i) W4_INLINE {
+  auto offset_of = [&](int i) W4_INLINE {  // k1 > 0
     if ((i & ~63) != batch) {
       batch = i & ~63;
       const int jw = k0 + tile_at(batch + lane) * KT + RW * rg, j = min(jw, k1 - 1);
@@ -1063,14 +1063,15 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
     held_v = i;
     return ready(i, V_, off);
   };
+  // a tile that is not there has no offset: with no keys at all (k1 = 0), not even of the table's first page
   auto get_k = [&](int i) W4_INLINE {
-    if (start_k(i, plain ? offset_of(i) : 0)) {
+    if (there(i) && start_k(i, plain ? offset_of(i) : 0)) {
 #pragma unroll
       for (int x = 0; x < NI; ++x) fetch_one(K_, x);
     }
   };
   auto get_v = [&](int i) W4_INLINE {
-    if (start_v(i, plain ? offset_of(i) : 0)) {
+    if (there(i) && start_v(i, plain ? offset_of(i) : 0)) {
 #pragma unroll
       for (int x = 0; x < NI; ++x) fetch_one(V_, x);
     }
