@@ -333,8 +333,9 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
  * 22 bits where max_q * Hq / heads <= 16, to f16 (or 22 bits) elsewhere; the result once to f16.
  * Requires B, W, max_q >= 1, T < 2^24, B <= 2^20, B <= T when q_start is NULL, max_q <= T,
  * 1 <= Hq <= 1024, Hq % heads == 0, T * Hq <= 2^30, W * page_size <= 2^30, ldt >= W, window >= 0, 1e-30 <= scale <= 1e30,
- * ldq, ldo >= Hq * dim and multiples of 8; q, out 16-byte aligned, the int32 arrays 4-byte.  The cache:
- * see w4_kv_cache.  Workspace (query it): partial results where the keys of a row are split over
+ * ldq, ldo >= Hq * dim and multiples of 8; q, out 16-byte aligned, the int32 arrays 4-byte; and no
+ * more work than a launch holds, 2^32 threads: always so while B * heads < 2^20 and T * Hq <= 2^29.
+ * The cache: see w4_kv_cache.  Workspace (query it): partial results where the keys of a row are split over
  * workgroups; contents need no initialisation; calls that may run at the same time need one each.
  * Deterministic.
  */

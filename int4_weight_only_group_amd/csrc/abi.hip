@@ -443,7 +443,8 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
     a.W = (int)W, a.B = (int)B, a.T = (int)T, a.max_q = (int)max_q, a.Hq = (int)Hq;
     a.window = window >= ((int64_t)1 << 30) ? 0 : (int)window;  // no sequence is longer
     a.scale = scale;
-    const size_t need = w4::attention_ws_bytes(a);
+    size_t need = 0;
+    if (!w4::attention_ws_bytes(a, need)) return W4_ERR_SHAPE;
     const int w = workspace(ws, ws_bytes, need);
     if (w < 0) return w;
     if (w == 1) return W4_OK;

@@ -1485,6 +1485,17 @@ Launch plan(const AttnArgs& a) {
   return x;
 }
 
+// Whether every launch stays below 2^32 threads, which is as many as one takes.
+bool launchable(const Launch& x, const AttnArgs& a) {
+  constexpr int64_t kMost = ((int64_t)1 << 32) / 256;  // workgroups
+  const int64_t heads = a.c.heads;
+  if (x.few) {
+    if ((x.few_parts ? x.few_parts : a.B) * heads >= kMost) return false;
+    if (x.few_parts && a.B * heads * x.few_rows >= kMost) return false;
+  }
+  return !x.many || x.tiles * heads * x.many_splits < kMost;  // parts are for few tiles: their join is small
+}
+
 template <int DP, bool FP8>
 void launch_few(const Plan& p, int items, hipStream_t st) {
   static std::once_flag flags[kMaxDevices];
@@ -1553,9 +1564,10 @@ void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
 
 }  // namespace
 
-size_t attention_ws_bytes(const AttnArgs& a) {
+bool attention_ws_bytes(const AttnArgs& a, size_t& bytes) {
   const Launch x = plan(a);
-  return x.few_bytes + x.many_bytes;
+  bytes = x.few_bytes + x.many_bytes;
+  return launchable(x, a);
 }
 
 void launch_attention(const AttnArgs& a, void* ws, hipStream_t st) {

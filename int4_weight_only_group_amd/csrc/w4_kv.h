@@ -37,7 +37,7 @@ struct AttnArgs {
   int W, B, T, max_q, Hq, window;
   float scale;
 };
-size_t attention_ws_bytes(const AttnArgs& a);
+bool attention_ws_bytes(const AttnArgs& a, size_t& bytes);  // false: no launch holds so many workgroups
 void launch_attention(const AttnArgs& a, void* ws, hipStream_t st);
 
 }  // namespace w4

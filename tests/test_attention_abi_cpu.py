@@ -129,3 +129,29 @@ def test_attention_scale_keeps_its_products_normal():
         assert attend(scale=bad) == SHAPE, bad
     n = ctypes.c_size_t(0)
     assert attend(scale=1e-30, size=n) == OK and attend(scale=9.9e29, size=n) == OK
+
+
+def _size(heads, G, dim=8, **kw):
+    # the size query of a call; strides as of a [pages][heads][16][dim] cache
+    n = ctypes.c_size_t(1)
+    c = cache(heads=heads, dim=dim, stride_page=heads * 16 * dim, stride_head=16 * dim, stride_token=dim)
+    ld = heads * G * dim
+    return attend(c=c, size=n, ldq=ld, ldo=ld, Hq=heads * G, **{**dict(ldt=1 << 16, W=1 << 16), **kw}), n.value
+
+
+def test_calls_that_no_launch_holds():
+    # a launch has fewer than 2^32 threads, of workgroups of up to 256
+    n = 1 << 20
+    for heads, G, kw in (
+            (1024, 1, dict(B=n, T=n, max_q=1, q_start=None)),  # parts (3 * 2^30 of them: past an int) and join
+            (1024, 1, dict(B=n, T=n, max_q=1, q_start=None, W=1)),  # a workgroup per sequence and kv head
+            (8, 16, dict(B=1 << 18, T=1 << 18, max_q=1, q_start=None)),  # the join's 16 rows of 2^21 pairs alone
+            (16, 1, dict(B=n, T=n, max_q=2, W=1)),  # short ones beside others
+            (1024, 1, dict(B=n, T=n, max_q=n)), (64, 17, dict(B=n - 1, T=n - 1, max_q=1 << 19))):  # tiles of many rows
+        assert _size(heads, G, **kw)[0] == SHAPE, (heads, G, kw)
+    # w4.h: taken while B * heads < 2^20 and T * Hq <= 2^29
+    for heads, G, kw in (
+            (1, 16, dict(B=n - 1, T=n - 1, max_q=1, q_start=None)), (1023, 1, dict(B=1025, T=1 << 19, max_q=512)),
+            (1, 512, dict(B=n - 1, T=n, max_q=n)), (1, 1, dict(B=n - 1, T=n, max_q=2, W=2)),
+            (1024, 1, dict(B=1023, T=1 << 19, max_q=1 << 19, W=2))):
+        assert _size(heads, G, **kw)[0] == OK, (heads, G, kw)
