@@ -4,6 +4,7 @@ Bounds as in test_gpu_attention.py unless stated."""
 
 from __future__ import annotations
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -23,3 +24,81 @@ def test_row_tiles_that_see_no_key(w4, hq, hkv, d, e4m3, page):  # noqa: F811
         s = Setup(lens, hq, hkv, d, page, e4m3, seed=d + page)
         print(lens, window, flush=True)
         s.check(s.run(w4, window=window), window=window)
+
+
+def _cache_of(k, v, page=16):
+    # [keys][dim] of one kv head as caches of whole pages, and their table, pages in another order
+    n, d = k.shape
+    order = np.random.default_rng(n).permutation(-(-n // page))
+    caches = []
+    for x in (k, v):
+        c = np.zeros((len(order) * page, d), dtype=np.float16)
+        c[:n] = x
+        y = np.empty((len(order), 1, page, d), dtype=np.float16)
+        y[order, 0] = c.reshape(-1, page, d)
+        caches.append(dev(y))
+    return caches, dev(order[None].astype(np.int32))
+
+
+def _attend(w4, q, caches, table, n, **kw):  # noqa: F811
+    return w4.attention_paged(dev(q), *caches, table, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                              q_start=torch.tensor([0, len(q)], dtype=torch.int32, device="cuda"), max_q=len(q),
+                              **kw).cpu().numpy().astype(np.float64)
+
+
+def _one_dim(q0, s, t, hq, d=64):
+    # q and k of one nonzero dim, so that a score is one exact product: every key's is s[key], for rows of q0
+    q, k = np.zeros((t, hq, d), dtype=np.float16), np.zeros((len(s), d), dtype=np.float16)
+    q[:, :, 0], k[:, 0] = q0, np.asarray(s) / q0
+    return q, k
+
+
+@pytest.mark.parametrize("t,n", [(1, 131072), (3, 131072), (40, 131072), (300, 131072), (1, 300), (5, 900), (90, 900)])
+@pytest.mark.parametrize("below", [11.5, 17.4, 20.0])
+def test_many_small_weights_beside_a_large_one(w4, t, n, below):  # noqa: F811
+    # one key, whose value is 0, has nearly all the weight; the others lie `below` nats under it and make up the result.
+    # The first row (of the last position all rows see all keys but the last t) sees n - t + 1 keys.
+    # Bound, relative to the result: weights to f16, 2^-11 each, or to half of f16's smallest step, 2^-25, which is 2^-36 of
+    # the largest weight, 2^11; the result to f16, 2^-11 or 2^-25; scores exact but for three roundings of 2^-24 * |s| in
+    # their product with scale * log2 e; exp2 2^-20; sums in f32, 2^-23 a block of 16 keys and 32 more.
+    rng = np.random.default_rng(t + n)
+    at = n // 3
+    s = np.round(rng.uniform(-1.0, 1.0, n) * 256) / 256  # exact in f16, as are their halves
+    s[at] = round((below + 1) * 16) / 16
+    q, k = _one_dim(2.0, s, t, 2)
+    v = (rng.uniform(0.5, 2.0, (n, 64)) * 4096).astype(np.float16)
+    v[at] = 0
+    got = _attend(w4, q, *_cache_of(k, v), n, scale=1.0)
+    s64 = 2.0 * k[:, 0].astype(np.float64)
+    w = np.exp(s64 - s64[at])
+    sums, total = np.cumsum(w[:, None] * v.astype(np.float64), 0), np.cumsum(w)
+    for i in range(t):
+        p = n - t + i
+        want = sums[p] / total[p]
+        rel = 2.0 ** -11 + 2.0 ** -11 + 2 * 3 * 2.0 ** -24 * s64[at] * 2 + 2.0 ** -20 + (n / 16 + 32) * 2.0 ** -23
+        assert (np.abs(got[i] - want) <= want * rel + n * 2.0 ** -36 * v.max().astype(np.float64) + 2.0 ** -25).all(), (i, np.abs(got[i] / want - 1).max())
+
+
+@pytest.mark.parametrize("n", [256, 5000])
+def test_few_rows_weigh_to_22_bits(w4, n):  # noqa: F811
+    # Two kinds of keys in turn, of weights 1 and x and values 1 and about -1 / x, so that they cancel: what is left is
+    # the weights' rounding, at the scale of 1.  One f16 a weight is off by up to 2^-12 of it, which the bound
+    # refuses for these x; two are off by 2^-22.  The scores' errors are two roundings of 2^-24 * |s| log2 e < 3.
+    for below in (0.3, 0.71, 1.37, 1.9):
+        s = np.zeros(n)
+        s[1::2] = -np.float64(np.float16(below))
+        q, k = _one_dim(1.0, s, 1, 4)
+        s64 = k[:, 0].astype(np.float64)
+        w = np.exp(s64)
+        v = np.ones((n, 64), dtype=np.float16)
+        v[1::2] = -np.float16(1 / w[1])
+        total = w.sum()
+        want = float((w * v[:, 0].astype(np.float64)).sum() / total)
+        size = float((w * np.abs(v[:, 0].astype(np.float64))).sum() / total)
+        bound = abs(want) * 2.0 ** -11 + 2.0 ** -25 + size * (2.0 ** -21 + 6 * 2.0 ** -23 + 2.0 ** -20 + (n / 16 + 32) * 2.0 ** -23)
+        one = np.float64(np.float16(w[1]))  # up to a power of two, the kernel's x in one f16
+        off = abs(((w[::2] * v[::2, 0]).sum() + (one * v[1::2, 0].astype(np.float64)).sum()) / (w[::2].sum() + one * (n // 2)) - want)
+        if n == 256:
+            assert off > 2 * bound, (off, bound)  # the test tells one f16 from two
+        got = _attend(w4, q, *_cache_of(k, v), n, scale=1.0)
+        assert (np.abs(got - want) <= bound).all(), (below, np.abs(got - want).max(), bound)
