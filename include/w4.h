@@ -331,7 +331,9 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
  * max_q: no sequence has more rows (1: decode); rows past it in a sequence are unspecified.
  * Scores, the softmax and its sums are f32; the weights are rounded before their product with v, to
  * 22 bits where max_q * Hq / heads <= 16, to f16's 11 (or 22) bits elsewhere, either way to 2^-36 of
- * the largest weight; the result once to f16.
+ * the largest weight; the result once to f16.  A score is scale * q . k, times k_scale, as an f32: one
+ * past f32's range (2^127 / log2 e) is an infinity, and the rows that see it are NaN.  scale * k_scale[head]
+ * has to be at most 1e30, and may be as small as it likes.
  * Requires B, W, max_q >= 1, T < 2^24, B <= 2^20, B <= T when q_start is NULL, max_q <= T,
  * 1 <= Hq <= 1024, Hq % heads == 0, T * Hq <= 2^30, W * page_size <= 2^30, ldt >= W, window >= 0, 1e-30 <= scale <= 1e30,
  * ldq, ldo >= Hq * dim and multiples of 8; q, out 16-byte aligned, the int32 arrays 4-byte; and no

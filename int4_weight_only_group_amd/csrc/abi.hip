@@ -433,7 +433,7 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
     if (!q_start && (B > T || max_q != 1)) return W4_ERR_SHAPE;
     if (W < 1 || W > ((int64_t)1 << 30) / c.page_size || ldt < W || ldt > kMaxDim) return W4_ERR_SHAPE;
     if (Hq < 1 || Hq % c.heads != 0 || Hq > kMaxHeads || T * Hq > kMaxDim || window < 0) return W4_ERR_SHAPE;
-    if (!(scale >= 1e-30f && scale <= 1e30f)) return W4_ERR_SHAPE;  // its product with log2 e and the scales stays normal
+    if (!(scale >= 1e-30f && scale <= 1e30f)) return W4_ERR_SHAPE;  // its product with log2 e is a normal number
     if (int e = check_rows(q, ldq, Hq, c.dim)) return e;
     if (int e = check_rows(out, ldo, Hq, c.dim)) return e;
     if (!al4(table) || !al4(kv_len) || !al4(q_start)) return W4_ERR_ALIGN;

@@ -49,6 +49,15 @@ constexpr float kLog2e = 1.44269504088896340736f;
 // f16's rounding takes 2^-36 of it at most from weights below f16's normal range: many keys far below one still
 // add up right.  (Slack 8 and lift 0, 7 or slack 4 and lift 11 take the same time in every case.)
 constexpr float kSlack = 4.f, kLift = 11.f;
+// A score, rounded.  Fused with the subtraction of m, the product would not be, while m comes from a rounded one: from 2^23
+// on (in powers of two) a weight could then exceed f16, and from 2^27 on vanish or be infinite.  So this is a
+// multiplication more per score than a fused one: 503 us against 491 for the chunk of 4096, 120.6 against 118.4 for the
+// windowed ragged batch, 31.1 against 30.5 for the 1570-token prompt, the same for decodes.
+__device__ __forceinline__ float score(float s, float c) {
+  float x = s * c;
+  asm("" : "+v"(x));
+  return x;
+}
 // whether m has to move for a score of top (not for one of -infinity before there is an m), and where to
 __device__ __forceinline__ bool above(float top, float m) { return top - m > kLift + kSlack; }
 __device__ __forceinline__ float moved(float top, float m) { return fmaxf(m, top - kLift); }
@@ -522,6 +531,10 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
     }
     // sc[kb][e]: key j0 + 16 kb + 4 grp + e of this lane's row
     const bool edge = j0 + KT > all1 || j0 < all0;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sc[kb][e] = score(sc[kb][e], c);
     if (edge) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -534,7 +547,6 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
     float top = -INFINITY;
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(sc[0][e], sc[1][e]));
-    top *= c;
     if (__any(above(top, m))) {
       const float mn = moved(across<true>(top, fmax2), m);
       const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
@@ -550,7 +562,7 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = __builtin_amdgcn_exp2f(sc[kb][e] * c - ms);
+        const float x = __builtin_amdgcn_exp2f(sc[kb][e] - ms);
         const f16 high = (f16)x;
         l += x;
         w[4 * kb + e] = high;
@@ -795,8 +807,8 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
   // the sums are rescaled after the products of u - 1).  Slices of four products carry their share of
   // the VALU work, fragments are read two slices ahead, and between(x) follows slice x.  l sums the
   // weights as rounded, which are the ones that multiply v.  One f16 a weight makes the result's error 2.9e-4 of its norm
-  // where its own rounding to f16 is 2.1e-4; two, as for few rows, would make it 2.1e-4 and take 705 us in place of
-  // 494 for the chunk of 4096, 35.7 in place of 29.9 for the 1570-token prompt.
+  // where its own rounding to f16 is 2.1e-4; two, as for few rows, would make it 2.1e-4 and take 43 % longer
+  // for the chunk of 4096, 19 % for the 1570-token prompt.
   f32x16 sc;
   f16x8 w[2];
   float ms = 0.f, top = 0.f;  // ms: m, or 0 before there is one
@@ -806,7 +818,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
     for (int e = 0; e < 5; ++e) y[e] = fmaxf(fmaxf(x[3 * e], x[3 * e + 1]), x[3 * e + 2]);
     y[0] = fmaxf(fmaxf(y[0], y[1]), x[15]);
     y[2] = fmaxf(fmaxf(y[2], y[3]), y[4]);
-    return fmaxf(y[0], y[2]) * c;
+    return score(fmaxf(y[0], y[2]), c);
   };
   constexpr int SLICES = STEPS / 2, EACH = 16 / SLICES;
   f16x8 frags[3][4];  // of three slices in turn
@@ -861,7 +873,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
       if (x > 0) round_to(x - 1);
 #pragma unroll
       for (int e = EACH * x; e < EACH * (x + 1); ++e) {
-        y[e] = __builtin_amdgcn_exp2f(sc[e] * c - ms);
+        y[e] = __builtin_amdgcn_exp2f(score(sc[e], c) - ms);
         asm volatile("" : "+v"(y[e]));  // in this slice: the compiler would move it behind the last branch
       }
       if constexpr (QK)
@@ -911,10 +923,10 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
 #pragma unroll
       for (int e = 0; e < 16; ++e) {  // key j0 + 8 (e / 4) + 4 h + e % 4 of this lane's row
         const int j = j0 + 8 * (e >> 2) + 4 * h + (e & 3);
-        sc[e] = j >= see0 && j < see1 ? sc[e] : -INFINITY;
+        sc[e] = j >= see0 && j < see1 ? score(sc[e], c) : -INFINITY;
         top = fmaxf(top, sc[e]);
       }
-      top = across<false>(top, fmax2) * c;
+      top = across<false>(top, fmax2);
       if (__any(above(top, m))) {
         const float mn = moved(top, m), f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
         l *= f;
@@ -927,7 +939,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        w[e >> 3][e & 7] = (f16)__builtin_amdgcn_exp2f(sc[e] * c - ms);
+        w[e >> 3][e & 7] = (f16)__builtin_amdgcn_exp2f(sc[e] - ms);
         l += (float)w[e >> 3][e & 7];
       }
       uint32_t odd = 0;

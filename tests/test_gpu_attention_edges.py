@@ -102,3 +102,45 @@ def test_few_rows_weigh_to_22_bits(w4, n):  # noqa: F811
             assert off > 2 * bound, (off, bound)  # the test tells one f16 from two
         got = _attend(w4, q, *_cache_of(k, v), n, scale=1.0)
         assert (np.abs(got - want) <= bound).all(), (below, np.abs(got - want).max(), bound)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "mixed"])
+@pytest.mark.parametrize("scale", [1.0, 1e4, 1e20, 1e30])
+def test_scores_far_from_zero(w4, scale, order):  # noqa: F811
+    # Integer keys on one dim, so that a product q . k is exact; the rows of four heads multiply them by 1/64, 1, 32768 and
+    # -32768: rows beside each other with scores of up to 2^26 * scale, all of one sign, and small ones.
+    # Bound: the result and the weights to f16; a weight is off by 6 * 2^-24 of the largest score in nats, unless the
+    # next one lies more than 100 nats below the largest (then all of the weight is its own).
+    q0 = np.array([1 / 64, 1.0, 32768.0, -32768.0])
+    for t, n in ((1, 40), (1, 1500), (4, 900), (90, 900), (300, 2000)):
+        rng = np.random.default_rng(n)
+        ints = rng.permutation(np.arange(1, n + 1))
+        ints = {"rising": np.sort(ints), "falling": np.sort(ints)[::-1], "mixed": ints}[order]
+        q, k = np.zeros((t, 4, 64), dtype=np.float16), np.zeros((n, 64), dtype=np.float16)
+        q[:, :, 0], k[:, 0] = q0, ints
+        v = rng.standard_normal((n, 64)).astype(np.float16)
+        got = _attend(w4, q, *_cache_of(k, v), n, scale=scale)
+        for i in range(t):
+            seen = n - t + i + 1
+            s = np.outer(q0, ints[:seen].astype(np.float64)) * scale
+            two = np.sort(s, 1)[:, -2:] if seen > 1 else np.array([[-np.inf, 0]] * 4)
+            w = np.exp(s - s.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            v64 = v[:seen].astype(np.float64)
+            want, size = w @ v64, w @ np.abs(v64)
+            off = np.where(two[:, 1] - two[:, 0] > 100, 0.0, 6 * 2.0 ** -24 * np.abs(s).max(1))[:, None]
+            bound = np.abs(want) * 2.0 ** -11 + 2.0 ** -25 + size * (
+                2.0 ** -11 + 2 * off + 2.0 ** -20 + (n / 16 + 32) * 2.0 ** -23) + n * 2.0 ** -36 * np.abs(v64).max()
+            err = np.abs(got[i] - want)
+            assert (err <= bound).all(), (t, n, i, (err / bound).max(1))
+
+
+@pytest.mark.parametrize("lens,window", [([(1, 300), (1, 1)], 0), ([(5, 1200)], 33), ([(150, 400), (40, 41)], 0),
+                                         ([(200, 700)], 100)])
+def test_scales_of_the_cache_far_from_one(w4, lens, window):  # noqa: F811
+    # the product of scale and k_scale, not each, is what a score takes: 1/300 from factors of 10^20; and down to nothing
+    # (2^-149 * 1e-30), where all keys weigh the same
+    for scale, k_scale in ((1e-20, 1e20 / 300), (1e20, 1e-20 / 300), (1e-30, 1e-20), (1e-30, 1e-38), (1e-30, 1e-45), (1.0, 1e-45)):
+        s = Setup(lens, 4, 2, 128, 16, True, seed=3)
+        s.scale_k = np.full(2, k_scale, dtype=np.float32)
+        s.check(s.run(w4, scale=scale, window=window), scale=scale, window=window)
