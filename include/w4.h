@@ -322,7 +322,7 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
  * Row i of a sequence with n rows stands at p = kv_len - n + i and sees the keys
  * max(0, p + 1 - window) <= j <= p (window 0: all of 0 .. p):
  *   out = sum_j softmax_j(scale * q . k_j) v_j.
- * A row that sees no key (kv_len < n, or 0) is 0.  Rows that belong to no sequence are left as
+ * A row that sees no key (kv_len < n, or 0) is 0; one that sees none but keys of score -infinity is NaN.  Rows that belong to no sequence are left as
  * they were.  What no row sees (pages past a sequence's end, tokens of a page past
  * it, tokens outside the window) does not reach the result, whatever it holds.  Lengths, starts
  * and the table are read on the device (a captured graph may be replayed as they grow) and kept

@@ -15,7 +15,8 @@
 // transposing LDS reads follow; the weights never leave their lane.
 //
 // Keys that no row of the workgroup sees are not read: zeros stand in for them (what a page holds
-// past its sequence's end may be anything).  A page number outside the cache gives NaN keys.
+// past its sequence's end may be anything).  A page number outside the cache gives NaN keys.  A row that sees no key is
+// 0; one that sees keys, all with scores of -infinity, has l = 0 and is NaN, as its softmax is.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -642,7 +643,7 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
       }
     } else {
       const int tk = divide(r, p.group);
-      const float f = lt == 0.f ? 0.f : vs / lt;
+      const float f = s.len - s.n + tk >= 0 ? vs / lt : 0.f;
       f16x4 h;
 #pragma unroll
       for (int e = 0; e < 4; ++e) h[e] = (f16)(o[e] * f);
@@ -1292,7 +1293,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
     __syncthreads();
     if (kg == 1) return;
   }
-  const float f = l == 0.f ? 0.f : (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+  const float f = see1 > 0 ? (FP8 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l : 0.f;
 #pragma unroll
   for (int d0 = 0; d0 < DP; d0 += DW) {
 #pragma unroll
@@ -1405,7 +1406,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
   }
   if (d >= D) return;
   const int row = r0 + r, tok = divide(row, p.group);
-  const float f = l == 0.f ? 0.f : (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l;
+  const float f = s.len - s.n + tok >= 0 ? (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l : 0.f;
   uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
   typedef uint16_t bits __attribute__((ext_vector_type(EL)));
   bits h;

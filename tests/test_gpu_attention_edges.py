@@ -144,3 +144,27 @@ def test_scales_of_the_cache_far_from_one(w4, lens, window):  # noqa: F811
         s = Setup(lens, 4, 2, 128, 16, True, seed=3)
         s.scale_k = np.full(2, k_scale, dtype=np.float32)
         s.check(s.run(w4, scale=scale, window=window), scale=scale, window=window)
+
+
+@pytest.mark.parametrize("lens,d", [([(1, 40), (1, 700)], 64), ([(1, 20000)], 128), ([(5, 9)], 64), ([(90, 300), (40, 41)], 128),
+                                    ([(300, 2000)], 128), ([(150, 400)], 256)])
+def test_rows_whose_scores_are_all_minus_infinity(w4, lens, d):  # noqa: F811
+    # no softmax: NaN, not the 0 of a row that sees nothing; a row that sees one finite key has that key's value
+    for ends in (lambda n, kv: kv, lambda n, kv: kv - n // 2 - 1):
+        s = Setup(lens, 4, 2, d, 16, seed=d)
+        s.q = np.abs(s.q) + np.float16(0.125)
+        want = np.full((s.q.shape[0], 4, d), np.nan)
+        for b, (n, kv) in enumerate(lens):
+            for j in range(kv):
+                s.host[0][s.table[b, j // 16], :, j % 16, 0] = -np.inf
+            j = ends(n, kv)  # the one finite key, if the sequence has it
+            if j < kv:
+                s.host[0][s.table[b, j // 16], :, j % 16, 0] = 1
+                v = s.host[1][s.table[b, j // 16], :, j % 16].astype(np.float64)
+                rows = np.arange(n)[kv - n + np.arange(n) >= j] + s.starts[b]
+                want[rows] = np.repeat(v, 2, 0)
+        s.dev = [s._place(c, "phtd") for c in s.host]
+        got = s.run(w4).cpu().numpy().astype(np.float64)
+        # a weight of 2^11 (or what it is rounded to) over its own sum: the value to 2^-22, rounded to f16
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert (np.abs(got - want) <= np.abs(want) * 2.0 ** -10)[~np.isnan(want)].all()
