@@ -168,3 +168,35 @@ def test_rows_whose_scores_are_all_minus_infinity(w4, lens, d):  # noqa: F811
         # a weight of 2^11 (or what it is rounded to) over its own sum: the value to 2^-22, rounded to f16
         assert np.array_equal(np.isnan(got), np.isnan(want))
         assert (np.abs(got - want) <= np.abs(want) * 2.0 ** -10)[~np.isnan(want)].all()
+
+
+def _workspace(w4, s, window, fill, max_q=None):  # noqa: F811
+    # exactly the bytes that the call needs, filled, and 4096 more behind them that are not the call's
+    need = w4.attention_workspace_bytes(s.dev[0], len(s.lens), s.q.shape[0], max_q or s.kw()["max_q"], s.hq,
+                                        s.table.shape[1], window)
+    ws = torch.full((need + 4096,), fill, dtype=torch.uint8, device="cuda")
+    return need, ws
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,page,window,e4m3", [
+    # single tokens: parts of one, of several sequences, of lengths 0 and 1 among long ones
+    ([(1, 1570)], 16, 2, 128, 16, 0, False), ([(1, 5000), (1, 1), (1, 0), (1, 33)], 16, 2, 128, 100, 0, False),
+    ([(1, 20011), (1, 3)], 2, 1, 64, 32, 0, True), ([(1, 3000), (1, 900)], 8, 4, 256, 16, 700, True),
+    ([(1, 10 * i) for i in range(70)] + [(1, 9000)], 4, 1, 64, 16, 0, False),
+    # rows of many tokens in few and in many parts, empty ones among them; both kinds together
+    ([(8, 1000), (8, 300)], 16, 2, 128, 16, 0, False), ([(600, 2000)], 2, 1, 128, 16, 0, False),
+    ([(200, 0), (3, 2000)], 4, 2, 64, 16, 0, False), ([(64, 6000)], 8, 1, 256, 16, 0, True),
+    ([(3, 9000), (2, 100)], 8, 1, 128, 16, 0, False), ([(130, 640), (3, 70), (0, 5), (20, 4)], 8, 2, 256, 64, 0, False),
+    ([(20, 2000), (1, 900), (1, 0)], 4, 2, 96, 5, 600, True),
+])
+def test_workspace_may_hold_anything(w4, lens, hq, hkv, d, page, window, e4m3):  # noqa: F811
+    s = Setup(lens, hq, hkv, d, page, e4m3, seed=d + len(lens))
+    first = None
+    for fill in (0xFF, 0x00, 0x7F):  # NaN and -1; 0; 3.4e38
+        need, ws = _workspace(w4, s, window, fill)
+        assert need > 0  # parts are kept there
+        got = s.run(w4, window=window, workspace=ws[:need])
+        s.check(got, window=window)
+        assert (ws[need:] == fill).all()
+        first = got if first is None else first
+        assert torch.equal(got, first)
