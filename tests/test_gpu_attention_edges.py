@@ -200,3 +200,66 @@ def test_workspace_may_hold_anything(w4, lens, hq, hkv, d, page, window, e4m3): 
         assert (ws[need:] == fill).all()
         first = got if first is None else first
         assert torch.equal(got, first)
+
+
+def _replays(w4, s, steps, window=0):  # noqa: F811
+    # two graphs of one call, which share a workspace, replayed while lengths and starts change; an eager call between
+    need, ws = _workspace(w4, s, window, 0xFF)
+    assert need > 0
+    q, table, kv_len, starts = dev(s.q), dev(s.table), dev(s.kv_len), dev(s.starts)
+    args = {**s.kw(), "q_start": starts}
+    outs = [torch.empty_like(q) for _ in range(2)]
+
+    def call(o, **kw):
+        w4.attention_paged(q, *s.dev, table, kv_len, window=window, out=o, **args, **kw)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(outs[0], workspace=ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            call(o, workspace=ws)
+    t = s.q.shape[0]
+    for i, lens in enumerate(steps):
+        s.lens = lens
+        s.starts = np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        s.kv_len = np.array([kv for _, kv in lens], dtype=np.int32)
+        kv_len.copy_(dev(s.kv_len))
+        starts.copy_(dev(s.starts))
+        for g, o in zip(graphs, outs):
+            o.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+        eager = torch.full_like(q, 7.0)
+        call(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], eager) and torch.equal(outs[1], eager), i
+        live = int(s.starts[-1])
+        assert (eager[live:] == 7).all()
+        whole, s.q = s.q, s.q[:live]
+        if live:
+            s.check(eager[:live], window=window)
+        s.q = whole
+    assert t == s.q.shape[0]
+
+
+@pytest.mark.parametrize("hq,hkv,d,e4m3,window", [(4, 2, 64, False, 0), (16, 2, 128, True, 0), (2, 1, 256, False, 900)])
+def test_captured_decode_replays_through_its_parts(w4, hq, hkv, d, e4m3, window):  # noqa: F811
+    # of one part and of many, with nothing and with everything cached, and back
+    s = Setup([(1, 3200), (1, 3200), (1, 3200)], hq, hkv, d, 16, e4m3, seed=d)
+    _replays(w4, s, [[(1, a), (1, b), (1, c)] for a, b, c in (
+        (30, 7, 1), (500, 1, 0), (3200, 0, 3200), (0, 0, 0), (1, 3200, 129), (128, 127, 256), (0, 1, 0), (2900, 3100, 40))], window)
+
+
+@pytest.mark.parametrize("hq,hkv,d,e4m3,window", [(4, 2, 64, False, 0), (8, 4, 128, True, 0), (2, 1, 256, False, 900)])
+@pytest.mark.parametrize("t", [100, 400])
+def test_captured_batches_replay_through_their_parts(w4, t, hq, hkv, d, e4m3, window):  # noqa: F811
+    # sequences of few rows and of many change places from replay to replay, and rows of no sequence are left
+    s = Setup([(t, 3200), (0, 3200), (0, 3200)], hq, hkv, d, 16, e4m3, seed=d + t)
+    _replays(w4, s, [
+        [(t - 10, 3000), (5, 2000), (5, 5)], [(1, 3200), (t - 2, t - 2), (1, 0)], [(t, 3200), (0, 9), (0, 0)],
+        [(t // 3, 20), (t // 3, 3200), (t // 4, 0)], [(0, 0), (0, 0), (0, 0)], [(2, 3000), (3, 1), (t - 5, 2900)],
+        [(8, 64), (9, 3200), (1, 1)]], window)
