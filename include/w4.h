@@ -329,6 +329,7 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
  * in bounds there: starts to 0 .. T, kv_len to 0 .. W * page_size; a page number outside the cache
  * is not read, and the rows that would see it are NaN.
  * max_q: no sequence has more rows (1: decode); rows past it in a sequence are unspecified.
+ * out may be q (ldo == ldq); no other overlap of what is written (out, ws) with what is read is allowed.
  * Scores, the softmax and its sums are f32; the weights are rounded before their product with v, to
  * 22 bits where max_q * Hq / heads <= 16, to f16's 11 (or 22) bits elsewhere, either way to 2^-36 of
  * the largest weight; the result once to f16.  A score is scale * q . k, times k_scale, as an f32: one

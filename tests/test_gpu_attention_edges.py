@@ -263,3 +263,16 @@ def test_captured_batches_replay_through_their_parts(w4, t, hq, hkv, d, e4m3, wi
         [(t - 10, 3000), (5, 2000), (5, 5)], [(1, 3200), (t - 2, t - 2), (1, 0)], [(t, 3200), (0, 9), (0, 0)],
         [(t // 3, 20), (t // 3, 3200), (t // 4, 0)], [(0, 0), (0, 0), (0, 0)], [(2, 3000), (3, 1), (t - 5, 2900)],
         [(8, 64), (9, 3200), (1, 1)]], window)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,e4m3", [
+    ([(1, 300), (1, 0), (1, 7000)], 16, 2, 128, False), ([(1, 200), (1, 9)], 8, 8, 64, True),
+    ([(300, 300)], 16, 2, 128, False), ([(64, 6000)], 8, 1, 256, True), ([(130, 640), (3, 2000), (1, 5)], 8, 2, 64, False)])
+def test_the_result_may_take_the_queries_place(w4, lens, hq, hkv, d, e4m3):  # noqa: F811
+    s = Setup(lens, hq, hkv, d, 16, e4m3, seed=d)
+    want = s.run(w4)
+    rows = torch.full((s.q.shape[0], hq + 2, d), 5.0, device="cuda", dtype=torch.float16)
+    q = rows[:, 1:hq + 1]
+    q.copy_(dev(s.q))
+    s.run(w4, q=q, out=q)
+    assert torch.equal(q, want) and (rows[:, 0] == 5).all() and (rows[:, hq + 1] == 5).all()
