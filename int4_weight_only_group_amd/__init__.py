@@ -654,7 +654,7 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     stands at p = kv_len - n + i and sees the keys max(0, p + 1 - window) .. p (window 0: from 0);
     scale defaults to dim ** -0.5.  max_q: the longest sequence's rows (default: T; give it, 1 for
     decode: it chooses the kernel).  Returns float16 [T][heads][dim]; a row that sees no key is 0,
-    rows past the last sequence are not written.  out may be q.  One is allocated for out and the workspace
+    rows past the last sequence are not written.  A table much wider than the sequences are long costs time.  out may be q.  One is allocated for out and the workspace
     (attention_workspace_bytes) when not given or too small."""
     dev = torch.cuda.current_device()
     c = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)

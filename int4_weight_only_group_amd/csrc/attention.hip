@@ -662,9 +662,9 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
 // waves of a SIMD cover each other's waits.  K's and V's fragments come from LDS at the rate that the products
 // take them.
 //
-// Measured, 16 heads on 2 of 128 dims: a chunk of 4096 tokens behind 12288, 480 us, 1.0 PFLOP/s (a library f16 product
-// of 8192^3: 1.1); a prompt of 1570, 29.6 us, of which the longest workgroup's 25 turns of 64 keys take 25.  8 heads
-// on 4 of 256 dims, 4096 tokens behind 4096: 267 us, 0.77 PFLOP/s, one wave a SIMD.
+// Measured, 16 heads on 2 of 128 dims: a chunk of 4096 tokens behind 12288, 501 us, 0.96 PFLOP/s (a library f16 product
+// of 8192^3: 1.1), 527 from an e4m3 cache; a prompt of 1570, 30.6 us, of which the longest workgroup's 25 turns of 64 keys
+// take 25, 38.3 from e4m3.  16 heads on 8 of 256 dims, 2048 tokens behind 6144: 293 us, 0.82 PFLOP/s, one wave a SIMD.
 constexpr int kManyWaves = 4;
 template <int DP, int KS>
 constexpr int many_keys() { return DP == 256 || KS == 2 ? 32 : 64; }  // of a key tile
@@ -973,7 +973,8 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
   // Pages of whole RW rows (and no padded dims): this wave's rows of a tile lie in one page, so their offset
   // from the base is scalar and a lane adds its row and chunk.  64 tiles' offsets are computed at once, one
   // per lane; the turn between two tiles then takes two lane reads.  (Scalar address arithmetic at every
-  // turn, and per-lane addresses the more so, cost more issue slots than the softmax.)
+  // turn, and per-lane addresses the more so, cost more issue slots than the softmax: 2048 tokens after 6144 take
+  // 152 us with pages of 16, 233 with pages of 8 or 100, and 232 at 80, 96 and 112 dims.)
   const bool plain = D == DP && g.c.page_size % RW == 0 && g.c.stride_token < (1 << 20);
   const uint32_t lane_row = (uint32_t)(lane / CH) * (uint32_t)g.c.stride_token * ES;
   const int64_t step_bytes = (int64_t)RPI * g.c.stride_token * ES;  // between the rows of two loads
@@ -1418,7 +1419,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
 // ------------------------------------------------------------------------------- the launch
 // Which kernels run: the one for few rows if no sequence has more than 16 rows, by max_q; the
 // other if all have the same number (or there is one): both, each leaving the other's sequences, when
-// they may differ.
+// they may differ.  So a single token of a group of more than 16 heads goes to the one for many: eight of 8192 tokens and one
+// kv head of 128 dims take 19.2 us with 32 heads, 22.8 with 64, and 16.0 with 16.
 struct Launch {
   bool few, many;
   int few_splits, few_parts, few_rows, few_least;  // few_parts 0: one workgroup per (sequence, kv head), no parts
@@ -1440,6 +1442,10 @@ FewShape few_shape_of(const AttnArgs& a) {
                   : d <= 64 ? few_shape<64, false>() : d <= 128 ? few_shape<128, false>() : few_shape<256, false>();
 }
 
+// Lengths are on the device, so that the table's width stands for every sequence's.  Where it is much wider than they
+// are, calls are cut for longer ones (16 heads on 2 of 128 dims, tables as wide as needed / of 1024 pages of 16): a
+// prompt of 1570 tokens 30.6 / 37.9 us (128 rows in two parts), 300 after 2000 27.7 / 30.3, one token after 200 8.1 /
+// 9.7, 64 after 1000 on 8 kv heads 42 / 50 (parts and a join), one after 1570, 4 x 8 after 16384 the same.
 Launch plan(const AttnArgs& a) {
   Launch x{};
   const int G = a.Hq / a.c.heads;
@@ -1475,8 +1481,9 @@ Launch plan(const AttnArgs& a) {
     auto row_tiles = [&](int rows) {  // at most: by all rows, and by max_q
       return std::min((int64_t)a.T * G / rows + std::min(a.B, a.T), a.B * (((int64_t)a.max_q * G + rows - 1) / rows));
     };
-    // Rows of a tile and parts of a row: what takes least by this sum, in us (its terms are measured; at 128 dims
-    // it is within a fifth of the whole).  A workgroup starts and ends in 5, and goes over 64 keys in `turn`, alone
+    // Rows of a tile and parts of a row: what takes least by this sum, in us.  Its terms are measured alone; the sum at 128
+    // dims is 35.6 for the 1570-token prompt (30.6 measured), 554 for the chunk of 4096 (501), 21.5 for 300
+    // tokens after 2000 (27.7), 18.3 for the drafts (26.9: the join grows with the parts).  A workgroup starts and ends in 5, and goes over 64 keys in `turn`, alone
     // or two on its CU; f32 parts are written and read at 4 TB/s, by one more launch.  Parts fill a round of
     // the workgroups that the CUs hold, or one for each CU: four sequences of 8 new tokens after 16384 (16 heads on 2)
     // take 29 us in 64 parts and 26 in 32, 256 new tokens 55 in 8 and 67 in 4; 200 after 2048 (32 on 8), 36 in
