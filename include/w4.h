@@ -195,7 +195,7 @@ int gemm_f16_dequant_next_sym128(const uint16_t* A, int64_t lda, const uint16_t*
  * Per row: the k largest logits ordered by value descending, ties to the lower index,
  * -0.0 equal to +0.0; idx[m][0] is the argmax; val[m][r] == logits[m][idx[m][r]] bit for bit.
  * Requires 1 <= M, 1 <= k <= min(V, 256), V < 2^31, ldl >= V, ceil(V / 8192) * k <= 8192;
- * logits 4-byte aligned, idx/val 4-byte aligned.  Logits must be finite (unchecked).
+ * logits 4-byte aligned, idx/val 4-byte aligned.  Logits must be finite or -infinity (unchecked).
  * Workspace (query it; 0 when V <= 4096): k <= 64: one 8-byte key per 64 logits,
  * M * ceil(V / 64) * 8 bytes (19 KB for one 151936-logit row); k > 64: M * ceil(V / chunk) * k * 8
  * bytes with chunk = 4096 or 8192 logits.  Contents need no initialisation.
@@ -349,6 +349,121 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
                     int64_t W, const int32_t* kv_len, const int32_t* q_start, int64_t B, int64_t T, int64_t max_q,
                     int64_t Hq, int64_t window, float scale, uint16_t* out, int64_t ldo, void* ws, size_t* ws_bytes,
                     w4_stream_t stream);
+
+/*
+ * A decode step with drafted tokens: kv_plan gives each sequence its pages and each row its position and slot,
+ * kv_append_norm_rope puts the rows' keys and values there, attention_paged_tree verifies them, logits_adjust
+ * prepares the logits for logits_argmax_topk.
+ *
+ * norm_rope_f16 -- rope_f16 behind a norm of each head: x w / sqrt(mean over the head's D dims of x^2 + eps) instead
+ * of x, with the same arguments, requirements and rotation (forward).  weight f32 [D], 16-byte aligned, or NULL for ones (a norm
+ * that scales by 1 + w takes weights with the one added).  1e-30 <= eps <= 1e30.  The squares are summed in f32 (so
+ * values past 1e18 are not for it), products are f32, rounded once to f16.  y may be x (f16, ldy == ldx).
+ */
+int norm_rope_f16(const void* x, int32_t x_type, int64_t ldx, const float* weight, float eps, const int32_t* pos,
+                  const float* freq, uint16_t* y, int64_t ldy, int64_t T, int64_t H, int64_t D, int64_t R,
+                  int32_t interleaved, float mscale, w4_stream_t stream);
+
+/*
+ * kv_append_norm_rope -- kv_append_rope with such a norm of each query head (q_weight) and each key head (k_weight)
+ * before the rotation, in the same launch; V is stored as it is.  Arguments, requirements and results are
+ * those of kv_append_rope; weights and eps as for norm_rope_f16.
+ */
+int kv_append_norm_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
+                        const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot,
+                        const int32_t* pos, const float* freq, const float* q_weight, const float* k_weight, float eps,
+                        int64_t T, int64_t R, int32_t interleaved, float mscale, w4_stream_t stream);
+
+/*
+ * kv_plan -- the tables of a step from the lengths of its sequences, and the pages that it needs.
+ *   kv_len  int32 [B]: the cached tokens that sequence b keeps;  new_len int32 [B]: its rows of this step;
+ *   table   int32 [B][W] (row stride ldt), in and out: its pages;  owned int32 [B], in and out: how many it has;
+ *   free_pages int32 [pages], free_count int32 [1], in and out: a stack of the cache's free pages and its height.
+ * With need = ceil((kv_len + new_len) / page_size): first the pages that a sequence owns past need go onto
+ * the stack, in order of sequence and page, their table entries becoming -1 (kv_len 0 and new_len 0 end a sequence; a shorter kv_len
+ * takes back what was not accepted); then the sequences in turn take the pages that they lack from its top.  One whose pages, with
+ * all that those before it lack, the stack does not cover gets none.
+ *   q_start int32 [B + 1]: the first row of each, and the end;  kv_total int32 [B]: kv_len + new_len, or kv_len if refused;
+ *   pos int32 [T], slot int64 [T]: of row i of a sequence: kv_len + i (kv_len + depth[row], for a
+ *   tree of drafted tokens), and page * page_size + token of the page of its cached token kv_len + i; -1 if refused.  Rows
+ *   past the last sequence are padding: 0 and -1.  (What kv_append_rope and attention_paged take.)
+ *   status int32 [B]: 0, or how many pages were lacking; -1 for a sequence that does not fit: a length below 0,
+ *   kv_len + new_len past W * page_size, or rows past T.  Such a one keeps what it has; its rows have position 0.
+ * Requires 1 <= B <= 2^20, 1 <= T < 2^24, W, page_size, pages >= 1, W * page_size <= 2^30, pages * page_size < 2^31, ldt >= W; int32
+ * arrays 4-byte aligned, slot 8-byte; depth may be NULL.  kv_total may be kv_len; no other overlap.  Entries of the
+ * stack past its height are left as they are.  Everything is read on the device and kept in bounds there (owned to 0 .. W, the height to
+ * 0 .. pages); a table entry that is no page of the cache gives slots of -1.  One launch up to 4096 rows, two
+ * above.  Deterministic.
+ */
+int kv_plan(const int32_t* kv_len, const int32_t* new_len, int64_t B, int32_t* table, int64_t ldt, int64_t W,
+            int32_t* owned, int32_t* free_pages, int32_t* free_count, int64_t pages, int64_t page_size,
+            const int32_t* depth, int64_t T, int32_t* q_start, int32_t* kv_total, int32_t* pos, int64_t* slot,
+            int32_t* status, w4_stream_t stream);
+
+/*
+ * attention_paged_tree -- attention_paged for drafted tokens that form trees: row i of a sequence with n new rows sees the
+ * cached tokens before them, 0 .. kv_len - n - 1, and of the new ones those whose bits are set for it:
+ *   mask uint64 [T][ldm]: bit j % 64 of word j / 64 of row t: it sees new token j of its sequence (itself, if
+ *   it is to).  Bits from n on are ignored.  Any pattern will do, not trees alone.
+ * window: the row's depth is the number of its bits, less one (0 at least), its position p = kv_len - n + depth, and of
+ * the tokens before the new ones it sees those from p + 1 - window on; new tokens go by their bits alone.
+ * A row that sees no key is 0.  Everything else is as for attention_paged: arguments, lengths in bounds, unseen keys that reach
+ * nothing, workspace (query it), roundings, determinism.
+ * Requires what attention_paged requires, window 0 or at least max_q, ldm >= ceil(max_q / 64), mask 8-byte
+ * aligned.
+ */
+int attention_paged_tree(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
+                         int64_t W, const int32_t* kv_len, const int32_t* q_start, const uint64_t* mask, int64_t ldm,
+                         int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t window, float scale, uint16_t* out,
+                         int64_t ldo, void* ws, size_t* ws_bytes, w4_stream_t stream);
+
+/*
+ * What logits_adjust does to rows of logits (the struct itself is host memory, read during the call; its arrays are the
+ * device's).  A group whose first pointer is NULL is off.
+ *   request int32 [M]: the request of each row (NULL: row m is request m), 0 .. requests - 1; a row of any
+ *   other has no penalties and no biases.
+ *   tokens int32 [requests][max_tokens] (row stride ld_tokens): the first token_len[s] are request s's tokens, the
+ *   first prompt_len[s] of these its prompt (NULL: 0).  repetition, frequency, presence f32 [requests] (NULL: 1, 0, 0).
+ *   bias f32, bias_id int32 [biases]: request s has the entries bias_start[s] .. bias_start[s + 1] - 1 (int32
+ *   [requests + 1]); of a token that it names twice the later entry counts.
+ *   mask uint32 [masks][ld_mask]: bit v % 32 of word v / 32: token v is allowed.  mask_row int32 [M]: the mask of
+ *   each row (NULL: row m has mask m); outside 0 .. masks - 1: all are allowed.
+ */
+typedef struct {
+  const int32_t* request;
+  int64_t requests;
+  const int32_t* tokens;
+  int64_t ld_tokens, max_tokens;
+  const int32_t* token_len;
+  const int32_t* prompt_len;
+  const float* repetition;
+  const float* frequency;
+  const float* presence;
+  const float* bias;
+  const int32_t* bias_id;
+  const int32_t* bias_start;
+  int64_t biases;
+  const uint32_t* mask;
+  int64_t ld_mask, masks;
+  const int32_t* mask_row;
+} w4_logit_rules;
+
+/*
+ * logits_adjust -- penalties for tokens that have occurred, biases and masks on logits, before logits_argmax_topk:
+ *   logits f32 [M][V] (ldl), out f32 [M][V] (ldo); out may be logits (ldo == ldl), no other overlap.
+ * With c the number of times that token v occurs in its request's tokens behind the prompt:
+ *   x = l > 0 ? l / repetition : l * repetition   if v occurs at all, in the prompt or behind it, else l;
+ *   x -= frequency * c + presence if c > 0;   x += bias of v;   x = -infinity if v is not allowed, whatever it was.
+ * All in f32.  Tokens and biases of ids outside 0 .. V - 1 are ignored; token_len is kept to 0 .. max_tokens, bias_start to
+ * 0 .. biases.  repetition has to be positive (not checked).  A row of which nothing is allowed is all -infinity;
+ * logits_argmax_topk takes -infinity as the smallest value.
+ * Requires M, V >= 1, V < 2^31, M * ceil(V / 4096) < 2^24, ldl, ldo >= V, requests >= 1 (and M <= requests without
+ * request), 0 <= max_tokens < 2^31, ld_tokens >= max_tokens, token_len with tokens, bias_id and bias_start with
+ * bias, 0 <= biases < 2^31 - 1, ld_mask >= ceil(V / 32), 1 <= masks < 2^31 (and M <= masks without mask_row); everything 4-byte
+ * aligned (16-byte rows of logits and out are faster).  No workspace.  Deterministic.
+ */
+int logits_adjust(const float* logits, int64_t ldl, int64_t M, int64_t V, const w4_logit_rules* rules, float* out,
+                  int64_t ldo, w4_stream_t stream);
 
 #ifdef __cplusplus
 }

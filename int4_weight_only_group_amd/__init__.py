@@ -17,13 +17,14 @@ import math
 
 import torch
 
-from ._lib import KvCache, lib, LIB_PATH  # noqa: F401
+from ._lib import KvCache, LogitRules, lib, LIB_PATH  # noqa: F401
 
 __all__ = [
     "W4Error", "w4_pack", "w4_quantize", "w4_gemv", "w4_gemv_sym128", "w4_dequant_f16_t_sym128", "w4_dequant_f16_t", "gemm_f16", "gemm_f16_dequant_next", "gemm_f16_dequant_next_sym128", "logits_argmax_topk",
     "logits_argmax_topk_noalloc", "w4_gemv_topk", "gemv_topk_workspace_bytes",
     "topk_workspace_bytes", "gemm_workspace_bytes", "status_string",
     "rope_frequencies", "rope_f16", "kv_append_rope", "attention_paged", "attention_workspace_bytes",
+    "norm_rope_f16", "kv_append_norm_rope", "kv_plan", "tree_mask", "attention_paged_tree", "logits_adjust",
 ]
 
 W4_OK, W4_ERR_WORKSPACE = 0, -4
@@ -567,6 +568,18 @@ def rope_f16(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, in
     freq float32 [R/2] (see rope_frequencies) -> float16 [T][H][D] with the first R dims of every
     head rotated by positions * freq, times mscale.  Pairs are (i, i + R/2), or (2i, 2i + 1) if
     interleaved.  inverse rotates back: the gradient of the rotation.  out may be x (float16)."""
+    return _rope("rope_f16", x, positions, freq, None, None, interleaved, mscale, inverse, out)
+
+
+def norm_rope_f16(x: torch.Tensor, weight: torch.Tensor | None, positions: torch.Tensor, freq: torch.Tensor, *,
+                  eps: float = 1e-6, interleaved: bool = False, mscale: float = 1.0,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """rope_f16 behind a norm of each head: of x * weight / sqrt(mean(x^2 over the head) + eps), weight
+    float32 [D] (None: ones).  out may be x (float16)."""
+    return _rope("norm_rope_f16", x, positions, freq, weight, eps, interleaved, mscale, False, out)
+
+
+def _rope(fn, x, positions, freq, weight, eps, interleaved, mscale, inverse, out):
     dev = torch.cuda.current_device()
     dtype = _row_dtype(x, "x")
     ldx = _rows(x, "x", dtype, dev)
@@ -579,9 +592,14 @@ def rope_f16(x: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor, *, in
         if out.shape != x.shape:
             raise ValueError("out must have x's shape")
     f, rot = _freq(freq, dev)
-    _check("rope_f16", lib().rope_f16(x.data_ptr(), _F32 if dtype is torch.float32 else _F16, ldx,
-                                      _vec(positions, "positions", torch.int32, t, dev), f, out.data_ptr(), ldy, t, h,
-                                      d, rot, interleaved, inverse, mscale, _raw_stream(dev)))
+    kind, pos = _F32 if dtype is torch.float32 else _F16, _vec(positions, "positions", torch.int32, t, dev)
+    if eps is None:
+        _check(fn, lib().rope_f16(x.data_ptr(), kind, ldx, pos, f, out.data_ptr(), ldy, t, h, d, rot, interleaved,
+                                  inverse, mscale, _raw_stream(dev)))
+    else:
+        w = None if weight is None else _vec(weight, "weight", torch.float32, d, dev)
+        _check(fn, lib().norm_rope_f16(x.data_ptr(), kind, ldx, w, eps, pos, f, out.data_ptr(), ldy, t, h, d, rot,
+                                       interleaved, mscale, _raw_stream(dev)))
     return out
 
 
@@ -597,6 +615,23 @@ def kv_append_rope(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     contiguous dim, float16 or float8_e4m3fn (value = code * scale[head], scales float32 [kv heads]);
     slots int64 [T] = page * page size + token of the page, distinct, -1: not written.
     Returns the rotated queries, float16 (None without q)."""
+    return _append("kv_append_rope", k, v, k_cache, v_cache, slots, positions, freq, None, q, q_out, interleaved, mscale,
+                   k_scale, v_scale)
+
+
+def kv_append_norm_rope(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        slots: torch.Tensor, positions: torch.Tensor, freq: torch.Tensor,
+                        k_weight: torch.Tensor | None, *, q: torch.Tensor | None = None,
+                        q_weight: torch.Tensor | None = None, eps: float = 1e-6, q_out: torch.Tensor | None = None,
+                        interleaved: bool = False, mscale: float = 1.0, k_scale: torch.Tensor | None = None,
+                        v_scale: torch.Tensor | None = None) -> torch.Tensor | None:
+    """kv_append_rope with a norm of each key and query head before the rotation (see norm_rope_f16), in the same launch:
+    k_weight, q_weight float32 [dim] (None: ones).  v is stored as it is."""
+    return _append("kv_append_norm_rope", k, v, k_cache, v_cache, slots, positions, freq, (q_weight, k_weight, eps), q,
+                   q_out, interleaved, mscale, k_scale, v_scale)
+
+
+def _append(fn, k, v, k_cache, v_cache, slots, positions, freq, norm, q, q_out, interleaved, mscale, k_scale, v_scale):
     dev = torch.cuda.current_device()
     c = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     dtype = _row_dtype(k, "k")
@@ -622,10 +657,15 @@ def kv_append_rope(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_ca
     elif q_out is not None:
         raise ValueError("q_out without q")
     f, rot = _freq(freq, dev)
-    _check("kv_append_rope", lib().kv_append_rope(
-        pq, ldq, pqo, ldqo, hq, k.data_ptr(), ldk, v.data_ptr(), ldv, _F32 if dtype is torch.float32 else _F16, c,
-        _vec(slots, "slots", torch.int64, t, dev), _vec(positions, "positions", torch.int32, t, dev), f, t, rot,
-        interleaved, mscale, _raw_stream(dev)))
+    args = (pq, ldq, pqo, ldqo, hq, k.data_ptr(), ldk, v.data_ptr(), ldv, _F32 if dtype is torch.float32 else _F16, c,
+            _vec(slots, "slots", torch.int64, t, dev), _vec(positions, "positions", torch.int32, t, dev), f)
+    if norm is None:
+        _check(fn, lib().kv_append_rope(*args, t, rot, interleaved, mscale, _raw_stream(dev)))
+    else:
+        q_weight, k_weight, eps = norm
+        qw = None if q_weight is None else _vec(q_weight, "q_weight", torch.float32, d, dev)
+        kw = None if k_weight is None else _vec(k_weight, "k_weight", torch.float32, d, dev)
+        _check(fn, lib().kv_append_norm_rope(*args, qw, kw, eps, t, rot, interleaved, mscale, _raw_stream(dev)))
     return q_out
 
 
@@ -656,6 +696,51 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     decode: it chooses the kernel).  Returns float16 [T][heads][dim]; a row that sees no key is 0,
     rows past the last sequence are not written.  A table much wider than the sequences are long costs time.  out may be q.  One is allocated for out and the workspace
     (attention_workspace_bytes) when not given or too small."""
+    return _attend("attention_paged", q, k_cache, v_cache, table, kv_len, None, q_start, max_q, scale, window, k_scale,
+                   v_scale, out, workspace)
+
+
+def tree_mask(parents) -> tuple[torch.Tensor, torch.Tensor]:
+    """(mask int64 [n][words], depth int32 [n]), on the CPU, of one sequence's drafted tokens: parents[i] < i is the token that
+    token i follows, -1: it follows the context.  A token sees its ancestors and itself; depth counts the ancestors.
+    Sequences' masks and depths, one after another (masks as wide as the longest needs), are what
+    attention_paged_tree and kv_plan take."""
+    seen, depth = [], []
+    for i, p in enumerate(parents):
+        p = int(p)
+        if not -1 <= p < i:
+            raise ValueError("parents[i] must be from -1 to i - 1")
+        seen.append((seen[p] if p >= 0 else 0) | 1 << i)
+        depth.append(depth[p] + 1 if p >= 0 else 0)
+    words = -(-len(seen) // 64)
+    rows = [[((s >> 64 * w & (1 << 64) - 1) ^ 1 << 63) - (1 << 63) for w in range(words)] for s in seen]
+    return torch.tensor(rows, dtype=torch.int64).view(len(seen), words), torch.tensor(depth, dtype=torch.int32)
+
+
+def attention_paged_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                         kv_len: torch.Tensor, mask: torch.Tensor, *, q_start: torch.Tensor | None = None,
+                         max_q: int | None = None, scale: float | None = None, window: int = 0,
+                         k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """attention_paged for drafted tokens that form trees (see tree_mask): a row sees the cached tokens before
+    its sequence's new ones and, of these, those whose bits are set in its row of mask, int64 [T][words] (bit j % 64 of
+    word j / 64: new token j), words >= ceil(max_q / 64).  A window, at least max_q, reaches back from the row's position,
+    kv_len - n + its bits set - 1.  Everything else, the workspace's size too, is as for attention_paged."""
+    dev = torch.cuda.current_device()
+    _need(mask, "mask", torch.int64, dev)
+    ldm = _rowmajor(mask, "mask")
+    if not isinstance(q, torch.Tensor) or mask.shape[0] != q.shape[0]:
+        raise ValueError("mask must have a row for each row of q")
+    if max_q is None:
+        max_q = 1 if q_start is None else q.shape[0]
+    if mask.shape[1] * 64 < max_q:
+        raise ValueError("mask must have ceil(max_q / 64) words a row")
+    return _attend("attention_paged_tree", q, k_cache, v_cache, table, kv_len, (mask.data_ptr(), ldm), q_start, max_q,
+                   scale, window, k_scale, v_scale, out, workspace)
+
+
+def _attend(name, q, k_cache, v_cache, table, kv_len, mask, q_start, max_q, scale, window, k_scale, v_scale, out,
+            workspace):
     dev = torch.cuda.current_device()
     c = _kv_cache(k_cache, v_cache, k_scale, v_scale, dev)
     ldq = _rows(q, "q", torch.float16, dev)
@@ -681,9 +766,9 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         max_q = 1
     if scale is None:
         scale = d ** -0.5
-    args = (q.data_ptr(), ldq, c, table.data_ptr(), ldt, width, _vec(kv_len, "kv_len", torch.int32, b, dev), start, b,
-            t, max_q, hq, window, scale, out.data_ptr(), ldo)
-    fn, stream = lib().attention_paged, _raw_stream(dev)
+    args = (q.data_ptr(), ldq, c, table.data_ptr(), ldt, width, _vec(kv_len, "kv_len", torch.int32, b, dev), start,
+            *(mask or ()), b, t, max_q, hq, window, scale, out.data_ptr(), ldo)
+    fn, stream = getattr(lib(), name), _raw_stream(dev)
     status = W4_ERR_WORKSPACE
     if workspace is not None:
         if workspace.get_device() != dev or not workspace.is_contiguous():
@@ -691,8 +776,120 @@ def attention_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         status = fn(*args, workspace.data_ptr(), ctypes.c_size_t(workspace.numel() * workspace.element_size()), stream)
     if status == W4_ERR_WORKSPACE:
         size = ctypes.c_size_t(0)
-        _check("attention_paged", fn(*args, None, size, None))
+        _check(name, fn(*args, None, size, None))
         workspace = torch.empty(max(16, size.value), dtype=torch.uint8, device=q.device)
         status = fn(*args, workspace.data_ptr(), size, stream)
-    _check("attention_paged", status)
+    _check(name, status)
+    return out
+
+
+# --------------------------------------------------------------- a step's tables, and its logits
+
+
+def kv_plan(kv_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor, owned: torch.Tensor, free: torch.Tensor,
+            free_count: torch.Tensor, page_size: int, rows: int, *, depth: torch.Tensor | None = None,
+            out: tuple | None = None):
+    """The tables of a step of B sequences, made on the device: pages go back to the stack of free ones and are taken from it, and
+    each of the step's rows gets its position and slot (see include/w4.h).
+
+    kv_len, new_len int32 [B]: cached tokens that a sequence keeps, and its rows of this step; table int32 [B][W], owned int32 [B] (how
+    many pages it has), free int32 [pages] and free_count int32 [1] (a stack of the cache's free pages and its
+    height) are updated; rows: of the step, padding included; depth int32 [rows]: of drafted tokens, instead of their
+    order.  Returns (q_start int32 [B + 1], kv_total int32 [B], positions int32 [rows], slots int64 [rows],
+    status int32 [B]: 0, pages lacking, or -1), written to `out` if given, of which kv_total may be kv_len."""
+    dev = torch.cuda.current_device()
+    _need(table, "table", torch.int32, dev)
+    ldt = _rowmajor(table, "table")
+    b, width = table.shape
+    _need(free, "free", torch.int32, dev)
+    if not free.is_contiguous() or free.dim() != 1:
+        raise ValueError("free must be contiguous and 1-D")
+    if out is None:
+        new = functools.partial(torch.empty, dtype=torch.int32, device=table.device)
+        out = (new(b + 1), new(b), new(rows), torch.empty(rows, dtype=torch.int64, device=table.device), new(b))
+    q_start, kv_total, positions, slots, status = out
+    i32 = torch.int32
+    _check("kv_plan", lib().kv_plan(
+        _vec(kv_len, "kv_len", i32, b, dev), _vec(new_len, "new_len", i32, b, dev), b, table.data_ptr(), ldt, width,
+        _vec(owned, "owned", i32, b, dev), free.data_ptr(), _vec(free_count, "free_count", i32, 1, dev), free.shape[0],
+        page_size, None if depth is None else _vec(depth, "depth", i32, rows, dev), rows,
+        _vec(q_start, "q_start", i32, b + 1, dev), _vec(kv_total, "kv_total", i32, b, dev),
+        _vec(positions, "positions", i32, rows, dev), _vec(slots, "slots", torch.int64, rows, dev),
+        _vec(status, "status", i32, b, dev), _raw_stream(dev)))
+    return out
+
+
+def logits_adjust(logits: torch.Tensor, *, tokens: torch.Tensor | None = None, token_len: torch.Tensor | None = None,
+                  prompt_len: torch.Tensor | None = None, repetition: torch.Tensor | None = None,
+                  frequency: torch.Tensor | None = None, presence: torch.Tensor | None = None,
+                  bias_start: torch.Tensor | None = None, bias_id: torch.Tensor | None = None,
+                  bias: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                  mask_row: torch.Tensor | None = None, request: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """Penalties for tokens that have occurred, biases and masks on float32 logits [M][V] (see include/w4.h).
+
+    tokens int32 [requests][max tokens] with token_len and prompt_len int32 [requests]; repetition (l / r or l * r of
+    tokens that occur), frequency (times the number behind the prompt) and presence float32 [requests]; bias_id
+    int32 and bias float32, request s having the entries bias_start[s] .. bias_start[s + 1] - 1; mask int32
+    [masks][ceil(V / 32)], a bit for each allowed token, mask_row int32 [M] (-1: no mask); request int32 [M]: which
+    request a row belongs to (None: row m is request m).  Returns out (which may be logits)."""
+    dev = torch.cuda.current_device()
+    f32, i32 = torch.float32, torch.int32
+    _need(logits, "logits", f32, dev)
+    ldl = _rowmajor(logits, "logits")
+    m, v = logits.shape
+    if out is None:
+        out, ldo = torch.empty((m, v), dtype=f32, device=logits.device), v
+    else:
+        _need(out, "out", f32, dev)
+        ldo = _rowmajor(out, "out")
+        if out.shape != logits.shape:
+            raise ValueError("out must have the shape of logits")
+    r = LogitRules()
+    if request is not None:
+        r.request = _vec(request, "request", i32, m, dev)
+    n = m  # requests, by the first of their arrays
+    if tokens is not None:
+        if token_len is None:
+            raise ValueError("tokens need token_len")
+        _need(tokens, "tokens", i32, dev)
+        if tokens.numel():  # else there is nothing to read, and no address
+            r.tokens, r.ld_tokens = tokens.data_ptr(), _rowmajor(tokens, "tokens")
+        n, r.max_tokens = tokens.shape
+        r.token_len = _vec(token_len, "token_len", i32, n, dev)
+        if prompt_len is not None:
+            r.prompt_len = _vec(prompt_len, "prompt_len", i32, n, dev)
+        if repetition is not None:
+            r.repetition = _vec(repetition, "repetition", f32, n, dev)
+        if frequency is not None:
+            r.frequency = _vec(frequency, "frequency", f32, n, dev)
+        if presence is not None:
+            r.presence = _vec(presence, "presence", f32, n, dev)
+    elif any(t is not None for t in (token_len, prompt_len, repetition, frequency, presence)):
+        raise ValueError("penalties need tokens")
+    if bias is not None:
+        if bias_start is None or bias_id is None:
+            raise ValueError("bias needs bias_start and bias_id")
+        _need(bias, "bias", f32, dev)
+        k = bias.numel()
+        if tokens is None:
+            n = bias_start.numel() - 1
+        r.bias_start = _vec(bias_start, "bias_start", i32, n + 1, dev)
+        if k:
+            r.bias, r.bias_id, r.biases = _vec(bias, "bias", f32, k, dev), _vec(bias_id, "bias_id", i32, k, dev), k
+    elif bias_start is not None or bias_id is not None:
+        raise ValueError("bias_start and bias_id need bias")
+    r.requests = n
+    if mask is not None:
+        _need(mask, "mask", i32, dev)
+        r.ld_mask = _rowmajor(mask, "mask")
+        r.masks, words = mask.shape
+        if words * 32 < v:
+            raise ValueError("mask must have ceil(V / 32) words a row")
+        r.mask = mask.data_ptr()
+        if mask_row is not None:
+            r.mask_row = _vec(mask_row, "mask_row", i32, m, dev)
+    elif mask_row is not None:
+        raise ValueError("mask_row without mask")
+    _check("logits_adjust", lib().logits_adjust(logits.data_ptr(), ldl, m, v, r, out.data_ptr(), ldo, _raw_stream(dev)))
     return out

@@ -20,7 +20,16 @@ class KvCache(_c.Structure):
                 ("stride_token", _i64), ("type", _i32)]
 
 
+class LogitRules(_c.Structure):
+    """w4_logit_rules of include/w4.h."""
+    _fields_ = [("request", _p), ("requests", _i64), ("tokens", _p), ("ld_tokens", _i64), ("max_tokens", _i64),
+                ("token_len", _p), ("prompt_len", _p), ("repetition", _p), ("frequency", _p), ("presence", _p),
+                ("bias", _p), ("bias_id", _p), ("bias_start", _p), ("biases", _i64), ("mask", _p), ("ld_mask", _i64),
+                ("masks", _i64), ("mask_row", _p)]
+
+
 _cache_p = _c.POINTER(KvCache)
+_rules_p = _c.POINTER(LogitRules)
 SIGNATURES = {
     "w4_strerror": (_c.c_char_p, [_c.c_int]),
     "w4_pack": (_c.c_int, [_p, _p, _i64, _i64, _p]),
@@ -41,6 +50,13 @@ SIGNATURES = {
                                   _i64, _i32, _f32, _p]),
     "attention_paged": (_c.c_int, [_p, _i64, _cache_p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64, _i64, _i64, _f32,
                                    _p, _i64, _p, _sz_p, _p]),
+    "norm_rope_f16": (_c.c_int, [_p, _i32, _i64, _p, _f32, _p, _p, _p, _i64, _i64, _i64, _i64, _i64, _i32, _f32, _p]),
+    "kv_append_norm_rope": (_c.c_int, [_p, _i64, _p, _i64, _i64, _p, _i64, _p, _i64, _i32, _cache_p, _p, _p, _p, _p,
+                                       _p, _f32, _i64, _i64, _i32, _f32, _p]),
+    "kv_plan": (_c.c_int, [_p, _p, _i64, _p, _i64, _i64, _p, _p, _p, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]),
+    "attention_paged_tree": (_c.c_int, [_p, _i64, _cache_p, _p, _i64, _i64, _p, _p, _p, _i64, _i64, _i64, _i64, _i64,
+                                        _i64, _f32, _p, _i64, _p, _sz_p, _p]),
+    "logits_adjust": (_c.c_int, [_p, _i64, _i64, _i64, _rules_p, _p, _i64, _p]),
     "w4_gemv_topk": (_c.c_int, [_p, _p, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p, _sz_p, _p]),
 }
 

@@ -122,6 +122,11 @@ int check_rope(int64_t T, int64_t D, int64_t R, int32_t x_type, const int32_t* p
   return W4_OK;
 }
 
+int check_norm(const w4::HeadNorm& n) {
+  if (!(n.eps >= 1e-30f && n.eps <= 1e30f)) return W4_ERR_SHAPE;
+  return al16(n.q) && al16(n.k) ? W4_OK : W4_ERR_ALIGN;
+}
+
 // w4_kv_cache's requirements; on W4_OK c is the kernels' view of it
 int check_cache(const w4_kv_cache* h, w4::KvCache& c) {
   if (!h || !h->k || !h->v) return W4_ERR_NULL;
@@ -388,17 +393,42 @@ int rope_f16(const void* x, int32_t x_type, int64_t ldx, const int32_t* pos, con
     if (int e = check_device()) return e;
     (void)hipGetLastError();
     w4::launch_rope(x, x_type == W4_F32, ldx, pos, freq, y, ldy, (int)T, (int)H, (int)D, (int)R, interleaved != 0,
-                    inverse != 0, mscale, (hipStream_t)stream);
+                    inverse != 0, mscale, nullptr, (hipStream_t)stream);
     return launched();
   } catch (...) {
     return W4_ERR_INTERNAL;
   }
 }
 
-int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
-                   const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot,
-                   const int32_t* pos, const float* freq, int64_t T, int64_t R, int32_t interleaved, float mscale,
-                   w4_stream_t stream) {
+int norm_rope_f16(const void* x, int32_t x_type, int64_t ldx, const float* weight, float eps, const int32_t* pos,
+                  const float* freq, uint16_t* y, int64_t ldy, int64_t T, int64_t H, int64_t D, int64_t R,
+                  int32_t interleaved, float mscale, w4_stream_t stream) {
+  try {
+    if (!x || !y) return W4_ERR_NULL;
+    if (int e = check_rope(T, D, R, x_type, pos, freq, mscale)) return e;
+    const w4::HeadNorm norm{weight, nullptr, eps};
+    if (int e = check_norm(norm)) return e;
+    if (int e = check_rows(x, ldx, H, D)) return e;
+    if (int e = check_rows(y, ldy, H, D)) return e;
+    if (int e = check_device()) return e;
+    (void)hipGetLastError();
+    w4::launch_rope(x, x_type == W4_F32, ldx, pos, freq, y, ldy, (int)T, (int)H, (int)D, (int)R, interleaved != 0, false,
+                    mscale, &norm, (hipStream_t)stream);
+    return launched();
+  } catch (...) {
+    return W4_ERR_INTERNAL;
+  }
+}
+
+}  // extern "C"
+
+namespace {
+
+// kv_append_rope, or kv_append_norm_rope with a norm
+int append(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
+           const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot, const int32_t* pos,
+           const float* freq, const w4::HeadNorm* norm, int64_t T, int64_t R, int32_t interleaved, float mscale,
+           w4_stream_t stream) {
   try {
     if (!k || !v || !slot || (!q) != (!q_out)) return W4_ERR_NULL;
     w4::KvCache c;
@@ -411,20 +441,23 @@ int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, in
       if (int e = check_rows(q_out, ldqo, Hq, c.dim)) return e;
     }
     if (((uintptr_t)slot & 7u) != 0) return W4_ERR_ALIGN;
+    if (norm)
+      if (int e = check_norm(*norm)) return e;
     if (int e = check_device()) return e;
     (void)hipGetLastError();
     w4::launch_kv_append(q, ldq, q_out, ldqo, (int)Hq, k, ldk, v, ldv, x_type == W4_F32, c, slot, pos, freq, (int)T,
-                         (int)R, interleaved != 0, mscale, (hipStream_t)stream);
+                         (int)R, interleaved != 0, mscale, norm, (hipStream_t)stream);
     return launched();
   } catch (...) {
     return W4_ERR_INTERNAL;
   }
 }
 
-int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
-                    int64_t W, const int32_t* kv_len, const int32_t* q_start, int64_t B, int64_t T, int64_t max_q,
-                    int64_t Hq, int64_t window, float scale, uint16_t* out, int64_t ldo, void* ws, size_t* ws_bytes,
-                    w4_stream_t stream) {
+// attention_paged, or attention_paged_tree with a mask
+int attend(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt, int64_t W,
+           const int32_t* kv_len, const int32_t* q_start, const uint64_t* mask, int64_t ldm, int64_t B, int64_t T,
+           int64_t max_q, int64_t Hq, int64_t window, float scale, uint16_t* out, int64_t ldo, void* ws,
+           size_t* ws_bytes, w4_stream_t stream) {
   try {
     if (!q || !table || !kv_len || !out) return W4_ERR_NULL;
     w4::KvCache c;
@@ -443,6 +476,11 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
     a.W = (int)W, a.B = (int)B, a.T = (int)T, a.max_q = (int)max_q, a.Hq = (int)Hq;
     a.window = window >= ((int64_t)1 << 30) ? 0 : (int)window;  // no sequence is longer
     a.scale = scale;
+    if (mask) {
+      if (((uintptr_t)mask & 7u) != 0) return W4_ERR_ALIGN;
+      if (ldm < (max_q + 63) / 64 || ldm > kMaxDim || (a.window && a.window < max_q)) return W4_ERR_SHAPE;
+      a.mask = mask, a.ldm = ldm;
+    }
     size_t need = 0;
     if (!w4::attention_ws_bytes(a, need)) return W4_ERR_SHAPE;
     const int w = workspace(ws, ws_bytes, need);
@@ -450,7 +488,119 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
     if (w == 1) return W4_OK;
     if (int e = check_device()) return e;
     (void)hipGetLastError();
-    w4::launch_attention(a, need ? ws : nullptr, (hipStream_t)stream);
+    if (mask)
+      w4::launch_attention_tree(a, need ? ws : nullptr, (hipStream_t)stream);
+    else
+      w4::launch_attention(a, need ? ws : nullptr, (hipStream_t)stream);
+    return launched();
+  } catch (...) {
+    return W4_ERR_INTERNAL;
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_append_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
+                   const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot,
+                   const int32_t* pos, const float* freq, int64_t T, int64_t R, int32_t interleaved, float mscale,
+                   w4_stream_t stream) {
+  return append(q, ldq, q_out, ldqo, Hq, k, ldk, v, ldv, x_type, cache, slot, pos, freq, nullptr, T, R, interleaved,
+                mscale, stream);
+}
+
+int kv_append_norm_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int64_t Hq, const void* k, int64_t ldk,
+                        const void* v, int64_t ldv, int32_t x_type, const w4_kv_cache* cache, const int64_t* slot,
+                        const int32_t* pos, const float* freq, const float* q_weight, const float* k_weight, float eps,
+                        int64_t T, int64_t R, int32_t interleaved, float mscale, w4_stream_t stream) {
+  const w4::HeadNorm norm{q_weight, k_weight, eps};
+  return append(q, ldq, q_out, ldqo, Hq, k, ldk, v, ldv, x_type, cache, slot, pos, freq, &norm, T, R, interleaved, mscale,
+                stream);
+}
+
+int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
+                    int64_t W, const int32_t* kv_len, const int32_t* q_start, int64_t B, int64_t T, int64_t max_q,
+                    int64_t Hq, int64_t window, float scale, uint16_t* out, int64_t ldo, void* ws, size_t* ws_bytes,
+                    w4_stream_t stream) {
+  return attend(q, ldq, cache, table, ldt, W, kv_len, q_start, nullptr, 0, B, T, max_q, Hq, window, scale, out, ldo, ws,
+                ws_bytes, stream);
+}
+
+int attention_paged_tree(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
+                         int64_t W, const int32_t* kv_len, const int32_t* q_start, const uint64_t* mask, int64_t ldm,
+                         int64_t B, int64_t T, int64_t max_q, int64_t Hq, int64_t window, float scale, uint16_t* out,
+                         int64_t ldo, void* ws, size_t* ws_bytes, w4_stream_t stream) {
+  if (!mask) return W4_ERR_NULL;
+  return attend(q, ldq, cache, table, ldt, W, kv_len, q_start, mask, ldm, B, T, max_q, Hq, window, scale, out, ldo, ws,
+                ws_bytes, stream);
+}
+
+int kv_plan(const int32_t* kv_len, const int32_t* new_len, int64_t B, int32_t* table, int64_t ldt, int64_t W,
+            int32_t* owned, int32_t* free_pages, int32_t* free_count, int64_t pages, int64_t page_size,
+            const int32_t* depth, int64_t T, int32_t* q_start, int32_t* kv_total, int32_t* pos, int64_t* slot,
+            int32_t* status, w4_stream_t stream) {
+  try {
+    if (!kv_len || !new_len || !table || !owned || !free_pages || !free_count || !q_start || !kv_total || !pos || !slot ||
+        !status)
+      return W4_ERR_NULL;
+    if (B < 1 || B > ((int64_t)1 << 20) || T < 1 || T >= kMaxTokens) return W4_ERR_SHAPE;
+    if (page_size < 1 || page_size > kMaxDim || W < 1 || W > kMaxDim / page_size || ldt < W || ldt > kMaxDim)
+      return W4_ERR_SHAPE;
+    if (pages < 1 || pages > (((int64_t)1 << 31) - 1) / page_size) return W4_ERR_SHAPE;
+    for (const void* p : {(const void*)kv_len, (const void*)new_len, (const void*)table, (const void*)owned,
+                          (const void*)free_pages, (const void*)free_count, (const void*)depth, (const void*)q_start,
+                          (const void*)kv_total, (const void*)pos, (const void*)status})
+      if (!al4(p)) return W4_ERR_ALIGN;
+    if (((uintptr_t)slot & 7u) != 0) return W4_ERR_ALIGN;
+    if (int e = check_device()) return e;
+    w4::PlanArgs a;
+    a.kv_len = kv_len, a.new_len = new_len, a.depth = depth;
+    a.table = table, a.owned = owned, a.free = free_pages, a.free_count = free_count, a.ldt = ldt;
+    a.q_start = q_start, a.kv_total = kv_total, a.pos = pos, a.status = status, a.slot = slot;
+    a.B = (int)B, a.W = (int)W, a.pages = (int)pages, a.page_size = (int)page_size, a.T = (int)T;
+    (void)hipGetLastError();
+    w4::launch_plan(a, (hipStream_t)stream);
+    return launched();
+  } catch (...) {
+    return W4_ERR_INTERNAL;
+  }
+}
+
+int logits_adjust(const float* logits, int64_t ldl, int64_t M, int64_t V, const w4_logit_rules* rules, float* out,
+                  int64_t ldo, w4_stream_t stream) {
+  try {
+    if (!logits || !rules || !out) return W4_ERR_NULL;
+    const w4_logit_rules& h = *rules;
+    const int64_t most = ((int64_t)1 << 31) - 1;
+    if ((h.tokens && !h.token_len) || (h.bias && (!h.bias_id || !h.bias_start))) return W4_ERR_NULL;
+    if (M < 1 || V < 1 || M > kMaxDim || V > most || ldl < V || ldo < V || ldl > ((int64_t)1 << 40) || ldo > ((int64_t)1 << 40))
+      return W4_ERR_SHAPE;
+    if (out == logits && ldo != ldl) return W4_ERR_OVERLAP;
+    if (h.requests < 1 || h.requests > most || (!h.request && M > h.requests)) return W4_ERR_SHAPE;
+    if (h.tokens && (h.max_tokens < 0 || h.max_tokens > most || h.ld_tokens < h.max_tokens || h.ld_tokens > ((int64_t)1 << 40)))
+      return W4_ERR_SHAPE;
+    if (h.bias && (h.biases < 0 || h.biases >= most)) return W4_ERR_SHAPE;
+    if (h.mask && (h.masks < 1 || h.masks > most || h.ld_mask < (V + 31) / 32 || h.ld_mask > ((int64_t)1 << 40) ||
+                   (!h.mask_row && M > h.masks)))
+      return W4_ERR_SHAPE;
+    for (const void* p : {(const void*)logits, (const void*)out, (const void*)h.request, (const void*)h.tokens,
+                          (const void*)h.token_len, (const void*)h.prompt_len, (const void*)h.repetition,
+                          (const void*)h.frequency, (const void*)h.presence, (const void*)h.bias, (const void*)h.bias_id,
+                          (const void*)h.bias_start, (const void*)h.mask, (const void*)h.mask_row})
+      if (!al4(p)) return W4_ERR_ALIGN;
+    w4::LogitArgs a;
+    a.logits = logits, a.out = out, a.ldl = ldl, a.ldo = ldo, a.M = (int)M, a.V = (int)V;
+    a.request = h.request, a.requests = (int)h.requests;
+    a.tokens = h.tokens, a.ld_tokens = h.ld_tokens, a.max_tokens = h.tokens ? (int)h.max_tokens : 0;
+    a.token_len = h.token_len, a.prompt_len = h.prompt_len;
+    a.repetition = h.repetition, a.frequency = h.frequency, a.presence = h.presence;
+    a.bias = h.bias, a.bias_id = h.bias_id, a.bias_start = h.bias_start, a.biases = h.bias ? (int)h.biases : 0;
+    a.mask = h.mask, a.ld_mask = h.ld_mask, a.masks = h.mask ? (int)h.masks : 0, a.mask_row = h.mask_row;
+    if (w4::logits_workgroups(a) >= ((int64_t)1 << 24)) return W4_ERR_SHAPE;
+    if (int e = check_device()) return e;
+    (void)hipGetLastError();
+    w4::launch_logits(a, (hipStream_t)stream);
     return launched();
   } catch (...) {
     return W4_ERR_INTERNAL;

@@ -1,4 +1,5 @@
-// rope_f16 and kv_append_rope: rotary positions, alone or on the way into a paged cache.
+// rope_f16 and kv_append_rope: rotary positions, alone or on the way into a paged cache; norm_rope_f16 and
+// kv_append_norm_rope: the same behind a norm of each query and key head.
 //
 // Mathematics.  Pair i of a head's first R dims is the complex number (a, b): dims (i, i + R/2)
 // in the half layout, (2i, 2i + 1) in the interleaved one.  It is multiplied by
@@ -8,6 +9,11 @@
 // in f64, in turns (theta / 2 pi), and reduced to [-1/2, 1/2] there; the reduced angle is good
 // to 1e-10 turns at 10^6 positions, and only then goes to f32 for sincospif.  The f64 work is
 // one pair per thread (R/2 per token, shared by all heads through LDS), so it costs little.
+//
+// The norm.  x becomes x w / sqrt(mean(x^2) + eps) over the D dims of its head, before it turns.  A head's items lie on
+// adjacent lanes, as many as the next power of two has, so that the squares of what the lanes hold anyway
+// are summed by lane moves and x is read once.  Rotations that leave single dims to a thread (R / 2 no multiple of 8) have more
+// items than a wave has lanes: there the sums are taken first, a chunk of 8 dims a lane, and x is read again, from the cache.
 //
 // Bound: HBM for prompts (each element read once, written once), the launch and the chain of
 // loads for a decode step.  So a thread's first elements, its token's slot and its head's scale
@@ -25,6 +31,7 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens of a workgroup, at most
+constexpr int kMaxHeads = 1024;  // of q, of k
 
 struct RopeArgs {
   const void* src[3];  // q, k, v rows (heads of one token are contiguous)
@@ -38,7 +45,10 @@ struct RopeArgs {
   const float* freq;
   float mscale, sign;
   int T, D, R, tokens;  // tokens: of each workgroup
-  int per, n;           // items of a rotated head, of a token
+  int per, n;           // items of a rotated head (norms: lanes, a power of two), of a token
+  int items;            // norms: items of a rotated head
+  const float* weight[2];  // norms: of q's and k's dims; nullptr: 1
+  float eps, per_dim;      // norms: per_dim = 1 / D
   float per_n, per_head, per_chunks;  // 1 / n, 1 / per, 1 / (D / 8)
 };
 
@@ -121,9 +131,31 @@ struct Item {
   int tl, item;  // token of the workgroup, item of the head
   bool rot;      // of a head that turns
   f32x8 a, b;
+  f32x8 wa, wb;  // norms: their weights
+  int head;      // norms: which of the token's
 };
 
-template <bool F32, int MODE>
+// Sum over aligned groups of n lanes, a power of two up to 32, all of them active; every lane gets it.
+__device__ __forceinline__ float lanes_sum(float v, int n) {
+  if (n >= 2) v += dpp_f<0xB1>(v);   // quad_perm [1,0,3,2]
+  if (n >= 4) v += dpp_f<0x4E>(v);   // quad_perm [2,3,0,1]
+  if (n >= 8) v += dpp_f<0x141>(v);  // row_half_mirror
+  if (n >= 16) v += dpp_f<0x140>(v);  // row_mirror
+  if (n >= 32) v += __shfl_xor(v, 16);
+  return v;
+}
+
+__device__ __forceinline__ float squares(const f32x8& x) {
+  float s = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) s += x[e] * x[e];
+  return s;
+}
+
+// what an item's values are multiplied with for a head whose squares sum up to s
+__device__ __forceinline__ float norm_of(const RopeArgs& g, float s) { return 1.f / sqrtf(s * g.per_dim + g.eps); }
+
+template <bool F32, int MODE, bool NORM>
 __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x) {
   const int half = g.R / 2, rot_heads = g.heads[0] + g.heads[1], n_rot = rot_heads * g.per;
   x.tl = divide(i, g.n, g.per_n);
@@ -140,14 +172,35 @@ __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x)
   const int64_t ldq = g.ld[0], ldk = g.ld[1], ldv = g.ld[2];
   const void* src = w == 0 ? q : w == 1 ? k : v;
   const int64_t at = (int64_t)t * (w == 0 ? ldq : w == 1 ? ldk : ldv) + (int64_t)h * g.D;
+  if constexpr (NORM) {
+    x.d.p = nullptr;
+    x.head = j;
+    x.a = 0.f, x.b = 0.f;
+    // a lane past the head's items, or past the token's: it only takes part in the sum
+    if (x.rot ? x.item >= g.items : w == 2 && h >= g.heads[2]) return;
+  }
+  const float* weight = nullptr;
+  if constexpr (NORM) {
+    const float *wq = g.weight[0], *wk = g.weight[1];
+    weight = !x.rot ? nullptr : w == 0 ? wq : wk;
+    x.wa = 1.f, x.wb = 1.f;
+  }
   if (MODE == kHalfOdd && x.rot) {
     if (x.item < half) x.a[0] = load1<F32>(src, at + x.item);
     x.b[0] = load1<F32>(src, at + x.item + half);
+    if (NORM && weight) {
+      if (x.item < half) x.wa[0] = weight[x.item];
+      x.wb[0] = weight[x.item + half];
+    }
   } else {
     const bool pair = MODE == kHalf && x.rot && x.item < g.R / 16;
     if (MODE == kHalf && x.rot && !pair) x.item += g.R / 16;
     x.a = load8<F32>(src, at + x.item * 8);
     if (pair) x.b = load8<F32>(src, at + x.item * 8 + half);
+    if (NORM && weight) {
+      x.wa = load8<true>(weight, x.item * 8);
+      if (pair) x.wb = load8<true>(weight, x.item * 8 + half);
+    }
   }
   x.d.e4m3 = w > 0 && g.c.e4m3;
   x.d.scale = 1.f;
@@ -164,8 +217,19 @@ __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x)
   }
 }
 
-template <bool F32, int MODE>
-__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, Item& x) {
+template <bool F32, int MODE, bool NORM>
+__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, const float* norms, Item& x) {
+  if constexpr (NORM) {
+    float f;
+    if (MODE == kHalfOdd)
+      f = x.rot ? norms[x.head] : 1.f;
+    else
+      f = norm_of(g, lanes_sum(squares(x.a) + squares(x.b), g.per));
+    if (x.rot) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x.a[e] = x.a[e] * f * x.wa[e], x.b[e] = x.b[e] * f * x.wb[e];
+    }
+  }
   if (x.d.p == nullptr) return;
   const int half = g.R / 2;
   const float2* cs = turn + x.tl * half;
@@ -203,13 +267,34 @@ __device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, It
   store8(x.d, c0, x.a);
 }
 
-template <bool F32, int MODE>
+// kHalfOdd's norms, of one token's rotated heads: a group of lanes takes a head.
+template <bool F32>
+__device__ __forceinline__ void odd_norms(const RopeArgs& g, int t, float* norms) {
+  int lanes = 1;
+  while (lanes < g.D / 8) lanes *= 2;
+  const int heads = g.heads[0] + g.heads[1], chunk = threadIdx.x % lanes;
+  for (int j0 = 0; j0 < heads; j0 += kThreads / lanes) {
+    const int j = j0 + threadIdx.x / lanes;
+    const bool of_q = j < g.heads[0];
+    const void *q = g.src[0], *k = g.src[1];
+    const int64_t ldq = g.ld[0], ldk = g.ld[1];
+    const int64_t at = t * (of_q ? ldq : ldk) + (int64_t)(of_q ? j : j - g.heads[0]) * g.D + chunk * 8;
+    float s = 0.f;
+    if (j < heads && chunk < g.D / 8) s = squares(load8<F32>(of_q ? q : k, at));
+    s = lanes_sum(s, lanes);
+    if (j < heads && chunk == 0) norms[j] = norm_of(g, s);
+  }
+}
+
+template <bool F32, int MODE, bool NORM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
   __shared__ float2 turn[kMaxTokens * 128];  // [token][pair]: mscale (cos, sin)
+  __shared__ float norms[NORM && MODE == kHalfOdd ? 2 * kMaxHeads : 1];
   const int t0 = blockIdx.x * g.tokens, nt = min(g.tokens, g.T - t0), half = g.R / 2, n = nt * g.n;
   Item x{};
   int i = threadIdx.x;
-  if (i < n) fetch<F32, MODE>(g, i, t0, x);
+  if (i < n) fetch<F32, MODE, NORM>(g, i, t0, x);
+  if constexpr (NORM && MODE == kHalfOdd) odd_norms<F32>(g, t0, norms);
   for (int k = threadIdx.x; k < nt * half; k += kThreads) {
     const int tl = k / half, p = k - tl * half;
     double a = (double)g.pos[t0 + tl] * (double)g.freq[p] * 0.15915494309189535;  // turns
@@ -220,32 +305,48 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
   }
   __syncthreads();
   while (i < n) {
-    finish<F32, MODE>(g, turn, x);
+    finish<F32, MODE, NORM>(g, turn, norms, x);
     i += kThreads;
-    if (i < n) fetch<F32, MODE>(g, i, t0, x);
+    if (i < n) fetch<F32, MODE, NORM>(g, i, t0, x);
   }
 }
 
-void launch(RopeArgs& g, bool f32, bool interleaved, hipStream_t st) {
+void launch(RopeArgs& g, bool f32, bool interleaved, bool norm, hipStream_t st) {
   const int mode = interleaved ? kInterleaved : (g.R / 2) % 8 == 0 ? kHalf : kHalfOdd;
-  g.per = items_of(mode, g.D, g.R);
+  g.per = g.items = items_of(mode, g.D, g.R);
+  const bool groups = norm && mode != kHalfOdd;
+  if (groups)
+    for (g.per = 1; g.per < g.items;) g.per *= 2;
   g.n = (g.heads[0] + g.heads[1]) * g.per + g.heads[2] * (g.D / 8);
+  if (groups) g.n = (g.n + g.per - 1) / g.per * g.per;  // the groups of the next token's lanes are aligned too
   g.per_n = 1.f / g.n, g.per_head = 1.f / g.per, g.per_chunks = 1.f / (g.D / 8);
   // Where tokens are plenty (8 workgroups a CU stay), narrow ones share a workgroup as long as its threads go about
   // once over their items: 8191 x 16 x 80 of f16 (160 items a token) take 10.5 us two at a time, 12.5 one at a time;
   // 8192 x 20 x 128 of f32 into the cache (176 items) 24.7 and 23.3.
   g.tokens = 1;
-  while (g.tokens < kMaxTokens && g.n * g.tokens * 2 <= kThreads * 5 / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
+  while (g.tokens < kMaxTokens && (!norm || groups) && g.n * g.tokens * 2 <= kThreads * 5 / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
   const int grid = (g.T + g.tokens - 1) / g.tokens;
-#define W4_ROPE(F, M) rope_kernel<F, M><<<grid, kThreads, 0, st>>>(g)
+#define W4_ROPE(F, M)                                               \
+  if (norm)                                                         \
+    rope_kernel<F, M, true><<<grid, kThreads, 0, st>>>(g);          \
+  else                                                              \
+    rope_kernel<F, M, false><<<grid, kThreads, 0, st>>>(g)
   if (f32) {
-    if (mode == kHalf) W4_ROPE(true, kHalf);
-    else if (mode == kInterleaved) W4_ROPE(true, kInterleaved);
-    else W4_ROPE(true, kHalfOdd);
+    if (mode == kHalf) {
+      W4_ROPE(true, kHalf);
+    } else if (mode == kInterleaved) {
+      W4_ROPE(true, kInterleaved);
+    } else {
+      W4_ROPE(true, kHalfOdd);
+    }
   } else {
-    if (mode == kHalf) W4_ROPE(false, kHalf);
-    else if (mode == kInterleaved) W4_ROPE(false, kInterleaved);
-    else W4_ROPE(false, kHalfOdd);
+    if (mode == kHalf) {
+      W4_ROPE(false, kHalf);
+    } else if (mode == kInterleaved) {
+      W4_ROPE(false, kInterleaved);
+    } else {
+      W4_ROPE(false, kHalfOdd);
+    }
   }
 #undef W4_ROPE
 }
@@ -253,18 +354,21 @@ void launch(RopeArgs& g, bool f32, bool interleaved, hipStream_t st) {
 }  // namespace
 
 void launch_rope(const void* x, bool f32, int64_t ldx, const int32_t* pos, const float* freq, uint16_t* y, int64_t ldy,
-                 int T, int H, int D, int R, bool interleaved, bool inverse, float mscale, hipStream_t st) {
+                 int T, int H, int D, int R, bool interleaved, bool inverse, float mscale, const HeadNorm* norm,
+                 hipStream_t st) {
   RopeArgs g{};
   g.src[0] = x, g.ld[0] = ldx, g.heads[0] = H;
   g.q_out = y, g.ldq_out = ldy;
   g.pos = pos, g.freq = freq, g.mscale = mscale, g.sign = inverse ? -1.f : 1.f;
   g.T = T, g.D = D, g.R = R;
-  launch(g, f32, interleaved, st);
+  if (norm) g.weight[0] = norm->q, g.eps = norm->eps, g.per_dim = 1.f / D;
+  launch(g, f32, interleaved, norm != nullptr, st);
 }
 
 void launch_kv_append(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo, int Hq, const void* k, int64_t ldk,
                       const void* v, int64_t ldv, bool f32, const KvCache& c, const int64_t* slots, const int32_t* pos,
-                      const float* freq, int T, int R, bool interleaved, float mscale, hipStream_t st) {
+                      const float* freq, int T, int R, bool interleaved, float mscale, const HeadNorm* norm,
+                      hipStream_t st) {
   RopeArgs g{};
   g.src[0] = q, g.ld[0] = ldq, g.heads[0] = q ? Hq : 0;
   g.src[1] = k, g.ld[1] = ldk, g.heads[1] = c.heads;
@@ -272,7 +376,8 @@ void launch_kv_append(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldqo,
   g.q_out = q_out, g.ldq_out = ldqo;
   g.c = c, g.slots = slots, g.pos = pos, g.freq = freq, g.mscale = mscale, g.sign = 1.f;
   g.T = T, g.D = c.dim, g.R = R;
-  launch(g, f32, interleaved, st);
+  if (norm) g.weight[0] = norm->q, g.weight[1] = norm->k, g.eps = norm->eps, g.per_dim = 1.f / c.dim;
+  launch(g, f32, interleaved, norm != nullptr, st);
 }
 
 }  // namespace w4

@@ -101,6 +101,20 @@ size_t head_topk_ws_bytes(int64_t V, int64_t K, int k);
 void launch_head_topk(const uint32_t* qw, const uint16_t* s, const uint16_t* b, const uint16_t* x, float* logits,
                       int32_t* idx, float* val, int V, int K, int k, void* ws, hipStream_t st);
 
+// Penalties, biases and token masks on logits; see w4_logit_rules and logits_adjust in w4.h.
+struct LogitArgs {
+  const float* logits;
+  float* out;
+  int64_t ldl, ldo;
+  int M, V, requests, max_tokens, biases, masks;
+  const int32_t *request, *tokens, *token_len, *prompt_len, *bias_start, *bias_id, *mask_row;  // tokens: nullptr: none
+  const float *repetition, *frequency, *presence, *bias;
+  const uint32_t* mask;
+  int64_t ld_tokens, ld_mask;
+};
+int64_t logits_workgroups(const LogitArgs& g);
+void launch_logits(const LogitArgs& g, hipStream_t st);
+
 // The allocation-free top-k's file-scope device array: its size, and its device address on
 // the current device (fetched once per device; nullptr if the runtime cannot give it).
 constexpr size_t kTopkScratchBytes = (size_t)4 << 20;
