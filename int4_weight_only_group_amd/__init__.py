@@ -670,14 +670,15 @@ def _append(fn, k, v, k_cache, v_cache, slots, positions, freq, norm, q, q_out, 
 
 
 def attention_workspace_bytes(k_cache: torch.Tensor, b: int, t: int, max_q: int, heads: int, pages_per_seq: int,
-                              window: int = 0) -> int:
+                              window: int = 0, tree: bool = False) -> int:
     """Workspace bytes attention_paged needs for t query rows of b sequences over this cache, with
-    tables of pages_per_seq pages."""
+    tables of pages_per_seq pages (tree: attention_paged_tree)."""
     c = _kv_cache(k_cache, k_cache, None, None, torch.cuda.current_device())
     need = ctypes.c_size_t(0)
     p, ld = 16, heads * c.dim
-    _check("attention_paged", lib().attention_paged(p, ld, c, p, pages_per_seq, pages_per_seq, p, p, b, t, max_q,
-                                                    heads, window, 1.0, p, ld, None, ctypes.byref(need), None))
+    name, mask = ("attention_paged_tree", (p, 1 << 18)) if tree else ("attention_paged", ())
+    _check(name, getattr(lib(), name)(p, ld, c, p, pages_per_seq, pages_per_seq, p, p, *mask, b, t, max_q, heads, window,
+                                      1.0, p, ld, None, ctypes.byref(need), None))
     return int(need.value)
 
 
@@ -725,7 +726,7 @@ def attention_paged_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """attention_paged for drafted tokens that form trees (see tree_mask): a row sees the cached tokens before
     its sequence's new ones and, of these, those whose bits are set in its row of mask, int64 [T][words] (bit j % 64 of
     word j / 64: new token j), words >= ceil(max_q / 64).  A window, at least max_q, reaches back from the row's position,
-    kv_len - n + its bits set - 1.  Everything else, the workspace's size too, is as for attention_paged."""
+    kv_len - n + its bits set - 1.  Everything else is as for attention_paged (attention_workspace_bytes with tree=True)."""
     dev = torch.cuda.current_device()
     _need(mask, "mask", torch.int64, dev)
     ldm = _rowmajor(mask, "mask")

@@ -142,6 +142,8 @@ struct Plan {
   int splits;       // few rows: parts of the keys of all sequences, about; many rows: of a row tile, at most
   int least;        // few rows: keys of a part at least
   int tiles;        // many rows: row tiles at most
+  int parts;        // trees of more rows: parts of all tiles at most (splits: workgroups of a round)
+  int start_keys;   // trees of more rows: how many keys a workgroup could take while it starts and ends
   int part_rows;    // rows kept of a part; many rows: of a row tile
   bool skip_short;  // both kernels run: sequences of at most kFewRows rows are the first one's
   float c;          // scale * log2 e
@@ -305,6 +307,129 @@ __device__ __forceinline__ int v_swz_few(int r) {
                        : (r & 7) | ((r >> 4) & 1) << 3;
 }
 
+// The 32-key tiles that one of a workgroup's NW waves takes, every NW-th of the keys [k0, k1): K and V in LDS of its own,
+// NB tiles of each, fetched by LDS DMA, and the operands that the matrix products take from there.  Turn i is tile i, or, once
+// whole_first() has been called, one of the `whole` tiles from f0 on first.
+template <int DP, bool FP8, int NW, int NB = 1>
+struct WaveTiles {
+  static constexpr int KT = kFewKeys, ES = FP8 ? 1 : 2, ROWB = DP * ES, TILE = few_tile<DP, FP8>();
+  static constexpr int CH = ROWB / 16, RPI = 64 / CH, NI = KT / RPI;  // chunks of a row; rows and count of a DMA instruction
+  static constexpr int KA = ROWB / 64;
+  static constexpr int IDS = NB == 1 ? 2 : NB == 2 ? 4 : 8;  // turns' page numbers: 2 NB at least
+  const Plan& p;
+  const int k0, k1, lane, wave;
+  const uint32_t kt, vt;
+  const int32_t* table;
+  const int* ids;
+  const uint32_t ids_at;
+  const char* bases[2];
+  const bool plain;
+  const uint32_t token_bytes;
+  uint32_t k_at[KA], v_row, v_chunk;
+  int f0 = 0, whole = 0;
+
+  // lds: NW NB pairs of tiles, then IDS * 256 bytes of page numbers a wave
+  __device__ __forceinline__ WaveTiles(const Plan& p, unsigned char* lds, int b, int kvh, int k0, int k1, int lane, int wave)
+      : p(p), k0(k0), k1(k1), lane(lane), wave(wave),
+        kt((uint32_t)(uintptr_t)(lds_void_t*)lds + wave * (2 * NB * TILE)), vt(kt + TILE),
+        table(p.a.table + (int64_t)b * p.a.ldt), ids(reinterpret_cast<const int*>(lds + NW * 2 * NB * TILE + wave * (IDS * 256))),
+        ids_at((uint32_t)(uintptr_t)(lds_void_t*)ids),
+        bases{reinterpret_cast<const char*>(p.a.c.k) + kvh * p.a.c.stride_head * ES,
+              reinterpret_cast<const char*>(p.a.c.v) + kvh * p.a.c.stride_head * ES},
+        // Whole tiles of pages of 16 n tokens: half a tile lies in one page, whose address is scalar; a lane adds its
+        // row and chunk.
+        plain(p.a.c.dim == DP && p.a.c.page_size % 16 == 0 && (k0 & 15) == 0 && p.a.c.stride_token < (1 << 20)),
+        token_bytes((uint32_t)p.a.c.stride_token * ES) {}
+
+  // the tiles that lie within [a, b) come first; all: tiles of this wave
+  __device__ __forceinline__ void whole_first(int a, int b, int all) {
+    const int at = k0 + wave * KT;  // first key of tile 0
+    f0 = min(all, max(0, a - at + KT * NW - 1) / (KT * NW));
+    whole = max(0, min(all, b - at < KT ? 0 : (b - at - KT) / (KT * NW) + 1) - f0);
+    if (whole == 0) f0 = 0;
+  }
+  __device__ __forceinline__ int first_key(int i) const {
+    if constexpr (NB > 0) i = i < whole ? f0 + i : i - whole < f0 ? i - whole : i;
+    return k0 + (i * NW + wave) * KT;
+  }
+  static __device__ __forceinline__ uint32_t buffer(int i) { return NB == 1 ? 0u : (uint32_t)(i % NB * 2 * TILE); }
+
+  __device__ __forceinline__ void fetch_ids(int t) const {
+    const int j = min(first_key(t) + (lane & 31), k1 - 1);
+    dma4(table + divide(j, p.page), ids_at + (t & (IDS - 1)) * 256);
+  }
+
+  template <class OfV>
+  __device__ __forceinline__ void fetch(int t, OfV) const {
+    constexpr bool V = OfV::value;
+    const KvCache& c = p.a.c;
+    const uint32_t st = (V ? vt : kt) + buffer(t);
+    const int j0 = first_key(t), *here = ids + (t & (IDS - 1)) * 64;
+    int lane_here = lane;  // opaque, or the lanes' offsets move out of the loop and fill registers
+    asm volatile("" : "+v"(lane_here));
+    auto chunk = [&](int r) {
+      const int ch = lane_here % CH;
+      return (V ? ch ^ v_swz_few<ROWB, FP8>(r) : ch ^ k_swz_few<ROWB>(r)) * 16;
+    };
+    if (plain && j0 + KT <= k1) {
+      const int id0 = __builtin_amdgcn_readfirstlane(here[0]);
+      const int id1 = __builtin_amdgcn_readfirstlane(here[16]);
+      if ((uint32_t)id0 < (uint32_t)c.pages && (uint32_t)id1 < (uint32_t)c.pages) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int j = j0 + 16 * half, id = half ? id1 : id0;
+          const int64_t at = id * c.stride_page + (j - divide(j, p.page) * c.page_size) * c.stride_token;
+          const char* base = bases[V] + at * ES;
+#pragma unroll
+          for (int i = 0; i < NI / 2; ++i) {
+            const int in = i * RPI + lane_here / CH;
+            dma16(base + (int64_t)i * RPI * token_bytes, (uint32_t)(lane_here / CH) * token_bytes + chunk(16 * half + in),
+                  st + (half * NI / 2 + i) * 1024);
+          }
+        }
+        return;
+      }
+    }
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + lane_here / CH, at_chunk = chunk(r);
+      const int j = j0 + r, page = divide(j, p.page), id = here[r];
+      const int64_t at = (id * c.stride_page + (j - page * c.page_size) * c.stride_token) * ES;
+      const bool in = j < k1, good = (uint32_t)id < (uint32_t)c.pages;
+      const void* from = in && !good && !V                       ? (const void*)(FP8 ? kNans8 : kNans)
+                         : in && good && at_chunk < c.dim * ES ? (const void*)(bases[V] + at + at_chunk)
+                                                               : (const void*)kZeros;
+      dma16(from, st + i * 1024);
+    }
+  }
+
+  // LDS offsets of a lane's fragments: the swizzles fold into the lane's part
+  __device__ __forceinline__ void places() {
+    const int row = lane & 15, grp = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < KA; ++x) k_at[x] = kt + row * ROWB + (((4 * x + grp) ^ k_swz_few<ROWB>(row)) * 16);
+    if constexpr (FP8) {  // 8 rows x 16 codes: lane L of 16 points at row L / 2, half L % 2
+      const int x = (lane & 15) >> 1, r = (x & 4) * 4 + 4 * grp + (x & 3);
+      v_row = vt + r * ROWB + (lane & 1) * 8, v_chunk = v_swz_few<ROWB, FP8>(r);
+    } else {
+      const int r = 4 * grp + ((lane & 15) >> 2);
+      v_row = vt + r * ROWB + (lane & 1) * 8, v_chunk = ((lane & 3) >> 1) ^ v_swz_few<ROWB, FP8>(r);
+    }
+  }
+  // V^T operand: dims 16 i + lane % 16, keys 4 grp .. + 3 and 16 + 4 grp .. + 3
+  __device__ __forceinline__ f16x8 v_frag(int i, uint32_t buf = 0) const {
+    if constexpr (FP8) {
+      const auto v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_i32x2*>(v_row + buf + (i ^ v_chunk) * 16));
+      return widen8(v[0], v[1]);
+    } else {
+      const uint32_t at = v_row + buf + ((2 * i) ^ v_chunk) * 16;
+      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
+      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 16 * ROWB));
+      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+  }
+};
+
 // The keys [lo, hi) that a sequence's rows see (lo rounded down to 16, for whole pages); n < 0: not this
 // kernel's sequence.
 struct FewKeys {
@@ -434,67 +559,10 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
   const int D = g.c.dim;
   if (p.part && kvh == 0 && index == 0 && threadIdx.x == 0) p.head[b] = {part, count, 0, 0};
 
-  const uint32_t kt = (uint32_t)(uintptr_t)(lds_void_t*)lds + wave * 2 * TILE, vt = kt + TILE;  // this wave's tiles
-  const int32_t* table = g.table + (int64_t)b * g.ldt;
-  auto first_key = [&](int t) { return k0 + (t * NW + wave) * KT; };
-
-  constexpr int CH = ROWB / 16, RPI = 64 / CH, NI = KT / RPI;  // chunks of a row; rows and count of a DMA instruction
-  const int* ids = reinterpret_cast<const int*>(lds + NW * 2 * TILE + wave * 512);  // two tiles' page numbers
-  const uint32_t ids_at = (uint32_t)(uintptr_t)(lds_void_t*)ids;
-  auto fetch_ids = [&](int t) {
-    const int j = min(first_key(t) + (lane & 31), k1 - 1);
-    dma4(table + divide(j, p.page), ids_at + (t & 1) * 256);
-  };
-  const char* bases[2] = {reinterpret_cast<const char*>(g.c.k) + kvh * g.c.stride_head * ES,
-                          reinterpret_cast<const char*>(g.c.v) + kvh * g.c.stride_head * ES};
-  // Whole tiles of pages of 16 n tokens: half a tile lies in one page, whose address is scalar; a lane adds its
-  // row and chunk.
-  const bool plain = D == DP && g.c.page_size % 16 == 0 && (k0 & 15) == 0 && g.c.stride_token < (1 << 20);
-  const uint32_t token_bytes = (uint32_t)g.c.stride_token * ES;
-  auto fetch = [&](int t, auto of_v) {
-    constexpr bool V = decltype(of_v)::value;
-    const uint32_t st = V ? vt : kt;
-    const int j0 = first_key(t);
-    int lane_here = lane;  // opaque, or the lanes' offsets move out of the loop and fill registers
-    asm volatile("" : "+v"(lane_here));
-    auto chunk = [&](int r) {
-      const int ch = lane_here % CH;
-      return (V ? ch ^ v_swz_few<ROWB, FP8>(r) : ch ^ k_swz_few<ROWB>(r)) * 16;
-    };
-    if (plain && j0 + KT <= k1) {
-      const int id0 = __builtin_amdgcn_readfirstlane(ids[(t & 1) * 64]);
-      const int id1 = __builtin_amdgcn_readfirstlane(ids[(t & 1) * 64 + 16]);
-      if ((uint32_t)id0 < (uint32_t)g.c.pages && (uint32_t)id1 < (uint32_t)g.c.pages) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int j = j0 + 16 * half, id = half ? id1 : id0;
-          const int64_t at = id * g.c.stride_page + (j - divide(j, p.page) * g.c.page_size) * g.c.stride_token;
-          const char* base = bases[V] + at * ES;
-#pragma unroll
-          for (int i = 0; i < NI / 2; ++i) {
-            const int in = i * RPI + lane_here / CH;
-            dma16(base + (int64_t)i * RPI * token_bytes, (uint32_t)(lane_here / CH) * token_bytes + chunk(16 * half + in),
-                  st + (half * NI / 2 + i) * 1024);
-          }
-        }
-        return;
-      }
-    }
-#pragma unroll 1
-    for (int i = 0; i < NI; ++i) {
-      const int r = i * RPI + lane_here / CH, at_chunk = chunk(r);
-      const int j = j0 + r, page = divide(j, p.page), id = ids[(t & 1) * 64 + r];
-      const int64_t at = (id * g.c.stride_page + (j - page * g.c.page_size) * g.c.stride_token) * ES;
-      const bool in = j < k1, good = (uint32_t)id < (uint32_t)g.c.pages;
-      const void* from = in && !good && !V                   ? (const void*)(FP8 ? kNans8 : kNans)
-                         : in && good && at_chunk < D * ES ? (const void*)(bases[V] + at + at_chunk)
-                                                           : (const void*)kZeros;
-      dma16(from, st + i * 1024);
-    }
-  };
+  WaveTiles<DP, FP8, NW> keys(p, lds, b, kvh, k0, k1, lane, wave);
   constexpr std::false_type K_{};
   constexpr std::true_type V_{};
-  if (mine > 0) fetch_ids(0), fetch_ids(1);
+  if (mine > 0) keys.fetch_ids(0), keys.fetch_ids(1);
 
   // Q^T operand: lane (row = lane % 16, grp = lane / 16), step t.  f16: dims 32 t + 8 grp ..; e4m3: a
   // 16-byte chunk of K feeds two steps, so dims 16 (4 (t / 2) + grp) + 8 (t % 2) ..
@@ -522,47 +590,24 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
 #pragma unroll
   for (int i = 0; i < DB; ++i) acc[i] = {0.f, 0.f, 0.f, 0.f};
 
-  // LDS offsets of a lane's fragments: the swizzles fold into the lane's part
+  keys.places();
   constexpr int KA = ROWB / 64;  // 64-byte blocks of a row: chunks 4 x + grp
-  uint32_t k_at[KA];
-#pragma unroll
-  for (int x = 0; x < KA; ++x) k_at[x] = kt + row * ROWB + (((4 * x + grp) ^ k_swz_few<ROWB>(row)) * 16);
-  uint32_t v_row, v_chunk;
-  if constexpr (FP8) {  // 8 rows x 16 codes: lane L of 16 points at row L / 2, half L % 2
-    const int x = (lane & 15) >> 1, r = (x & 4) * 4 + 4 * grp + (x & 3);
-    v_row = vt + r * ROWB + (lane & 1) * 8, v_chunk = v_swz_few<ROWB, FP8>(r);
-  } else {
-    const int r = 4 * grp + ((lane & 15) >> 2);
-    v_row = vt + r * ROWB + (lane & 1) * 8, v_chunk = ((lane & 3) >> 1) ^ v_swz_few<ROWB, FP8>(r);
-  }
-  // V^T operand: dims 16 i + lane % 16, keys 4 grp .. + 3 and 16 + 4 grp .. + 3
-  auto v_frag = [&](int i) {
-    if constexpr (FP8) {
-      const auto v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(reinterpret_cast<lds_i32x2*>(v_row + (i ^ v_chunk) * 16));
-      return widen8(v[0], v[1]);
-    } else {
-      const uint32_t at = v_row + ((2 * i) ^ v_chunk) * 16;
-      const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at));
-      const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_s16x4*>(at + 16 * ROWB));
-      return __builtin_bit_cast(f16x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-    }
-  };
 
   if (mine > 0) {
     wait_vm<0>();
-    fetch(0, K_);
-    fetch(0, V_);
+    keys.fetch(0, K_);
+    keys.fetch(0, V_);
   }
   for (int t = 0; t < mine; ++t) {
-    const int j0 = first_key(t);
-    wait_vm<NI>();  // V of this tile may be in flight
+    const int j0 = keys.first_key(t);
+    wait_vm<keys.NI>();  // V of this tile may be in flight
     f32x4 sc[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       sc[kb] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < KA; ++x) {
-        const uint32_t at = k_at[x] + 16 * kb * ROWB;
+        const uint32_t at = keys.k_at[x] + 16 * kb * ROWB;
         if constexpr (FP8) {
           const u32x4 codes = *reinterpret_cast<const lds_u32x4*>(at);
           sc[kb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(codes[0], codes[1]), q[2 * x], sc[kb], 0, 0, 0);
@@ -574,8 +619,8 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
     }
     if (t + 1 < mine) {
       wait_lds();  // K has been read
-      fetch_ids(t + 2);
-      fetch(t + 1, K_);
+      keys.fetch_ids(t + 2);
+      keys.fetch(t + 1, K_);
     }
     // sc[kb][e]: key j0 + 16 kb + 4 grp + e of this lane's row
     const bool edge = j0 + KT > all1 || j0 < all0;
@@ -625,16 +670,16 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
       acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w_low, acc[i], 0, 0, 0);
     };
     if (t + 1 < mine)
-      wait_vm<NI + 1>();  // K and the page numbers of the next tiles may be in flight
+      wait_vm<keys.NI + 1>();  // K and the page numbers of the next tiles may be in flight
     else
       wait_vm<0>();
     if (!edge || (!TREE && n == 1 && j0 >= all0)) {  // no row sees less of the tile's keys (past k1: zeros) than another
 #pragma unroll
-      for (int i = 0; i < DB; ++i) add(i, v_frag(i));
+      for (int i = 0; i < DB; ++i) add(i, keys.v_frag(i));
     } else {
       uint32_t odd = 0;
 #pragma unroll
-      for (int i = 0; i < DB; ++i) add(i, finite(v_frag(i), odd));
+      for (int i = 0; i < DB; ++i) add(i, finite(keys.v_frag(i), odd));
       if (__any(odd != 0)) {
 #pragma unroll 1
         for (int r = 0; r < KT; ++r) {
@@ -642,7 +687,7 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
 #pragma unroll
           for (int i = 0; i < DB; ++i) {
             const int byte = (16 * i + 4 * grp) * ES;
-            const uint32_t at = vt + r * ROWB + ((byte / 16) ^ v_swz_few<ROWB, FP8>(r)) * 16 + byte % 16;
+            const uint32_t at = keys.vt + r * ROWB + ((byte / 16) ^ v_swz_few<ROWB, FP8>(r)) * 16 + byte % 16;
             f16x4 v;
             if constexpr (FP8) {
               const f16x8 x = widen8(*reinterpret_cast<const lds_i32*>(at), 0);
@@ -658,7 +703,7 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
     }
     if (t + 1 < mine) {
       wait_lds();  // V has been read
-      fetch(t + 1, V_);
+      keys.fetch(t + 1, V_);
     }
   }
 
@@ -762,6 +807,108 @@ __device__ __forceinline__ Seq locate(const Plan& p, int tile, int& b, int& at) 
   return {0, 0, 0};
 }
 
+// Trees: which row tile and which of its parts the part-th workgroup takes.  All rows of a sequence see its old keys, so that a
+// tile's work goes by its sequence's length, and the keys of all tiles are dealt out in parts of about the same
+// length, which the workgroups choose from the lengths: by the longest sequence's, 16 of 301 to 8192 keys (7 to 48 rows of two
+// heads each, on 8 kv heads of 128 dims, e4m3) take 125 us in the kernel for many rows, and so 67.  (Ranges of equal length
+// that go on from tile to tile balance better and take longer: a workgroup's second part starts as slowly as its first.)
+struct DealtTile {
+  int b, tile, slot;        // b < 0: past the last; slot: the tile's number in the batch
+  int index, count, first;  // part of the tile, its parts, the first of them
+  Seq s;
+};
+template <int NW, int KT, int UNIT>
+__device__ __forceinline__ DealtTile deal_tiles(const Plan& p, int part, unsigned char* lds) {
+  __shared__ int64_t sums[2][NW];
+  __shared__ DealtTile found;
+  const int B = p.a.B, each = (B + 64 * NW - 1) / (64 * NW), lane = threadIdx.x & 63;
+  auto keys = [&](const Seq& s) {
+    const Keys k = keys_of<true>(p, s, 0, 0, KT, UNIT, UNIT);
+    return k.hi - k.lo;
+  };
+  auto parts_of = [&](int keys, int per) { return max(1, (keys + per - 1) / per); };
+  // Keys of a part where all tiles have `all`, f of an equal share of the p.splits workgroups of a round.
+  auto share = [&](int64_t all, float f) {
+    const int64_t x = (int64_t)((float)all * f / (float)p.splits) + 1;
+    return (int)min((int64_t)1 << 30, max((int64_t)kMinPart, (x + UNIT - 1) / UNIT * UNIT));
+  };
+  // The best of 64 lengths of parts from a half to 4 shares: rounds of the parts they make, times their length and what a
+  // workgroup takes to start and end, in keys.  count(per): parts of all tiles.
+  auto choose = [&](int64_t all, auto count) {
+    const int per = share(all, .5f * __builtin_amdgcn_exp2f((float)lane * (3.f / 63.f)));
+    const float rounds = ceilf(count(per) / (float)p.splits);
+    float best = rounds * (float)(per + p.start_keys), least = best;
+    least = fminf(least, __shfl_xor(least, 32));
+    least = fminf(least, __shfl_xor(least, 16));
+    least = fminf(least, __shfl_xor(least, 8));
+    least = fminf(least, __shfl_xor(least, 4));
+    least = fminf(least, __shfl_xor(least, 2));
+    least = fminf(least, __shfl_xor(least, 1));
+    return __builtin_amdgcn_readlane(per, __builtin_ctzll(__ballot(best == least)));
+  };
+  auto spare = [&](int tiles) {  // tiles that the launch allows for and the batch does not have
+    if (p.part && blockIdx.x == 0)
+      for (int i = tiles + threadIdx.x; i < p.tiles; i += 64 * NW) p.head[i] = {0, 0, 0, 0};
+  };
+  if (B == 1) {
+    const Seq s = sequence(p.a, 0);
+    const int n = tiles_of(p, s.n), k = keys(s);
+    spare(n);
+    int per = 1 << 30;
+    if (p.part) per = choose((int64_t)n * k, [&](int per) { return (float)n * (float)parts_of(k, per); });
+    const int count = parts_of(k, per), tile = part / count;
+    return {tile < n ? 0 : -1, tile, tile, part - tile * count, count, tile * count, s};
+  }
+  const int b0 = min(B, (int)threadIdx.x * each), b1 = min(B, b0 + each);
+  if (threadIdx.x == 0) found.b = -1;
+  int64_t mine = 0, before = 0;
+  Seq one{0, 0, 0};  // this thread's sequence when it has at most one
+  int one_keys = 0;
+  for (int b = b0; b < b1; ++b) {
+    one = sequence(p.a, b);
+    one_keys = keys(one);
+    mine += (int64_t)tiles_of(p, one.n) * one_keys;
+  }
+  int per = 1 << 30;
+  if (p.part) {
+    int2* seqs = reinterpret_cast<int2*>(lds);  // keys, tiles
+    if (each == 1 && b0 < B) seqs[b0] = {one_keys, tiles_of(p, one.n)};
+    const int64_t all = block_scan<NW>(mine, before, sums[0]);
+    if (each == 1)
+      per = choose(all, [&](int per) {
+        const float f = 1.f / (float)per;
+        float n = 0.f;
+        for (int b = 0; b < B; ++b) n += (float)seqs[b].y * fmaxf(1.f, ceilf((float)seqs[b].x * f));
+        return n;
+      });
+    else  // many sequences: parts are short beside a round
+      per = share(all, .5f);
+  }
+  mine = 0;  // tiles, and their parts
+  for (int b = b0; b < b1; ++b) {
+    const Seq s = each == 1 ? one : sequence(p.a, b);
+    const int n = tiles_of(p, s.n);
+    mine += (int64_t)n << 32 | (uint32_t)(n * parts_of(keys(s), per));
+  }
+  const int64_t total = block_scan<NW>(mine, before, sums[1]);
+  int at = (int)before, slot = (int)(before >> 32);
+  if (part >= at && part < at + (int)mine) {
+    for (int b = b0; b < b1; ++b) {
+      const Seq s = each == 1 ? one : sequence(p.a, b);
+      const int n = tiles_of(p, s.n), count = n > 0 ? parts_of(keys(s), per) : 1;
+      if (part < at + n * count) {
+        const int tile = (part - at) / count;
+        found = {b, tile, slot + tile, part - at - tile * count, count, at + tile * count, s};
+        break;
+      }
+      at += n * count, slot += n;
+    }
+  }
+  spare((int)(total >> 32));
+  __syncthreads();
+  return found;
+}
+
 template <int DP, bool FP8, int KS, bool TREE>
 __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attention_many_kernel(Plan p) {
   constexpr int NW = kManyWaves, RG = NW / KS, ROWS = 32 * RG;  // row blocks, rows
@@ -772,18 +919,35 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // the last tiles of a sequence see the most keys: they go first
   const int kvh = blockIdx.x % g.c.heads, rest = blockIdx.x / g.c.heads;
-  const int split = rest % p.splits, slot = p.tiles - 1 - rest / p.splits;
-  int b, tile;
-  const Seq s = locate(p, slot, b, tile);
-  if (b < 0) {
-    if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {0, 0, 0, 0};
-    return;
+  int b, tile, split, slot, part;  // part: its number in the workspace
+  Seq s;
+  int first = 0, parts = 0;
+  if constexpr (TREE) {
+    const DealtTile d = deal_tiles<NW, KT, KT * KS>(p, rest, lds);
+    if (d.b < 0) return;
+    auto scalar = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    b = scalar(d.b), tile = scalar(d.tile), split = scalar(d.index), slot = scalar(d.slot);
+    s = {scalar(d.s.first), scalar(d.s.n), scalar(d.s.len)};
+    first = scalar(d.first), parts = scalar(d.count), part = rest;
+  } else {
+    split = rest % p.splits, slot = p.tiles - 1 - rest / p.splits, part = slot * p.splits + split;
+    s = locate(p, slot, b, tile);
+    if (b < 0) {
+      if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {0, 0, 0, 0};
+      return;
+    }
   }
   const int D = g.c.dim, all_rows = s.n * p.G, r0 = tile * ROWS, r1 = min(all_rows, r0 + ROWS);
-  const Keys k = keys_of<TREE>(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT * KS);
-  if (split >= k.act) return;
-  if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {slot * p.splits, k.act, b, tile};
-  const int k0 = k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
+  Keys k = keys_of<TREE>(p, s, divide(r0, p.group), divide(r1 - 1, p.group), KT, KT, 2 * KT * KS);
+  if constexpr (TREE) {
+    k.act = parts;
+    k.per = ((k.hi - k.lo + parts - 1) / parts + KT * KS - 1) / (KT * KS) * (KT * KS);
+  } else {
+    if (split >= k.act) return;
+    first = slot * p.splits;
+  }
+  if (p.part && kvh == 0 && split == 0 && threadIdx.x == 0) p.head[slot] = {first, k.act, b, tile};
+  const int k0 = TREE ? min(k.hi, k.lo + split * k.per) : k.lo + split * k.per, k1 = min(k.hi, k0 + k.per);
   const int tiles = (k1 - k0 + KT - 1) / KT;
   const int32_t* table = g.table + (int64_t)b * g.ldt;
 
@@ -845,7 +1009,17 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
   int f0 = 0, whole;
   {
     const int end = TREE ? at0 - 1 : at0 + divide(r0, p.group);
-    const int beg = g.window ? at0 + (TREE ? s.n - 1 : divide(r1 - 1, p.group)) - g.window : 0;
+    int beg = g.window ? at0 + (TREE ? s.n - 1 : divide(r1 - 1, p.group)) - g.window : 0;
+    if constexpr (TREE) {  // depths are known: the deepest row's first key
+      if (g.window) {
+        __shared__ int deepest;
+        if (threadIdx.x == 0) deepest = 0;
+        __syncthreads();
+        atomicMax(&deepest, tree.lo);
+        __syncthreads();
+        beg = __builtin_amdgcn_readfirstlane(deepest);
+      }
+    }
     f0 = max(0, beg - k0 + KT - 1) / KT;
     whole = max(0, max(0, min(end, k1) - k0) / KT - f0);
     if (whole == 0) f0 = 0;
@@ -970,6 +1144,11 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
     for (int u = 0; u < SUB; ++u) {
       const int j0 = k0 + tile_at(i) * KT + 32 * u;
       if (j0 >= any1 || j0 + 32 <= any0) continue;
+      uint32_t sees = 0;
+      if constexpr (TREE) {
+        sees = tree_sees(tree, j0);
+        if (!__any(sees != 0)) continue;
+      }
       const uint32_t kt = k_tile(i) + u * HALF, vt = v_tile(i) + u * HALF;
 #pragma unroll
       for (int e = 0; e < 16; ++e) sc[e] = 0.f;
@@ -977,8 +1156,6 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
       for (int st = 0; st < STEPS; ++st)
         sc = __builtin_amdgcn_mfma_f32_32x32x16_f16(k_frag(kt, st), q[st], sc, 0, 0, 0);
       top = -INFINITY;
-      uint32_t sees = 0;
-      if constexpr (TREE) sees = tree_sees(tree, j0);
       // whether this lane's row sees key j0 + r
       auto seen = [&](int r) W4_INLINE { return TREE ? (sees >> r & 1) != 0 : j0 + r >= see0 && j0 + r < see1; };
 #pragma unroll
@@ -1369,7 +1546,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
       for (int i = lane; i < rows * XW; i += 64) {
         const int r = i / XW, x = i % XW;
         if (d0 + 4 * x < D)
-          *reinterpret_cast<f32x4*>(part_row(p, (int64_t)slot * p.splits + split, kvh, wr0 - r0 + r) + d0 + 4 * x) = *four_of(r, x);
+          *reinterpret_cast<f32x4*>(part_row(p, part, kvh, wr0 - r0 + r) + d0 + 4 * x) = *four_of(r, x);
       }
     } else {
       for (int i = lane; i < rows * XW / 2; i += 64) {
@@ -1387,7 +1564,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
     wait_lds();
   }
   if (k.act > 1 && h == 0 && lane < rows) {
-    float* to_ml = part_row(p, (int64_t)slot * p.splits + split, kvh, wr0 - r0 + lane) + D;
+    float* to_ml = part_row(p, part, kvh, wr0 - r0 + lane) + D;
     to_ml[0] = m, to_ml[1] = l;
   }
 }
@@ -1485,6 +1662,9 @@ struct Launch {
   bool few, many;
   int few_splits, few_parts, few_rows, few_least;  // few_parts 0: one workgroup per (sequence, kv head), no parts
   int many_splits, many_rows, tiles;
+  bool tree;       // trees: attention_tree.hip's kernel
+  int start_keys;  // trees: see Plan
+  int tree_parts;  // trees: of all tiles, at most (many_splits: about)
   size_t few_bytes, many_bytes;
 };
 
@@ -1502,6 +1682,49 @@ FewShape few_shape_of(const AttnArgs& a) {
                   : d <= 64 ? few_shape<64, false>() : d <= 128 ? few_shape<128, false>() : few_shape<256, false>();
 }
 
+// Up to how many rows, and words of a mask: 16 sequences of up to 4096 keys, 8 kv heads, in that kernel and in the one for many rows:
+// e4m3, 128 dims: 64 rows 39.1 / 46.5 us, 96 rows 46.5 / 48.8, 128 rows 54.2 / 52.6; 256 dims, 96 rows 75.5 / 91.7;
+// f16, 128 dims: 64 rows 46.6 / 51.1, 96 rows 52.5 / 52.4, 128 rows 69.8 / 55.5; 256 dims, 64 rows 102 / 97 (two
+// sequences 30 / 39), 96 rows 120 / 101; 64 dims, 80 rows 33.7 / 38.6, 128 rows 41.8 / 40.4.
+int tree_most(const AttnArgs& a) { return a.c.e4m3 || a.c.dim <= 64 ? 96 : 64; }
+constexpr int kTreeWords = 2;
+template <int DP>
+constexpr int tree_blocks() { return DP == 256 ? 2 : 4; }  // of 16 rows
+template <int DP, bool FP8>
+constexpr int tree_waves() { return few_tile<DP, FP8>() == 8192 ? 8 : 4; }
+template <int DP, bool FP8>
+constexpr int tree_buffers() { return few_tile<DP, FP8>() > 2048 ? 1 : 2; }
+template <int DP, bool FP8>
+constexpr int tree_per_cu() { return few_tile<DP, FP8>() <= 4096 ? 2 : 1; }  // workgroups
+// a wave's tiles and page numbers; then the queries and masks
+template <int DP, bool FP8>
+constexpr int tree_wave_lds() {
+  return 2 * tree_buffers<DP, FP8>() * few_tile<DP, FP8>() + 256 * WaveTiles<DP, FP8, 1, tree_buffers<DP, FP8>()>::IDS;
+}
+template <int DP, bool FP8>
+constexpr int tree_lds() { return tree_waves<DP, FP8>() * tree_wave_lds<DP, FP8>() + 16 * tree_blocks<DP>() * (DP * 2 + 8 * kTreeWords); }
+int tree_rows(const AttnArgs& a) { return 16 * (a.c.dim <= 128 ? tree_blocks<128>() : tree_blocks<256>()); }
+
+// Trees of many rows: rows of a tile, and about how many parts there should be of all tiles together, for one round of the
+// workgroups that the CUs hold.
+template <class F>
+void plan_tree(const AttnArgs& a, int64_t most, F row_tiles, Launch& x) {
+  const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.heads);
+  x.tree = rows <= tree_most(a);
+  // The kernel for many rows in tiles of 128: 64 take 140 us against 127 for 4 sequences of 61 to 200 rows of two heads,
+  // 256 dims, a window of 4096, 168 and 124 at 128 dims without it in e4m3, 24 and 22 for one of 512 rows and 4096 keys.
+  x.many_rows = x.tree ? tree_rows(a) : 128;
+  const int per_cu = x.tree ? (a.c.dim * (a.c.e4m3 ? 1 : 2) <= 128 ? 2 : 1)
+                            : a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>();
+  // what a workgroup takes to start and end, and its part to be joined: about 12 us
+  x.start_keys = (x.tree ? 1000 : 500) * 128 / std::max(a.c.dim, 64);
+  const int64_t tiles = row_tiles(x.many_rows), slots = std::max(1, per_cu * kCus / a.c.heads);
+  const int64_t keys = a.window ? std::min(most, (int64_t)a.window + a.max_q + 64) : most;
+  x.tiles = (int)tiles;
+  x.many_splits = (int)slots;
+  x.tree_parts = (int)std::min(2 * slots + tiles, tiles * ((keys + kMinPart - 1) / kMinPart));
+}
+
 // Lengths are on the device, so that the table's width stands for every sequence's.  Where it is much wider than they
 // are, calls are cut for longer ones (16 heads on 2 of 128 dims, tables as wide as needed / of 1024 pages of 16): a
 // prompt of 1570 tokens 30.6 / 37.9 us (128 rows in two parts), 300 after 2000 27.7 / 30.3, one token after 200 8.1 /
@@ -1512,7 +1735,7 @@ Launch plan(const AttnArgs& a) {
   const int64_t most = (int64_t)a.W * a.c.page_size;
   x.few = (int64_t)a.max_q * G <= kFewRows;
   x.many = !x.few;
-  if (x.many && a.B > 1 && G <= kFewRows && (int64_t)a.B * a.max_q != a.T) x.few = true;
+  if (x.many && !a.mask && a.B > 1 && G <= kFewRows && (int64_t)a.B * a.max_q != a.T) x.few = true;
   const size_t row = (size_t)(a.c.dim + 4) * sizeof(float);
   if (x.few) {
     // at most: 16 tokens' window, from a multiple of 16
@@ -1565,8 +1788,12 @@ Launch plan(const AttnArgs& a) {
         x.many_rows = rows, x.tiles = (int)tiles, x.many_splits = (int)splits;
       }
     }
+    if (a.mask) plan_tree(a, most, row_tiles, x);
     const int64_t items = (int64_t)x.tiles * a.c.heads;
-    if (x.many_splits > 1)
+    if (a.mask) {
+      if (x.tree_parts > x.tiles)
+        x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)x.tree_parts * a.c.heads * x.many_rows * row;
+    } else if (x.many_splits > 1)
       x.many_bytes = (size_t)x.tiles * sizeof(int4) + (size_t)items * x.many_splits * x.many_rows * row;
   }
   return x;
@@ -1580,6 +1807,7 @@ bool launchable(const Launch& x, const AttnArgs& a) {
     if ((x.few_parts ? x.few_parts : a.B) * heads >= kMost) return false;
     if (x.few_parts && a.B * heads * x.few_rows >= kMost) return false;
   }
+  if (x.many && a.mask) return (int64_t)x.tree_parts * heads < kMost;
   return !x.many || x.tiles * heads * x.many_splits < kMost;  // parts are for few tiles: their join is small
 }
 
@@ -1600,14 +1828,14 @@ void launch_many_ks(const Plan& p, int items, hipStream_t st) {
     (void)hipFuncSetAttribute(reinterpret_cast<const void*>(attention_many_kernel<DP, FP8, KS, TREE>),
                               hipFuncAttributeMaxDynamicSharedMemorySize, many_lds<DP, KS>());
   });
-  attention_many_kernel<DP, FP8, KS, TREE><<<items * p.splits, 64 * kManyWaves, many_lds<DP, KS>(), st>>>(p);
+  attention_many_kernel<DP, FP8, KS, TREE><<<TREE ? p.parts * p.a.c.heads : items * p.splits, 64 * kManyWaves, many_lds<DP, KS>(), st>>>(p);
 }
 template <int DP, bool FP8, bool TREE>
 void launch_many(const Plan& p, int items, hipStream_t st) {
-  if (p.part_rows == 64)
-    launch_many_ks<DP, FP8, 2, TREE>(p, items, st);
-  else
-    launch_many_ks<DP, FP8, 1, TREE>(p, items, st);
+  if constexpr (!TREE) {
+    if (p.part_rows == 64) return launch_many_ks<DP, FP8, 2, false>(p, items, st);
+  }
+  launch_many_ks<DP, FP8, 1, TREE>(p, items, st);
 }
 
 template <bool FEW, bool WIDE>
@@ -1620,6 +1848,9 @@ void launch_join(const Plan& p, int items, hipStream_t st) {
   else
     attention_join_kernel<FEW, WIDE, 4><<<grid, 256, 0, st>>>(p);
 }
+
+template <bool FP8>
+void launch_tree(const Plan& p, hipStream_t st);  // attention_tree.hip's; no other file has TREE
 
 template <bool FP8, bool TREE>
 void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
@@ -1638,14 +1869,24 @@ void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
     ws += x.few_bytes;
     p.splits = x.many_splits, p.part_rows = x.many_rows, p.tiles = x.tiles;
     p.head = reinterpret_cast<int4*>(ws);
-    p.part = x.many_splits > 1 ? reinterpret_cast<float*>(ws + (size_t)x.tiles * sizeof(int4)) : nullptr;
+    p.parts = x.tree_parts, p.start_keys = x.start_keys;
+    p.part = (TREE ? x.tree_parts > x.tiles : x.many_splits > 1) ? reinterpret_cast<float*>(ws + (size_t)x.tiles * sizeof(int4)) : nullptr;
     const int items = x.tiles * heads;
-    if (D <= 64) launch_many<64, FP8, TREE>(p, items, st);
-    else if (D <= 128) launch_many<128, FP8, TREE>(p, items, st);
-    else launch_many<256, FP8, TREE>(p, items, st);
+    bool between = false;
+    if constexpr (TREE)
+      if (x.tree) launch_tree<FP8>(p, st), between = true;
+    if (between) {
+    } else if (D <= 64) {
+      launch_many<64, FP8, TREE>(p, items, st);
+    } else if (D <= 128) {
+      launch_many<128, FP8, TREE>(p, items, st);
+    } else {
+      launch_many<256, FP8, TREE>(p, items, st);
+    }
     // many parts: a workgroup per row
-    if (p.splits >= 16) launch_join<false, true>(p, items, st);
-    else if (p.splits > 1) launch_join<false, false>(p, items, st);
+    // (trees: or few rows)
+    if (p.part && ((TREE ? x.tree_parts / x.tiles : p.splits) >= 16 || (TREE && items * x.many_rows <= 2048))) launch_join<false, true>(p, items, st);
+    else if (p.part) launch_join<false, false>(p, items, st);
   }
 }
 

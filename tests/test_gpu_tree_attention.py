@@ -218,3 +218,81 @@ def test_bindings_refuse(w4):  # noqa: F811
     for bad in (dict(window=1), dict(scale=0.0), dict(window=-1)):
         with pytest.raises(w4.W4Error):
             w4.attention_paged_tree(**{**ok, **bad})
+
+
+@pytest.mark.parametrize("b,hq,hkv,d,e4m3", [(130, 4, 1, 64, False), (300, 8, 2, 128, True), (700, 4, 2, 64, False),
+                                             (1300, 4, 1, 64, True)])
+@pytest.mark.parametrize("n", [3, 24, 70])
+def test_many_sequences(w4, b, hq, hkv, d, e4m3, n):  # noqa: F811
+    # more than a workgroup's threads, lengths from none to some; rows of one kernel and of the others
+    rng = np.random.default_rng(b + n)
+    if n == 70:
+        b = b // 5
+    kv = rng.integers(0, 90, b)
+    kv[[0, b // 2]] = 1500, 400
+    new = rng.integers(0, n + 1, b)
+    new[b // 3] = n
+    s = Tree([(int(q), int(x)) for q, x in zip(new, kv)], hq, hkv, d, 16, e4m3, seed=b, kind="any")
+    s.check(s.run(w4))
+    s.check(s.run(w4, window=75), window=75)
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,e4m3", [
+    ([(24, 5000), (11, 900), (5, 64)], 8, 2, 128, True), ([(24, 5000), (11, 900)], 8, 2, 64, False),
+    ([(16, 5000), (9, 900), (1, 31)], 8, 2, 256, False), ([(24, 3000), (20, 900)], 8, 2, 256, True),
+    ([(16, 9000)], 4, 1, 96, False), ([(9, 700), (8, 40), (32, 32)], 2, 2, 128, False)])
+def test_the_kernel_between(w4, lens, hq, hkv, d, e4m3):  # noqa: F811
+    # up to 96 rows of a tile or two, whole and half full, in one part and in many
+    for window in (0, 200):
+        s = Tree(lens, hq, hkv, d, 16, e4m3, seed=21, kind="any")
+        s.check(s.run(w4, window=window), window=window)
+    s = Tree(lens, hq, hkv, d, 7, e4m3, seed=22)
+    s.check(s.run(w4))
+
+
+def test_workspace_is_of_the_size_that_is_asked_for(w4):  # noqa: F811
+    for lens, hq, hkv, d in (([(24, 5000), (11, 900)], 8, 2, 128), ([(100, 3000), (60, 900)], 8, 2, 64), ([(4, 3000)], 8, 2, 128)):
+        s = Tree(lens, hq, hkv, d, 16, seed=23)
+        need = w4.attention_workspace_bytes(s.dev[0], len(lens), s.q.shape[0], max(n for n, _ in lens), hq, s.table.shape[1],
+                                            tree=True)
+        assert need > 0
+        ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+        for fill in (0xFF, 0x00, 0x7E):
+            ws[:need].fill_(fill)
+            s.check(s.run(w4, workspace=ws[:need]))
+            assert (ws[need:] == 0xA5).all()
+
+
+def test_captured_and_replayed(w4):  # noqa: F811
+    # two graphs share a workspace; lengths and masks change between replays, each is compared with the eager call
+    s = Tree([(12, 400), (9, 300), (12, 40)], 8, 2, 128, 16, seed=24)
+    q, t, ln, mask, kw = dev(s.q), dev(s.table), dev(s.kv_len), s.mask[:, :1].clone(), s.kw()
+    out = [torch.empty_like(q) for _ in range(2)]
+    kw["workspace"] = torch.empty(max(16, w4.attention_workspace_bytes(s.dev[0], 3, q.shape[0], 12, 8, t.shape[1], tree=True)),
+                                  dtype=torch.uint8, device="cuda")
+
+    def call(o):
+        w4.attention_paged_tree(q, *s.dev, t, ln, mask, out=o, **kw)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        side.wait_stream(torch.cuda.current_stream())
+        call(out[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, o in zip(graphs, out):
+        with torch.cuda.graph(g):
+            call(o)
+    for i in range(5):
+        s.kv_len = np.array([400 - 90 * i, 300 - 7 * i, 40 - 5 * i], dtype=np.int32)
+        s.sees = [x if (j + i) % 3 else set() for j, x in enumerate(s.sees)]
+        ln.copy_(dev(s.kv_len))
+        mask.copy_(dev(words_of(s.sees, 1)))
+        for g, o in zip(graphs, out):
+            o.fill_(7.0)
+            g.replay()
+        torch.cuda.synchronize()
+        s.check(out[0])
+        assert torch.equal(out[0], out[1])
+        want = w4.attention_paged_tree(q, *s.dev, t, ln, mask, **{**kw, "workspace": None})
+        assert torch.equal(out[0], want), i

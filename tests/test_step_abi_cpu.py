@@ -107,14 +107,13 @@ def test_tree_refusals():
         assert attend(size=n, **good) == OK, good
 
 
-def test_tree_workspace_is_attentions():
-    from test_attention_abi_cpu import attend as plain
-    for kw in (dict(W=4096, ldt=4096, B=1, T=1, max_q=1), dict(W=900, ldt=900, B=3, T=90, max_q=40), dict()):
-        a, b = ctypes.c_size_t(1), ctypes.c_size_t(2)
-        assert attend(size=a, **kw) == OK and plain(size=b, **kw) == OK and a.value == b.value
-        if a.value:
-            assert attend(ws=P, size=ctypes.c_size_t(a.value - 1), **kw) == WORKSPACE
-            assert attend(ws=P + 8, size=a, **kw) == ALIGN
+def test_tree_workspace():
+    for kw in (dict(W=4096, ldt=4096, B=1, T=1, max_q=1), dict(W=900, ldt=900, B=3, T=90, max_q=40, ldm=1), dict()):
+        n = ctypes.c_size_t(1)
+        assert attend(size=n, **kw) == OK
+        if n.value:
+            assert attend(ws=P, size=ctypes.c_size_t(n.value - 1), **kw) == WORKSPACE
+            assert attend(ws=P + 8, size=n, **kw) == ALIGN
 
 
 def test_adjust_refusals():
