@@ -457,8 +457,8 @@ typedef struct {
  * All in f32.  Tokens and biases of ids outside 0 .. V - 1 are ignored; token_len is kept to 0 .. max_tokens, bias_start to
  * 0 .. biases.  repetition has to be positive (not checked).  A row of which nothing is allowed is all -infinity;
  * logits_argmax_topk takes -infinity as the smallest value.
- * Requires M, V >= 1, V < 2^31, M * ceil(V / 4096) < 2^24, ldl, ldo >= V, requests >= 1 (and M <= requests without
- * request), 0 <= max_tokens < 2^31, ld_tokens >= max_tokens, token_len with tokens, bias_id and bias_start with
+ * Requires M, V >= 1, V < 2^31, M * ceil(V / 8192) < 2^23, ldl, ldo >= V, requests >= 1 (and M <= requests without
+ * request), 0 <= max_tokens < 2^30, ld_tokens >= max_tokens, token_len with tokens, bias_id and bias_start with
  * bias, 0 <= biases < 2^31 - 1, ld_mask >= ceil(V / 32), 1 <= masks < 2^31 (and M <= masks without mask_row); everything 4-byte
  * aligned (16-byte rows of logits and out are faster).  No workspace.  Deterministic.
  */

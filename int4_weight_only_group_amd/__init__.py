@@ -494,17 +494,22 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, scaling: str | None = N
 # tensor once and leaves the wording of a refusal to _dev().
 
 
+_Tensor, _empty = torch.Tensor, torch.empty  # torch.empty takes sizes one by one faster than as a tuple
+
+
 def _need(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
         _dev(t, name, dtype)
 
 
 def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
     """Elements between the tokens of a [tokens][heads][dim] tensor with contiguous heads."""
-    _need(t, name, dtype, dev)
-    if t.dim() != 3:
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _dev(t, name, dtype)
+    shape = t.shape
+    if len(shape) != 3:
         raise ValueError(f"{name} must be [tokens][heads][dim]")
-    n, h, d = t.shape
+    n, h, d = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -512,7 +517,7 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
 
 
 def _row_dtype(t: torch.Tensor, name: str) -> torch.dtype:
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in (torch.float32, torch.float16):
         raise TypeError(f"{name} must be torch.float16 or torch.float32, got {t.dtype}")
@@ -520,7 +525,8 @@ def _row_dtype(t: torch.Tensor, name: str) -> torch.dtype:
 
 
 def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> int:
-    _need(t, name, dtype, dev)
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != dev:
+        _dev(t, name, dtype)
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and hold {n} elements")
     return t.data_ptr()
@@ -528,7 +534,8 @@ def _vec(t: torch.Tensor, name: str, dtype: torch.dtype, n: int, dev: int) -> in
 
 def _freq(t: torch.Tensor, dev: int) -> tuple[int | None, int]:
     """(address, dims that it rotates) of a vector of frequencies"""
-    _need(t, "freq", torch.float32, dev)
+    if not isinstance(t, _Tensor) or t.dtype is not torch.float32 or t.get_device() != dev:
+        _dev(t, "freq", torch.float32)
     if not t.is_contiguous():
         raise ValueError("freq must be contiguous")
     n = t.numel()
@@ -585,7 +592,7 @@ def _rope(fn, x, positions, freq, weight, eps, interleaved, mscale, inverse, out
     ldx = _rows(x, "x", dtype, dev)
     t, h, d = x.shape
     if out is None:
-        out = torch.empty((t, h, d), dtype=torch.float16, device=x.device)
+        out = _empty(t, h, d, dtype=torch.float16, device=x.device)
         ldy = h * d
     else:
         ldy = _rows(out, "out", torch.float16, dev)
@@ -647,7 +654,7 @@ def _append(fn, k, v, k_cache, v_cache, slots, positions, freq, norm, q, q_out, 
         if n != t or dq != d:
             raise ValueError("q must be [T][heads][dim] with k's T and dim")
         if q_out is None:
-            q_out = torch.empty((t, hq, d), dtype=torch.float16, device=q.device)
+            q_out = _empty(t, hq, d, dtype=torch.float16, device=q.device)
             ldqo = hq * d
         else:
             ldqo = _rows(q_out, "q_out", torch.float16, dev)
@@ -749,7 +756,7 @@ def _attend(name, q, k_cache, v_cache, table, kv_len, mask, q_start, max_q, scal
     if d != c.dim:
         raise ValueError("q must have the cache's dim")
     if out is None:
-        out = torch.empty((t, hq, d), dtype=torch.float16, device=q.device)
+        out = _empty(t, hq, d, dtype=torch.float16, device=q.device)
         ldo = hq * d
     else:
         ldo = _rows(out, "out", torch.float16, dev)
@@ -805,18 +812,21 @@ def kv_plan(kv_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor, ow
     _need(free, "free", torch.int32, dev)
     if not free.is_contiguous() or free.dim() != 1:
         raise ValueError("free must be contiguous and 1-D")
-    if out is None:
-        new = functools.partial(torch.empty, dtype=torch.int32, device=table.device)
-        out = (new(b + 1), new(b), new(rows), torch.empty(rows, dtype=torch.int64, device=table.device), new(b))
-    q_start, kv_total, positions, slots, status = out
     i32 = torch.int32
+    if out is None:
+        on = table.device
+        out = (_empty(b + 1, dtype=i32, device=on), _empty(b, dtype=i32, device=on), _empty(rows, dtype=i32, device=on),
+               _empty(rows, dtype=torch.int64, device=on), _empty(b, dtype=i32, device=on))
+        to = [t.data_ptr() for t in out]
+    else:
+        q_start, kv_total, positions, slots, status = out
+        to = (_vec(q_start, "q_start", i32, b + 1, dev), _vec(kv_total, "kv_total", i32, b, dev),
+              _vec(positions, "positions", i32, rows, dev), _vec(slots, "slots", torch.int64, rows, dev),
+              _vec(status, "status", i32, b, dev))
     _check("kv_plan", lib().kv_plan(
         _vec(kv_len, "kv_len", i32, b, dev), _vec(new_len, "new_len", i32, b, dev), b, table.data_ptr(), ldt, width,
         _vec(owned, "owned", i32, b, dev), free.data_ptr(), _vec(free_count, "free_count", i32, 1, dev), free.shape[0],
-        page_size, None if depth is None else _vec(depth, "depth", i32, rows, dev), rows,
-        _vec(q_start, "q_start", i32, b + 1, dev), _vec(kv_total, "kv_total", i32, b, dev),
-        _vec(positions, "positions", i32, rows, dev), _vec(slots, "slots", torch.int64, rows, dev),
-        _vec(status, "status", i32, b, dev), _raw_stream(dev)))
+        page_size, None if depth is None else _vec(depth, "depth", i32, rows, dev), rows, *to, _raw_stream(dev)))
     return out
 
 
@@ -840,7 +850,7 @@ def logits_adjust(logits: torch.Tensor, *, tokens: torch.Tensor | None = None, t
     ldl = _rowmajor(logits, "logits")
     m, v = logits.shape
     if out is None:
-        out, ldo = torch.empty((m, v), dtype=f32, device=logits.device), v
+        out, ldo = _empty(m, v, dtype=f32, device=logits.device), v
     else:
         _need(out, "out", f32, dev)
         ldo = _rowmajor(out, "out")

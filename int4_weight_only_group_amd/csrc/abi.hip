@@ -578,7 +578,7 @@ int logits_adjust(const float* logits, int64_t ldl, int64_t M, int64_t V, const 
       return W4_ERR_SHAPE;
     if (out == logits && ldo != ldl) return W4_ERR_OVERLAP;
     if (h.requests < 1 || h.requests > most || (!h.request && M > h.requests)) return W4_ERR_SHAPE;
-    if (h.tokens && (h.max_tokens < 0 || h.max_tokens > most || h.ld_tokens < h.max_tokens || h.ld_tokens > ((int64_t)1 << 40)))
+    if (h.tokens && (h.max_tokens < 0 || h.max_tokens >= kMaxDim || h.ld_tokens < h.max_tokens || h.ld_tokens > ((int64_t)1 << 40)))
       return W4_ERR_SHAPE;
     if (h.bias && (h.biases < 0 || h.biases >= most)) return W4_ERR_SHAPE;
     if (h.mask && (h.masks < 1 || h.masks > most || h.ld_mask < (V + 31) / 32 || h.ld_mask > ((int64_t)1 << 40) ||
@@ -597,7 +597,7 @@ int logits_adjust(const float* logits, int64_t ldl, int64_t M, int64_t V, const 
     a.repetition = h.repetition, a.frequency = h.frequency, a.presence = h.presence;
     a.bias = h.bias, a.bias_id = h.bias_id, a.bias_start = h.bias_start, a.biases = h.bias ? (int)h.biases : 0;
     a.mask = h.mask, a.ld_mask = h.ld_mask, a.masks = h.mask ? (int)h.masks : 0, a.mask_row = h.mask_row;
-    if (w4::logits_workgroups(a) >= ((int64_t)1 << 24)) return W4_ERR_SHAPE;
+    if (w4::logits_workgroups(a) >= ((int64_t)1 << 23)) return W4_ERR_SHAPE;  // 2^32 threads
     if (int e = check_device()) return e;
     (void)hipGetLastError();
     w4::launch_logits(a, (hipStream_t)stream);

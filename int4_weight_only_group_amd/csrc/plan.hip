@@ -6,9 +6,12 @@
 // stack (of pages given back) and ranks from its top (of pages wanted).  Wants are summed whether they are met or not, so
 // the sequences that get pages are those whose running sum the stack covers: a prefix, whose ranks need no second sum.
 //
-// One workgroup: the sums are a few thousand additions, and pages given back must be on the stack before any are taken.  Rows
-// follow in the same launch while there are few, else in one of their own.  Bound: latency, of the loads that follow from
-// each other (lengths, page, table entry).
+// One workgroup: the sums are a few thousand additions, and pages given back must be on the stack before any are taken.  Up to
+// 1024 sequences, a thread each, the sums stay in LDS, and every page that moves and every row finds its sequence there by
+// bisection, so that all are under way at once; above, sequences come in rounds of 1024.  Rows follow in the same launch while
+// there are few, else in one of their own.
+// Bound: latency, of the launch and the loads that follow from each other (lengths, page, table entry).
+// MEASURED
 #include <algorithm>
 
 #include "w4_internal.h"
@@ -110,34 +113,154 @@ __device__ __forceinline__ int sequence_of(const int32_t* starts, int n, int t) 
   return lo == n ? -1 : lo;
 }
 
+// Inclusive sum over a wave, kept to `most` (below 2^31): adding so is associative, and fits 32 bits.
+__device__ __forceinline__ uint32_t wave_sum(uint32_t x, uint32_t most) {
+#define W4_STEP(CTRL, ROWS) x = min(most, x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false))
+  W4_STEP(0x111, 0xF);  // row_shr 1, 2, 4, 8: sums of the rows of 16
+  W4_STEP(0x112, 0xF);
+  W4_STEP(0x114, 0xF);
+  W4_STEP(0x118, 0xF);
+  W4_STEP(0x142, 0xA);  // row_bcast15 into rows 1 and 3, row_bcast31 into rows 2 and 3
+  W4_STEP(0x143, 0xC);
+#undef W4_STEP
+  return x;
+}
+// The sums of the waves before this one, and of all; mine: a wave's inclusive sum (its last lane's counts).
+template <int WAVES>
+__device__ __forceinline__ uint32_t before_wave(const uint32_t* waves, uint32_t most, uint32_t& all) {
+  const int wave = threadIdx.x >> 6;
+  uint32_t before = 0;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    if (w == wave) before = all;
+    all = min(most, all + waves[w]);
+  }
+  return before;
+}
+
+// Up to THREADS sequences.
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void plan_few_kernel(PlanArgs g, bool rows_too) {
+  constexpr int WAVES = THREADS / 64;
+  constexpr uint32_t kMost = 0x7fffffffu;
+  constexpr int DEEP = 4;  // pages under way for each thread
+  __shared__ uint32_t waves[3][WAVES];
+  __shared__ int starts[THREADS + 1], backs[THREADS], wants[THREADS], firsts[THREADS];
+  __shared__ uint32_t taken;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, b = tid;
+  const int count = min(max(*g.free_count, 0), g.pages);
+  Asked s = b < g.B ? asked(g, b) : Asked{};
+  if (tid == 0) taken = 0;
+  uint32_t all;
+  const uint32_t rows = wave_sum((uint32_t)s.rows, (uint32_t)g.T);
+  if (lane == 63) waves[0][wave] = rows;
+  __syncthreads();
+  // kept to T, an end may be less than a start and its rows, but then all further ones are T
+  const uint32_t row0 = before_wave<WAVES>(waves[0], (uint32_t)g.T, all);
+  const uint32_t up = (uint32_t)__shfl_up((int)rows, 1);  // by all lanes
+  const uint32_t lane_before = lane ? up : 0u;
+  const int start = (int)min((uint32_t)g.T, row0 + lane_before);
+  if (b < g.B) {
+    fit(g, start, s);
+    g.q_start[b] = start, starts[b] = start;
+  }
+  if (tid == 0) g.q_start[g.B] = (int)all, starts[g.B] = (int)all;
+  // pages that go back, and pages that are lacked
+  const uint32_t back = max(0, s.have - s.need), want = max(0, s.need - s.have);
+  const uint32_t back_to = wave_sum(back, kMost), want_to = wave_sum(want, kMost);
+  if (lane == 63) waves[1][wave] = back_to, waves[2][wave] = want_to;
+  __syncthreads();
+  uint32_t given, wanted;
+  const uint32_t back0 = before_wave<WAVES>(waves[1], kMost, given), want0 = before_wave<WAVES>(waves[2], kMost, wanted);
+  const uint32_t back_end = min(kMost, back0 + back_to), want_end = min(kMost, want0 + want_to);
+  backs[tid] = (int)(back_end - min(back, back_end)), wants[tid] = (int)(want_end - min(want, want_end));
+  firsts[tid] = min(s.have, s.need);
+  const int there = (int)min((uint32_t)g.pages, (uint32_t)count + given);
+  const bool granted = want == 0 || want_end <= (uint32_t)there;
+  if (granted && want > 0) atomicMax(&taken, want_end);
+  if (b < g.B) {
+    g.owned[b] = granted ? s.need : s.have;
+    g.status[b] = !s.fits ? -1 : granted ? 0 : (int)want;
+    g.kv_total[b] = s.fits && granted ? s.len + s.n : s.len;
+  }
+  __syncthreads();
+  // the last of B ascending sums that is not above i: the sequence of page i
+  auto of = [&](const int* sums, int i) {
+    int lo = 0, hi = g.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (sums[mid] <= i)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  };
+  if (given > 0) {
+    for (uint32_t i0 = tid; i0 < given; i0 += DEEP * THREADS) {
+      int32_t* entry[DEEP];
+      int32_t page[DEEP];
+#pragma unroll
+      for (int e = 0; e < DEEP; ++e) {
+        const int i = (int)min(i0 + e * THREADS, given - 1), x = of(backs, i);
+        entry[e] = g.table + x * g.ldt + firsts[x] + (i - backs[x]);
+        page[e] = *entry[e];
+      }
+#pragma unroll
+      for (int e = 0; e < DEEP; ++e) {
+        const uint32_t i = i0 + e * THREADS;
+        if (i >= given) break;
+        if (count + (int64_t)i < g.pages) g.free[count + i] = page[e];
+        *entry[e] = -1;
+      }
+    }
+    __syncthreads();  // the stack holds what was given back
+  }
+  const uint32_t all_taken = taken;
+  for (uint32_t i0 = tid; i0 < all_taken; i0 += DEEP * THREADS) {
+    int32_t page[DEEP];
+#pragma unroll
+    for (int e = 0; e < DEEP; ++e) page[e] = g.free[there - 1 - (int)min(i0 + e * THREADS, all_taken - 1)];
+#pragma unroll
+    for (int e = 0; e < DEEP; ++e) {
+      const uint32_t i = i0 + e * THREADS;
+      if (i >= all_taken) break;
+      const int x = of(wants, (int)i);
+      g.table[x * g.ldt + firsts[x] + ((int)i - wants[x])] = page[e];
+    }
+  }
+  if (tid == 0) *g.free_count = there - (int)all_taken;
+  if (!rows_too) return;
+  __syncthreads();
+  for (int t = tid; t < g.T; t += THREADS) {
+    const int x = sequence_of(starts, g.B, t), at = max(x, 0);
+    write_row(g, t, x, starts[at], starts[at + 1]);
+  }
+}
+
+// Any number of sequences.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs g, bool rows_too) {
   __shared__ int64_t sums[3][kPlanThreads / 64];
-  __shared__ int starts[kPlanThreads + 1];
   __shared__ int last_taken;
   const int tid = threadIdx.x;
-  const bool once = g.B <= kPlanThreads;
   const int count = min(max(*g.free_count, 0), g.pages);
-  Asked s{};
   int64_t row0 = 0, given = 0, all = 0;
   if (tid == 0) last_taken = 0;
   // starts, and pages that go back
   for (int b0 = 0; b0 < g.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    s = b < g.B ? asked(g, b) : Asked{};
+    Asked s = b < g.B ? asked(g, b) : Asked{};
     const int64_t end = row0 + block_sum<kPlanThreads>(s.rows, all, sums[0]);
     row0 += all;
     const int start = (int)min((int64_t)g.T, end - s.rows);
     if (b < g.B) {
       fit(g, start, s);
       g.q_start[b] = start;
-      if (once) starts[b] = start;
-      if (b == g.B - 1) {
-        g.q_start[g.B] = (int)min((int64_t)g.T, end);
-        if (once) starts[g.B] = (int)min((int64_t)g.T, end);
-      }
+      if (b == g.B - 1) g.q_start[g.B] = (int)min((int64_t)g.T, end);
     }
     const int back = max(0, s.have - s.need);
-    const int64_t at = count + given + block_sum<kPlanThreads>(back, all, sums[1]) - back;
+    const int64_t at = min((int64_t)0x7fffffff, count + given + block_sum<kPlanThreads>(back, all, sums[1]) - back);
     given += all;
     for_pages(b, back, at | (int64_t)s.need << 32, [&](int of, int64_t x, int i) {
       int32_t* entry = g.table + of * g.ldt + (x >> 32) + i;
@@ -145,23 +268,21 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs g, bool row
       if (to < g.pages) g.free[to] = *entry;
       *entry = -1;
     });
-    if (!once) __syncthreads();
+    __syncthreads();
   }
-  __syncthreads();  // the stack holds what was given back
-  const int there = (int)min((int64_t)g.pages, count + given);
+  const int there = (int)min((int64_t)g.pages, count + given);  // the stack holds what was given back
   // pages that are taken
   int64_t wanted = 0;
   for (int b0 = 0; b0 < g.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
-    if (!once) {
-      s = b < g.B ? asked(g, b) : Asked{};
-      if (b < g.B) fit(g, g.q_start[b], s);
-    }
+    Asked s = b < g.B ? asked(g, b) : Asked{};
+    if (b < g.B) fit(g, g.q_start[b], s);
     const int want = max(0, s.need - s.have);
     const int64_t end = wanted + block_sum<kPlanThreads>(want, all, sums[2]);
     wanted += all;
     const bool granted = want == 0 || end <= there;
-    for_pages(b, granted ? want : 0, (there - 1 - (end - want)) | (int64_t)s.have << 32, [&](int of, int64_t x, int i) {
+    const int64_t from = granted && want > 0 ? (there - 1 - (end - want)) | (int64_t)s.have << 32 : 0;
+    for_pages(b, granted ? want : 0, from, [&](int of, int64_t x, int i) {
       g.table[of * g.ldt + (x >> 32) + i] = g.free[(x & 0xffffffff) - i];
     });
     if (granted && want > 0) atomicMax(&last_taken, (int)end);
@@ -170,15 +291,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs g, bool row
       g.status[b] = !s.fits ? -1 : granted ? 0 : want;
       g.kv_total[b] = s.fits && granted ? s.len + s.n : s.len;
     }
-    if (!once) __syncthreads();
+    __syncthreads();
   }
-  __syncthreads();
   if (tid == 0) *g.free_count = there - last_taken;
   if (!rows_too) return;
   for (int t = tid; t < g.T; t += kPlanThreads) {
-    const int b = once ? sequence_of(starts, g.B, t) : sequence_of(g.q_start, g.B, t);
-    const int at = max(b, 0);
-    write_row(g, t, b, once ? starts[at] : g.q_start[at], once ? starts[at + 1] : g.q_start[at + 1]);
+    const int b = sequence_of(g.q_start, g.B, t), at = max(b, 0);
+    write_row(g, t, b, g.q_start[at], g.q_start[at + 1]);
   }
 }
 
@@ -193,7 +312,12 @@ __global__ __launch_bounds__(kRowThreads) void plan_rows_kernel(PlanArgs g) {
 
 void launch_plan(const PlanArgs& a, hipStream_t st) {
   const bool rows_too = a.T <= kOneLaunchRows;
-  plan_kernel<<<1, kPlanThreads, 0, st>>>(a, rows_too);
+  if (a.B <= 256 && a.T <= 1024)
+    plan_few_kernel<256><<<1, 256, 0, st>>>(a, rows_too);
+  else if (a.B <= kPlanThreads)
+    plan_few_kernel<kPlanThreads><<<1, kPlanThreads, 0, st>>>(a, rows_too);
+  else
+    plan_kernel<<<1, kPlanThreads, 0, st>>>(a, rows_too);
   if (!rows_too) plan_rows_kernel<<<(a.T + kRowThreads - 1) / kRowThreads, kRowThreads, 0, st>>>(a);
 }
 

@@ -91,6 +91,7 @@ CASES = [  # rows, vocabulary, requests, history, biases, masks, penalties
     (64, 2000, None, 257, 300, "some", True), (2, 262144, 1, 20001, 7, "row", True), (4, 777, None, 9, None, "row", False),
     (4, 776, None, 9, 6, None, False), (4, 776, 2, 9, 6, "some", False), (3, 500, None, 9, None, None, False),
     (300, 130, 7, 64, 3, "some", True), (2, 50257, None, 70000, 1000, None, True),
+    (5, 9000, 2, 64, 20000, "row", True), (70, 40000, 3, 300, 30, "row", True), (40, 70000, 5, 3000, None, "some", True),
 ]
 
 

@@ -170,3 +170,17 @@ def test_bindings_refuse(w4):  # noqa: F811
     for bad in (dict(page_size=0), dict(rows=0), dict(page_size=1 << 30)):
         with pytest.raises((w4.W4Error, ValueError)):
             w4.kv_plan(**{**ok, **bad})
+
+
+def test_pages_of_many_sequences_move_at_once(w4):  # noqa: F811
+    # long sequences end and others take their places, some pages, many or none each
+    rng = np.random.default_rng(6)
+    for seqs in (3, 200, 256, 257, 1024, 1100):
+        width = 300
+        kv = rng.integers(0, width * 4 - 20, seqs)
+        s = State(rng, seqs, width, 4, -(-kv // 4), spare=seqs * 40)
+        for _ in range(3):
+            kv = np.where(rng.random(seqs) < 0.4, rng.integers(0, width * 4 - 20, seqs), kv)
+            n = rng.integers(0, 3, seqs)
+            (_, total, _, _, _), _ = s.step(w4, kv, n, max(1, int(n.sum())))
+            kv = total.cpu().numpy().copy()
