@@ -322,9 +322,10 @@ void launch(RopeArgs& g, bool f32, bool interleaved, bool norm, hipStream_t st) 
   g.per_n = 1.f / g.n, g.per_head = 1.f / g.per, g.per_chunks = 1.f / (g.D / 8);
   // Where tokens are plenty (8 workgroups a CU stay), narrow ones share a workgroup as long as its threads go about
   // once over their items: 8191 x 16 x 80 of f16 (160 items a token) take 10.5 us two at a time, 12.5 one at a time;
-  // 8192 x 20 x 128 of f32 into the cache (176 items) 24.7 and 23.3.
+  // 8192 x 20 x 128 of f32 into the cache (176 items) 24.7 and 23.3.  With a norm, up to twice: 8191 x 16 x 128 of f32 (128
+  // lanes a token) 19.4 two at a time, 21.2 one at a time; 8191 x 16 x 80 of f16 (256 lanes) 17.7 and 19.1.
   g.tokens = 1;
-  while (g.tokens < kMaxTokens && (!norm || groups) && g.n * g.tokens * 2 <= kThreads * 5 / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
+  while (g.tokens < kMaxTokens && (!norm || groups) && g.n * g.tokens * 2 <= kThreads * (norm ? 8 : 5) / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
   const int grid = (g.T + g.tokens - 1) / g.tokens;
 #define W4_ROPE(F, M)                                               \
   if (norm)                                                         \
