@@ -12,8 +12,8 @@
 //
 // The norm.  x becomes x w / sqrt(mean(x^2) + eps) over the D dims of its head, before it turns.  A head's items lie on
 // adjacent lanes, as many as the next power of two has, so that the squares of what the lanes hold anyway
-// are summed by lane moves and x is read once.  Rotations that leave single dims to a thread (R / 2 no multiple of 8) have more
-// items than a wave has lanes: there the sums are taken first, a chunk of 8 dims a lane, and x is read again, from the cache.
+// are summed by lane moves and x is read once.  Where R / 2 is no multiple of 8, pairs do not share chunks of 8 dims: a lane holds a
+// chunk all the same, and takes the other halves of its pairs from LDS, where the lanes of its head leave their normed values.
 //
 // Bound: HBM for prompts (each element read once, written once), the launch and the chain of
 // loads for a decode step.  So a thread's first elements, its token's slot and its head's scale
@@ -31,7 +31,6 @@ typedef float f32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens of a workgroup, at most
-constexpr int kMaxHeads = 1024;  // of q, of k
 
 struct RopeArgs {
   const void* src[3];  // q, k, v rows (heads of one token are contiguous)
@@ -132,7 +131,6 @@ struct Item {
   bool rot;      // of a head that turns
   f32x8 a, b;
   f32x8 wa, wb;  // norms: their weights
-  int head;      // norms: which of the token's
 };
 
 // Sum over aligned groups of n lanes, a power of two up to 32, all of them active; every lane gets it.
@@ -174,7 +172,6 @@ __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x)
   const int64_t at = (int64_t)t * (w == 0 ? ldq : w == 1 ? ldk : ldv) + (int64_t)h * g.D;
   if constexpr (NORM) {
     x.d.p = nullptr;
-    x.head = j;
     x.a = 0.f, x.b = 0.f;
     // a lane past the head's items, or past the token's: it only takes part in the sum
     if (x.rot ? x.item >= g.items : w == 2 && h >= g.heads[2]) return;
@@ -185,13 +182,9 @@ __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x)
     weight = !x.rot ? nullptr : w == 0 ? wq : wk;
     x.wa = 1.f, x.wb = 1.f;
   }
-  if (MODE == kHalfOdd && x.rot) {
+  if (MODE == kHalfOdd && !NORM && x.rot) {
     if (x.item < half) x.a[0] = load1<F32>(src, at + x.item);
     x.b[0] = load1<F32>(src, at + x.item + half);
-    if (NORM && weight) {
-      if (x.item < half) x.wa[0] = weight[x.item];
-      x.wb[0] = weight[x.item + half];
-    }
   } else {
     const bool pair = MODE == kHalf && x.rot && x.item < g.R / 16;
     if (MODE == kHalf && x.rot && !pair) x.item += g.R / 16;
@@ -218,13 +211,9 @@ __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x)
 }
 
 template <bool F32, int MODE, bool NORM>
-__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, const float* norms, Item& x) {
+__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, float* staged, Item& x) {
   if constexpr (NORM) {
-    float f;
-    if (MODE == kHalfOdd)
-      f = x.rot ? norms[x.head] : 1.f;
-    else
-      f = norm_of(g, lanes_sum(squares(x.a) + squares(x.b), g.per));
+    const float f = norm_of(g, lanes_sum(squares(x.a) + squares(x.b), g.per));
     if (x.rot) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x.a[e] = x.a[e] * f * x.wa[e], x.b[e] = x.b[e] * f * x.wb[e];
@@ -233,6 +222,30 @@ __device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, co
   if (x.d.p == nullptr) return;
   const int half = g.R / 2;
   const float2* cs = turn + x.tl * half;
+  if constexpr (MODE == kHalfOdd && NORM) {
+    // all lanes of a head are in this wave, and here or not here together (a lane past the head's items holds none of its dims)
+    float* head = staged + (threadIdx.x & ~(g.per - 1)) * 8;
+    if (x.rot) {
+      *reinterpret_cast<f32x8*>(staged + threadIdx.x * 8) = x.a;
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = x.item * 8 + e;
+        if (d >= g.R) break;
+        const bool first = d < half;
+        const float2 w = cs[first ? d : d - half];
+        const float other = head[first ? d + half : d - half];
+        x.a[e] = x.a[e] * w.x + (first ? -other : other) * w.y;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+      __builtin_amdgcn_wave_barrier();  // read before the next heads are left there
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    }
+    store8(x.d, x.item * 8, x.a);
+    return;
+  }
   if (MODE == kHalfOdd && x.rot) {
     if (x.item < half) {
       const float2 w = cs[x.item];
@@ -267,34 +280,14 @@ __device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, co
   store8(x.d, c0, x.a);
 }
 
-// kHalfOdd's norms, of one token's rotated heads: a group of lanes takes a head.
-template <bool F32>
-__device__ __forceinline__ void odd_norms(const RopeArgs& g, int t, float* norms) {
-  int lanes = 1;
-  while (lanes < g.D / 8) lanes *= 2;
-  const int heads = g.heads[0] + g.heads[1], chunk = threadIdx.x % lanes;
-  for (int j0 = 0; j0 < heads; j0 += kThreads / lanes) {
-    const int j = j0 + threadIdx.x / lanes;
-    const bool of_q = j < g.heads[0];
-    const void *q = g.src[0], *k = g.src[1];
-    const int64_t ldq = g.ld[0], ldk = g.ld[1];
-    const int64_t at = t * (of_q ? ldq : ldk) + (int64_t)(of_q ? j : j - g.heads[0]) * g.D + chunk * 8;
-    float s = 0.f;
-    if (j < heads && chunk < g.D / 8) s = squares(load8<F32>(of_q ? q : k, at));
-    s = lanes_sum(s, lanes);
-    if (j < heads && chunk == 0) norms[j] = norm_of(g, s);
-  }
-}
-
 template <bool F32, int MODE, bool NORM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
   __shared__ float2 turn[kMaxTokens * 128];  // [token][pair]: mscale (cos, sin)
-  __shared__ float norms[NORM && MODE == kHalfOdd ? 2 * kMaxHeads : 1];
+  __shared__ float staged[NORM && MODE == kHalfOdd ? 8 * kThreads : 1];  // [thread][dim of its chunk]
   const int t0 = blockIdx.x * g.tokens, nt = min(g.tokens, g.T - t0), half = g.R / 2, n = nt * g.n;
   Item x{};
   int i = threadIdx.x;
   if (i < n) fetch<F32, MODE, NORM>(g, i, t0, x);
-  if constexpr (NORM && MODE == kHalfOdd) odd_norms<F32>(g, t0, norms);
   for (int k = threadIdx.x; k < nt * half; k += kThreads) {
     const int tl = k / half, p = k - tl * half;
     double a = (double)g.pos[t0 + tl] * (double)g.freq[p] * 0.15915494309189535;  // turns
@@ -305,7 +298,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
   }
   __syncthreads();
   while (i < n) {
-    finish<F32, MODE, NORM>(g, turn, norms, x);
+    finish<F32, MODE, NORM>(g, turn, staged, x);
     i += kThreads;
     if (i < n) fetch<F32, MODE, NORM>(g, i, t0, x);
   }
@@ -313,19 +306,18 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
 
 void launch(RopeArgs& g, bool f32, bool interleaved, bool norm, hipStream_t st) {
   const int mode = interleaved ? kInterleaved : (g.R / 2) % 8 == 0 ? kHalf : kHalfOdd;
-  g.per = g.items = items_of(mode, g.D, g.R);
-  const bool groups = norm && mode != kHalfOdd;
-  if (groups)
+  g.per = g.items = norm && mode == kHalfOdd ? g.D / 8 : items_of(mode, g.D, g.R);
+  if (norm)
     for (g.per = 1; g.per < g.items;) g.per *= 2;
   g.n = (g.heads[0] + g.heads[1]) * g.per + g.heads[2] * (g.D / 8);
-  if (groups) g.n = (g.n + g.per - 1) / g.per * g.per;  // the groups of the next token's lanes are aligned too
+  if (norm) g.n = (g.n + g.per - 1) / g.per * g.per;  // the groups of the next token's lanes are aligned too
   g.per_n = 1.f / g.n, g.per_head = 1.f / g.per, g.per_chunks = 1.f / (g.D / 8);
   // Where tokens are plenty (8 workgroups a CU stay), narrow ones share a workgroup as long as its threads go about
   // once over their items: 8191 x 16 x 80 of f16 (160 items a token) take 10.5 us two at a time, 12.5 one at a time;
   // 8192 x 20 x 128 of f32 into the cache (176 items) 24.7 and 23.3.  With a norm, up to twice: 8191 x 16 x 128 of f32 (128
   // lanes a token) 19.4 two at a time, 21.2 one at a time; 8191 x 16 x 80 of f16 (256 lanes) 17.7 and 19.1.
   g.tokens = 1;
-  while (g.tokens < kMaxTokens && (!norm || groups) && g.n * g.tokens * 2 <= kThreads * (norm ? 8 : 5) / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
+  while (g.tokens < kMaxTokens && g.n * g.tokens * 2 <= kThreads * (norm ? 8 : 5) / 4 && g.T / g.tokens > 8 * 256) g.tokens *= 2;
   const int grid = (g.T + g.tokens - 1) / g.tokens;
 #define W4_ROPE(F, M)                                               \
   if (norm)                                                         \
