@@ -19,7 +19,9 @@
 // loads for a decode step.  So a thread's first elements, its token's slot and its head's scale
 // are all on their way before the angles are formed.
 // Measured: 8192 tokens of 16 + 2 + 2 heads of 128 dims, f32, into an f16 cache 23.7 us, 5.3 TB/s;
-// 8191 of 16 heads of 80, f16, 10.1 us, 4.2 TB/s; one token 2.4 us.
+// 8191 of 16 heads of 80, f16, 10.1 us, 4.2 TB/s; one token 2.4 us.  With norms: 8191 tokens of 16 + 8 + 8 heads of 128 dims, f32, into an f16
+// cache 40.0 us, 5.0 TB/s; 8191 of 16 heads of 128, f32, 18.7 (partly from the last-level cache); of 80, f16, interleaved, 17.5 (10 of a head's 16
+// lanes hold dims); one token 4.5 in a replayed graph.  (Weights in LDS in place of registers: 43.1, 19.3, 18.8.)
 #include "w4_internal.h"
 #include "w4_kv.h"
 
