@@ -389,7 +389,7 @@ int kv_append_norm_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldq
  *   past the last sequence are padding: 0 and -1.  (What kv_append_rope and attention_paged take.)
  *   status int32 [B]: 0, or how many pages were lacking; -1 for a sequence that does not fit: a length below 0,
  *   kv_len + new_len past W * page_size, or rows past T.  Such a one keeps what it has; its rows have position 0.
- * Requires 1 <= B <= 2^20, 1 <= T < 2^24, W, page_size, pages >= 1, W * page_size <= 2^30, pages * page_size < 2^31, ldt >= W; int32
+ * Requires 1 <= B <= 2^20, 1 <= T < 2^24, W, page_size, pages >= 1, W * page_size <= 2^30, B * W < 2^31, pages * page_size < 2^31, ldt >= W; int32
  * arrays 4-byte aligned, slot 8-byte; depth may be NULL.  kv_total may be kv_len; no other overlap.  Entries of the
  * stack past its height are left as they are.  Everything is read on the device and kept in bounds there (owned to 0 .. W, the height to
  * 0 .. pages); a table entry that is no page of the cache gives slots of -1.  One launch up to 4096 rows, two
@@ -410,7 +410,7 @@ int kv_plan(const int32_t* kv_len, const int32_t* new_len, int64_t B, int32_t* t
  * A row that sees no key is 0.  Everything else is as for attention_paged: arguments, lengths in bounds, unseen keys that reach
  * nothing, workspace (query it), roundings, determinism.
  * Requires what attention_paged requires, window 0 or at least max_q, ldm >= ceil(max_q / 64), mask 8-byte
- * aligned.
+ * aligned, and no more work than a launch holds: always so while B * heads < 2^20 and T * Hq <= 2^27.
  */
 int attention_paged_tree(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, const int32_t* table, int64_t ldt,
                          int64_t W, const int32_t* kv_len, const int32_t* q_start, const uint64_t* mask, int64_t ldm,

@@ -547,7 +547,7 @@ int kv_plan(const int32_t* kv_len, const int32_t* new_len, int64_t B, int32_t* t
     if (B < 1 || B > ((int64_t)1 << 20) || T < 1 || T >= kMaxTokens) return W4_ERR_SHAPE;
     if (page_size < 1 || page_size > kMaxDim || W < 1 || W > kMaxDim / page_size || ldt < W || ldt > kMaxDim)
       return W4_ERR_SHAPE;
-    if (pages < 1 || pages > (((int64_t)1 << 31) - 1) / page_size) return W4_ERR_SHAPE;
+    if (pages < 1 || pages > (((int64_t)1 << 31) - 1) / page_size || B * W >= (int64_t)1 << 31) return W4_ERR_SHAPE;
     for (const void* p : {(const void*)kv_len, (const void*)new_len, (const void*)table, (const void*)owned,
                           (const void*)free_pages, (const void*)free_count, (const void*)depth, (const void*)q_start,
                           (const void*)kv_total, (const void*)pos, (const void*)status})

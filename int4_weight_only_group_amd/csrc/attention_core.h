@@ -185,6 +185,8 @@ __device__ __forceinline__ Keys keys_of(const Plan& p, const Seq& s, int t0, int
   if constexpr (TREE) t0 = 0, t1 = s.n - 1;  // any row may see any new token
   k.hi = max(0, s.len - s.n + t1 + 1);
   k.lo = p.a.window ? max(0, s.len - s.n + t0 + 1 - p.a.window) : 0;
+  // as many keys as the launch allows for, if a sequence has more rows than max_q
+  if (TREE && p.a.window) k.lo = max(k.lo, k.hi - p.a.window - p.a.max_q);
   k.lo = min(k.lo / align * align, k.hi);
   const int all = p.a.window ? k.hi - k.lo : s.len;
   k.per = max(least, (max(all, k.hi - k.lo) + p.splits - 1) / p.splits);
@@ -819,7 +821,7 @@ struct DealtTile {
 };
 template <int NW, int KT, int UNIT>
 __device__ __forceinline__ DealtTile deal_tiles(const Plan& p, int part, unsigned char* lds) {
-  __shared__ int64_t sums[2][NW];
+  __shared__ int64_t sums[3][NW];
   __shared__ DealtTile found;
   const int B = p.a.B, each = (B + 64 * NW - 1) / (64 * NW), lane = threadIdx.x & 63;
   auto keys = [&](const Seq& s) {
@@ -884,27 +886,30 @@ __device__ __forceinline__ DealtTile deal_tiles(const Plan& p, int part, unsigne
     else  // many sequences: parts are short beside a round
       per = share(all, .5f);
   }
-  mine = 0;  // tiles, and their parts
+  mine = 0;
+  int64_t tiles = 0, slot;
   for (int b = b0; b < b1; ++b) {
     const Seq s = each == 1 ? one : sequence(p.a, b);
-    const int n = tiles_of(p, s.n);
-    mine += (int64_t)n << 32 | (uint32_t)(n * parts_of(keys(s), per));
+    const int64_t n = tiles_of(p, s.n);
+    tiles += n, mine += n * parts_of(keys(s), per);
   }
-  const int64_t total = block_scan<NW>(mine, before, sums[1]);
-  int at = (int)before, slot = (int)(before >> 32);
-  if (part >= at && part < at + (int)mine) {
+  (void)block_scan<NW>(mine, before, sums[1]);
+  const int64_t total = block_scan<NW>(tiles, slot, sums[2]);
+  if (part >= before && part < before + mine) {
     for (int b = b0; b < b1; ++b) {
       const Seq s = each == 1 ? one : sequence(p.a, b);
-      const int n = tiles_of(p, s.n), count = n > 0 ? parts_of(keys(s), per) : 1;
-      if (part < at + n * count) {
-        const int tile = (part - at) / count;
-        found = {b, tile, slot + tile, part - at - tile * count, count, at + tile * count, s};
+      const int64_t n = tiles_of(p, s.n);
+      const int count = n > 0 ? parts_of(keys(s), per) : 1;
+      if (part < before + n * count) {
+        const int in = (int)(part - before), tile = in / count;
+        // (starts that fall make more tiles than the launch allows for)
+        if (slot + tile < p.tiles) found = {b, tile, (int)slot + tile, in - tile * count, count, part - (in - tile * count), s};
         break;
       }
-      at += n * count, slot += n;
+      before += n * count, slot += n;
     }
   }
-  spare((int)(total >> 32));
+  spare((int)min(total, (int64_t)p.tiles));
   __syncthreads();
   return found;
 }
@@ -1722,7 +1727,8 @@ void plan_tree(const AttnArgs& a, int64_t most, F row_tiles, Launch& x) {
   const int64_t keys = a.window ? std::min(most, (int64_t)a.window + a.max_q + 64) : most;
   x.tiles = (int)tiles;
   x.many_splits = (int)slots;
-  x.tree_parts = (int)std::min(2 * slots + tiles, tiles * ((keys + kMinPart - 1) / kMinPart));
+  // at most; whole tiles where they are many rounds
+  x.tree_parts = (int)(tiles > 8 * slots ? tiles : std::min(2 * slots + tiles, tiles * ((keys + kMinPart - 1) / kMinPart)));
 }
 
 // Lengths are on the device, so that the table's width stands for every sequence's.  Where it is much wider than they
@@ -1807,7 +1813,7 @@ bool launchable(const Launch& x, const AttnArgs& a) {
     if ((x.few_parts ? x.few_parts : a.B) * heads >= kMost) return false;
     if (x.few_parts && a.B * heads * x.few_rows >= kMost) return false;
   }
-  if (x.many && a.mask) return (int64_t)x.tree_parts * heads < kMost;
+  if (x.many && a.mask) return (int64_t)x.tree_parts * heads < kMost / 2;  // of 512 threads
   return !x.many || x.tiles * heads * x.many_splits < kMost;  // parts are for few tiles: their join is small
 }
 

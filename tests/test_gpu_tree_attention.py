@@ -296,3 +296,39 @@ def test_captured_and_replayed(w4):  # noqa: F811
         assert torch.equal(out[0], out[1])
         want = w4.attention_paged_tree(q, *s.dev, t, ln, mask, **{**kw, "workspace": None})
         assert torch.equal(out[0], want), i
+
+
+@pytest.mark.parametrize("n,window", [(12, 0), (12, 40), (90, 0), (90, 95)])
+def test_more_rows_than_max_q(w4, n, window):  # noqa: F811
+    # of the first sequence: its rows past max_q are unspecified, the others' are right, and nothing leaves the workspace
+    s = Tree([(n, 3000), (5, 700), (3, 90)], 4, 2, 64, 16, seed=25, kind="any")
+    most = n * 3 // 4
+    need = w4.attention_workspace_bytes(s.dev[0], 3, s.q.shape[0], most, 4, s.table.shape[1], window, tree=True)
+    ws = torch.full((need + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    got = s.run(w4, window=window, max_q=most, workspace=ws[:max(need, 16)]).cpu().numpy().astype(np.float64)
+    assert (ws[max(need, 16):] == 0xA5).all()
+    want, size, wobble = s.want(None, window)
+    keep = np.r_[n:s.q.shape[0]]
+    assert (np.abs(got - want) <= s.bound(want, size, wobble))[keep].all()
+
+
+@pytest.mark.parametrize("new", [3, 30, 200])
+def test_starts_that_fall(w4, new):  # noqa: F811
+    # starts in any order are kept in bounds: sequences then share rows, whose results are one or another's
+    s = Tree([(new, 1000), (new, 1000), (new, 1000), (new, 1000)], 4, 2, 64, 16, seed=26, kind="none")
+    t = s.q.shape[0]
+    for starts in ([0, t, 0, t, 0], [t, 0, t, 0, t], [-9, 2 ** 31 - 1, -2 ** 31, t, 5], [new, new, 0, t, t]):
+        need = w4.attention_workspace_bytes(s.dev[0], 4, t, new, 4, s.table.shape[1], tree=True)
+        ws = torch.full((need + 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+        s.run(w4, q_start=dev(np.array(starts, dtype=np.int32)), max_q=new, workspace=ws[:max(need, 16)])
+        torch.cuda.synchronize()
+        assert (ws[max(need, 16):] == 0xA5).all()
+
+
+def test_many_tiles_in_many_rounds(w4):  # noqa: F811
+    # more tiles than parts are made for
+    rng = np.random.default_rng(27)
+    kv = rng.integers(20, 60, 600)
+    kv[7] = 900
+    s = Tree([(20, int(x)) for x in kv], 64, 8, 64, 16, seed=27, kind="any")
+    s.check(s.run(w4))

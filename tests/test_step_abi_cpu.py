@@ -83,7 +83,7 @@ def test_plan_refusals():
         assert plan(**{n: None}) == NULL, n
     for bad in (dict(B=0), dict(B=(1 << 20) + 1), dict(T=0), dict(T=1 << 24), dict(W=0), dict(ldt=7), dict(page=0),
                 dict(page=-1), dict(pages=0), dict(pages=1 << 27), dict(W=1 << 26, ldt=1 << 26, page=17), dict(pages=1 << 62),
-                dict(page=1 << 62), dict(W=1 << 62, ldt=1 << 62)):
+                dict(page=1 << 62), dict(W=1 << 62, ldt=1 << 62), dict(B=1 << 20, W=1 << 11, ldt=1 << 11)):
         assert plan(**bad) == SHAPE, bad
     for bad in (dict(kv_len=P + 1), dict(new_len=P + 2), dict(table=P + 3), dict(owned=P + 1), dict(free=P + 2),
                 dict(count=P + 2), dict(depth=P + 1), dict(q_start=P + 2), dict(kv_total=P + 2), dict(pos=P + 2),
@@ -114,6 +114,23 @@ def test_tree_workspace():
         if n.value:
             assert attend(ws=P, size=ctypes.c_size_t(n.value - 1), **kw) == WORKSPACE
             assert attend(ws=P + 8, size=n, **kw) == ALIGN
+
+
+def test_trees_that_no_launch_holds():
+    def size(heads, G, dim=8, **kw):
+        n = ctypes.c_size_t(1)
+        c = cache(heads=heads, dim=dim, stride_page=heads * 16 * dim, stride_head=16 * dim, stride_token=dim)
+        ld = heads * G * dim
+        return attend(c=c, size=n, ldq=ld, ldo=ld, Hq=heads * G, **{**dict(ldt=1 << 16, W=1 << 16, ldm=1 << 14), **kw}), n.value
+
+    n = 1 << 20
+    for heads, G, dim, kw in ((1024, 1, 8, dict(B=n, T=n, max_q=1, q_start=None)), (64, 4, 256, dict(B=n, T=1 << 22, max_q=16)),
+                              (1024, 1, 8, dict(B=n, T=n, max_q=n))):
+        assert size(heads, G, dim, **kw)[0] == SHAPE, (heads, G, kw)
+    for heads, G, dim, kw in ((1, 16, 8, dict(B=n - 1, T=n - 1, max_q=1, q_start=None)), (1, 128, 8, dict(B=n - 1, T=n, max_q=n)),
+                              (1, 8, 256, dict(B=n - 1, T=1 << 23, max_q=8)), (8, 16, 128, dict(B=1 << 16, T=1 << 20, max_q=16)),
+                              (1023, 1, 256, dict(B=1025, T=1 << 17, max_q=128))):
+        assert size(heads, G, dim, **kw)[0] == OK, (heads, G, kw)
 
 
 def test_adjust_refusals():
