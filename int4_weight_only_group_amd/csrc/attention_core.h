@@ -763,7 +763,8 @@ __global__ __launch_bounds__((64 * few_waves<DP, FP8>()), (few_per_cu<DP, FP8>()
 //
 // Measured, 16 heads on 2 of 128 dims: a chunk of 4096 tokens behind 12288, 501 us, 0.96 PFLOP/s (a library f16 product
 // of 8192^3: 1.1), 527 from an e4m3 cache; a prompt of 1570, 30.6 us, of which the longest workgroup's 25 turns of 64 keys
-// take 25, 38.3 from e4m3.  16 heads on 8 of 256 dims, 2048 tokens behind 6144: 293 us, 0.82 PFLOP/s, one wave a SIMD.
+// take 25, 38.3 from e4m3.  16 heads on 8 of 256 dims, 2048 tokens behind 6144: 293 us, 0.82 PFLOP/s, one wave a SIMD
+// (the same with four buffers, whose loads have three turns to arrive).
 constexpr int kManyWaves = 4;
 template <int DP, int KS>
 constexpr int many_keys() { return DP == 256 || KS == 2 ? 32 : 64; }  // of a key tile

@@ -12,8 +12,8 @@
 //
 // Bound: HBM, each logit read and written once; for long histories the counting, a token in each slice.  So tokens are loaded
 // eight deep, and the code is kept to few registers: waits of many waves cover each other.  (Rows of one request in a
-// workgroup that counts once take as many registers again, and longer: 100 rows of 4 requests, 262144 logits, 20001 tokens
-// 102 us against 58; 64 of requests of their own, 151936 logits, up to 8191 tokens 41 against 20.)
+// workgroup that counts once and takes them in turn: 100 rows of 4 requests, 262144 logits, up to 20001 tokens, 64, 68 and 60 us with
+// 2, 4 and 6 rows against 59; 32 rows of 4 requests, 151936 logits, 15, 21 and 29 against 12.5: fewer workgroups, loads in turn.)
 // Measured: those 64, with biases and masks for half of them, 20.4 us, 3.9 TB/s; with 10 tokens, at 262144 logits, 26.3, 5.1 TB/s;
 // the 100 58, 3.7 TB/s; one of 151936 logits and 1570 tokens 4.4.
 #include "w4_internal.h"

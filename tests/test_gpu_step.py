@@ -50,7 +50,7 @@ class Engine:
         host = c.view(torch.uint8).cpu().numpy() if self.e4m3 else c.cpu().numpy()
         return attnref.e4m3_values()[host] if self.e4m3 else host.astype(np.float64)
 
-    def step(self, parents, tokens):
+    def step(self, parents):
         """One pass over the sequences' new tokens (parents[b]: their trees); returns what was chosen for each row."""
         w4, t = self.w4, sum(map(len, parents))
         rows = t + 2  # two rows of padding
@@ -144,17 +144,17 @@ class Engine:
 def test_steps(w4, e4m3):  # noqa: F811
     e = Engine(w4, 31, e4m3)
     prompts = [20, 5, 11]
-    plan, qkv, _ = e.step([list(range(-1, n - 1)) for n in prompts], None)
+    plan, qkv, _ = e.step([list(range(-1, n - 1)) for n in prompts])
     e.accept(plan, qkv, [list(range(n)) for n in prompts])
     # trees; a path through each is kept: 0 - 2 - 4, nothing, 1
-    plan, qkv, _ = e.step([[-1, -1, 0, 0, 2, 2, 4], [-1, 0, 1], [-1, -1, 1, 2, 0]], None)
+    plan, qkv, _ = e.step([[-1, -1, 0, 0, 2, 2, 4], [-1, 0, 1], [-1, -1, 1, 2, 0]])
     e.accept(plan, qkv, [[0, 2, 4], [], [1]])
     assert e.kv.tolist() == [23, 5, 12]
     # one ends and another takes its place; single tokens beside it
     e.kv[0], e.length[0] = 0, 0
-    plan, qkv, _ = e.step([list(range(-1, 17)), [-1], [-1, 0, 0, 1, 1, 2, 2, 3, 3]], None)
+    plan, qkv, _ = e.step([list(range(-1, 17)), [-1], [-1, 0, 0, 1, 1, 2, 2, 3, 3]])
     e.accept(plan, qkv, [list(range(18)), [0], [0, 2, 5]])
-    e.step([[-1], [-1], [-1]], None)
+    e.step([[-1], [-1], [-1]])
 
 
 def test_a_captured_step(w4):  # noqa: F811

@@ -13,8 +13,8 @@ pytestmark = pytest.mark.gpu
 from test_gpu_attention import Setup, dev, w4  # noqa: E402, F401
 
 
-def words_of(sees, words, junk=None):
-    """int64 [T][words] of sets of new tokens; junk: a generator that fills the bits past each row's n"""
+def words_of(sees, words):
+    """int64 [T][words] of sets of new tokens"""
     out = np.zeros((len(sees), words), dtype=np.uint64)
     for t, s in enumerate(sees):
         for j in s:
