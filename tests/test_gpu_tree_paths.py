@@ -53,3 +53,85 @@ def test_weights_of_few_rows_keep_22_bits(w4, d, e4m3, n, old):  # noqa: F811
     assert np.abs(want).max() <= 0.032 and size.max() <= 1
     err = np.abs(got - want)
     assert (err <= np.abs(want) * 2.0 ** -11 + 2.0 ** -19 + 2 * 2.0 ** -21).all(), err.max()
+
+
+class Shared(Tree):
+    """One head's keys, values and queries for `heads` kv heads (which share the cache's memory), so that few workgroups are left for
+    the keys of each and the oracle has one head to do."""
+
+    def __init__(self, lens, d, e4m3, heads, page=16, seed=0, group=1, **kw):
+        super().__init__(lens, group, 1, d, page, e4m3, seed=seed, **kw)
+        self.heads = heads
+
+    def run(self, w4, **kw):
+        kw = self.kw(**kw)
+        for n in ("k_scale", "v_scale"):
+            if n in kw:
+                kw[n] = kw[n].repeat(self.heads)
+        caches = [c.expand(-1, self.heads, -1, -1) for c in self.dev]
+        self.need = w4.attention_workspace_bytes(caches[0], len(self.lens), self.q.shape[0], kw["max_q"], self.heads * self.hq,
+                                                 self.table.shape[1], kw.get("window", 0), tree=True)
+        q = dev(self.q).repeat(1, self.heads, 1)
+        out = w4.attention_paged_tree(q, *caches, dev(self.table), dev(self.kv_len), self.mask[:, :self.words], **kw)
+        out = out.view(-1, self.heads, self.hq, self.d)
+        assert torch.equal(out, out[:, :1].expand_as(out))
+        return out[:, 0]
+
+    def turns(self, rows, waves):
+        """32-key tiles that each wave takes at least: the workspace has a row of dims + 4 floats for each row of every part of
+        a tile, and 16 bytes a tile."""
+        tiles = sum(-(-n * self.hq // rows) for n, _ in self.lens)
+        parts = (self.need - 16 * tiles) // (self.heads * rows * (self.d + 4) * 4) if self.need else tiles
+        assert parts >= tiles
+        # a tile has the parts that the others leave, at most
+        return [int(kv) // (parts - tiles + 1) // (32 * waves) for _, kv in self.lens]
+
+
+FORMS = [  # dims, e4m3, rows of a tile, waves, the most rows that this kernel takes
+    (64, False, 64, 4, 96), (64, True, 64, 4, 96), (128, False, 64, 8, 64), (128, True, 64, 4, 96), (256, False, 32, 4, 64),
+    (256, True, 32, 8, 96)]
+
+
+@pytest.mark.parametrize("d,e4m3,rows,waves,most", FORMS)
+@pytest.mark.parametrize("window", [False, True])
+@pytest.mark.parametrize("page", [16, 7])
+def test_many_turns_of_a_wave(w4, d, e4m3, rows, waves, most, window, page):  # noqa: F811
+    # 17 rows and more: tiles that are fetched while others are multiplied, page numbers and buffers that come round again, maxima
+    # that move from turn to turn; half full and full tiles, two tiles; with a window the first turn of some waves is not whole
+    kv = 32 * waves * 24 + 75
+    for i, (new, sharp) in enumerate([([24], 1.0), ([60], 8.0), ([most - 5], 1.0), ([20, 60], 8.0)]):
+        s = Shared([(n, kv - 301 * j) for j, n in enumerate(new)], d, e4m3, 1024, page, seed=30 + i + d, kind="any", sharp=sharp)
+        win = kv - 32 * waves * 3 + 11 if window else 0
+        a = s.run(w4, window=win)
+        assert min(s.turns(rows, waves)) >= 5, s.turns(rows, waves)
+        s.check(a, window=win)
+
+
+@pytest.mark.parametrize("d,e4m3,rows,waves,most", FORMS)
+def test_many_turns_with_gaps(w4, d, e4m3, rows, waves, most):  # noqa: F811
+    # the longest sequence beside others of one turn or none, and rows of two query heads
+    kv = 32 * waves * 36 + 75
+    s = Shared([(9, 9), (most // 2, kv), (2, 40), (0, 0), (30, 31)], d, e4m3, 512, 16, seed=40 + d, group=2, kind="any")
+    s.check(s.run(w4))
+    assert s.turns(rows, waves)[1] >= 5
+    s.check(s.run(w4, window=200), window=200)
+
+
+@pytest.mark.parametrize("d,e4m3", [(64, False), (64, True), (128, True), (256, True)])
+@pytest.mark.parametrize("n", [65, 95, 96])
+@pytest.mark.parametrize("old", [0, 20, 31, 407])
+def test_the_second_word_of_a_mask(w4, d, e4m3, n, old):  # noqa: F811
+    # 65 to 96 new tokens of a head each: tiles of keys whose bits lie in both words
+    s = Tree([(n, n + old), (n - 31, n + old)], 2, 2, d, 16, e4m3, seed=n + old, kind="any")
+    s.check(s.run(w4))
+    s.check(s.run(w4, window=n + 3), window=n + 3)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new", [12, 130])
+@pytest.mark.parametrize("window,page", [(0, 16), (2900, 16), (0, 7)])
+def test_many_turns_in_the_kernels_for_few_and_for_many(w4, d, e4m3, new, window, page):  # noqa: F811
+    # two parts of 2500 keys or more: ten turns of two or four waves, or of 64 keys for all
+    s = Shared([(new, 5075), (new // 2, 4800)], d, e4m3, 1024, page, seed=60 + d, kind="any", sharp=3.0)
+    s.check(s.run(w4, window=window), window=window)
