@@ -135,3 +135,59 @@ def test_many_turns_in_the_kernels_for_few_and_for_many(w4, d, e4m3, new, window
     # two parts of 2500 keys or more: ten turns of two or four waves, or of 64 keys for all
     s = Shared([(new, 5075), (new // 2, 4800)], d, e4m3, 1024, page, seed=60 + d, kind="any", sharp=3.0)
     s.check(s.run(w4, window=window), window=window)
+
+
+@pytest.mark.parametrize("new", [3, 30, 200])
+@pytest.mark.parametrize("d,e4m3", [(64, False), (128, True), (256, False)])
+def test_starts_that_fall_write_no_other_rows(w4, new, d, e4m3):  # noqa: F811
+    # rows before and behind the call's, and the other heads of a wider row, keep what they hold
+    s = Tree([(new, 700)] * 4, 4, 2, d, 16, e4m3, seed=50, kind="none")
+    t = s.q.shape[0]
+    for starts in ([0, t, 0, t, 0], [t, 0, t, 0, t], [-9, 2 ** 31 - 1, -2 ** 31, t, 5], [new, new, 0, t, t]):
+        wide = torch.full((t + 64, 6, d), 9.0, dtype=torch.float16, device="cuda")
+        s.run(w4, q_start=dev(np.array(starts, dtype=np.int32)), max_q=new, out=wide[32:32 + t, 1:5])
+        torch.cuda.synchronize()
+        assert (wide[:32] == 9).all() and (wide[32 + t:] == 9).all()
+        assert (wide[:, 0] == 9).all() and (wide[:, 5] == 9).all()
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (32, 1), (130, 1)])
+@pytest.mark.parametrize("b", [1, 3])
+def test_a_batch_without_rows(w4, hq, hkv, b):  # noqa: F811
+    # padding alone: nothing is written, whatever the workspace holds
+    s = Tree([(0, 900)] * b, hq, hkv, 64, 16, seed=51)
+    t = 7
+    q = torch.randn((t, hq, 64), device="cuda", dtype=torch.float16)
+    out = torch.full_like(q, 9.0)
+    mask = torch.full((t, 1), -1, dtype=torch.int64, device="cuda")
+    w4.attention_paged_tree(q, *s.dev, dev(s.table), dev(s.kv_len), mask, q_start=dev(s.starts), max_q=t, out=out,
+                            workspace=torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda"))
+    assert (out == 9).all()
+
+
+@pytest.mark.parametrize("hq,hkv", [(4, 2), (16, 1), (32, 1), (130, 1)])
+def test_one_row_each_without_starts(w4, hq, hkv):  # noqa: F811
+    # of each kernel: 2, 16, 32 and 130 rows; a row sees itself, or only what is before it
+    lens = [(1, 700), (1, 1), (1, 33), (1, 0), (1, 1)]
+    s = Tree(lens, hq, hkv, 64, 16, seed=52)
+    for bits in (1, 0, -2):  # (bits from 1 on are ignored)
+        s.sees = [{0} if bits & 1 else set()] * len(lens)
+        mask = torch.full((len(lens), 1), bits, dtype=torch.int64, device="cuda")
+        for window in (0, 40):
+            got = w4.attention_paged_tree(dev(s.q), *s.dev, dev(s.table), dev(s.kv_len), mask, window=window)
+            s.check(got, window=window)
+
+
+@pytest.mark.parametrize("new,hq", [(3, 2), (20, 2), (70, 4)])
+def test_lengths_outside_the_table(w4, new, hq):  # noqa: F811
+    # kept to 0 .. W * page size: below 0 nothing is cached, and past the table the pages that there are count
+    s = Tree([(new, 96), (new, 50), (new, 64)], hq, 2, 64, 16, seed=53, kind="any")
+    width = 6
+    s.table = np.ascontiguousarray(s.table[:, :width])
+    s.table[1] = s.table[0]
+    given = np.array([2 ** 31 - 1, 97, -2 ** 31], dtype=np.int32)
+    kept = np.array([96, 96, 0], dtype=np.int32)
+    got = w4.attention_paged_tree(dev(s.q), *s.dev, dev(s.table), dev(given), s.mask[:, :s.words], q_start=dev(s.starts),
+                                  max_q=new)
+    s.kv_len = kept
+    s.check(got)
