@@ -389,6 +389,9 @@ int kv_append_norm_rope(const void* q, int64_t ldq, uint16_t* q_out, int64_t ldq
  *   past the last sequence are padding: 0 and -1.  (What kv_append_rope and attention_paged take.)
  *   status int32 [B]: 0, or how many pages were lacking; -1 for a sequence that does not fit: a length below 0,
  *   kv_len + new_len past W * page_size, or rows past T.  Such a one keeps what it has; its rows have position 0.
+ *   A sequence with a status other than 0 has its rows in q_start all the same, but no tokens of theirs in the cache:
+ *   attention_paged and attention_paged_tree take the last of its cached tokens for them, so that their outputs, and
+ *   everything made of these, mean nothing and are to be dropped by status.  They reach no other sequence's rows.
  * Requires 1 <= B <= 2^20, 1 <= T < 2^24, W, page_size, pages >= 1, W * page_size <= 2^30, B * W < 2^31, pages * page_size < 2^31, ldt >= W; int32
  * arrays 4-byte aligned, slot 8-byte; depth may be NULL.  kv_total may be kv_len; no other overlap.  Entries of the
  * stack past its height are left as they are.  Everything is read on the device and kept in bounds there (owned to 0 .. W, the height to

@@ -804,7 +804,8 @@ def kv_plan(kv_len: torch.Tensor, new_len: torch.Tensor, table: torch.Tensor, ow
     many pages it has), free int32 [pages] and free_count int32 [1] (a stack of the cache's free pages and its
     height) are updated; rows: of the step, padding included; depth int32 [rows]: of drafted tokens, instead of their
     order.  Returns (q_start int32 [B + 1], kv_total int32 [B], positions int32 [rows], slots int64 [rows],
-    status int32 [B]: 0, pages lacking, or -1), written to `out` if given, of which kv_total may be kv_len."""
+    status int32 [B]: 0, pages lacking, or -1), written to `out` if given, of which kv_total may be kv_len.  The rows of a
+    sequence with another status than 0 are in no cache: drop what attention and logits give for them."""
     dev = torch.cuda.current_device()
     _need(table, "table", torch.int32, dev)
     ldt = _rowmajor(table, "table")
