@@ -411,7 +411,8 @@ int kv_plan(const int32_t* kv_len, const int32_t* new_len, int64_t B, int32_t* t
  * window: the row's depth is the number of its bits, less one (0 at least), its position p = kv_len - n + depth, and of
  * the tokens before the new ones it sees those from p + 1 - window on; new tokens go by their bits alone.
  * A row that sees no key is 0.  Everything else is as for attention_paged: arguments, lengths in bounds, unseen keys that reach
- * nothing, workspace (query it), roundings, determinism.
+ * nothing, workspace (query it), roundings, determinism; but of a sequence with more than max_q rows all rows are unspecified,
+ * not only those past max_q (it writes no rows but its own, and reaches no other sequence's).
  * Requires what attention_paged requires, window 0 or at least max_q, ldm >= ceil(max_q / 64), mask 8-byte
  * aligned, and no more work than a launch holds: always so while B * heads < 2^20 and T * Hq <= 2^27.
  */

@@ -733,7 +733,8 @@ def attention_paged_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """attention_paged for drafted tokens that form trees (see tree_mask): a row sees the cached tokens before
     its sequence's new ones and, of these, those whose bits are set in its row of mask, int64 [T][words] (bit j % 64 of
     word j / 64: new token j), words >= ceil(max_q / 64).  A window, at least max_q, reaches back from the row's position,
-    kv_len - n + its bits set - 1.  Everything else is as for attention_paged (attention_workspace_bytes with tree=True)."""
+    kv_len - n + its bits set - 1.  All rows of a sequence with more than max_q are unspecified.  Everything else is as for
+    attention_paged (attention_workspace_bytes with tree=True)."""
     dev = torch.cuda.current_device()
     _need(mask, "mask", torch.int64, dev)
     ldm = _rowmajor(mask, "mask")

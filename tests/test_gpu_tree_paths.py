@@ -191,3 +191,19 @@ def test_lengths_outside_the_table(w4, new, hq):  # noqa: F811
                                   max_q=new)
     s.kv_len = kept
     s.check(got)
+
+
+@pytest.mark.parametrize("n,most", [(9, 8), (12, 3), (60, 24), (160, 40), (200, 97)])
+@pytest.mark.parametrize("d,window", [(64, 0), (128, 300), (256, 0)])
+def test_more_rows_than_max_q_stay_in_place(w4, n, most, d, window):  # noqa: F811
+    # of the second sequence: it writes no rows but its own, whatever mask and kernel were chosen for fewer, and the others are right
+    lens = [(min(most, 5), 700), (n, 900), (2, 90)]
+    s = Tree(lens, 2, 2, d, 16, seed=54 + n, kind="any")
+    t = s.q.shape[0]
+    wide = torch.full((t + 64, 2, d), 9.0, dtype=torch.float16, device="cuda")
+    got = s.run(w4, window=window, max_q=most, mask=s.mask[:, :-(-most // 64)].contiguous(), out=wide[32:32 + t])
+    assert (wide[:32] == 9).all() and (wide[32 + t:] == 9).all()
+    want, size, wobble = s.want(None, window)
+    keep = np.r_[:lens[0][0], lens[0][0] + n:t]
+    got = got.cpu().numpy().astype(np.float64)
+    assert (np.abs(got - want) <= s.bound(want, size, wobble))[keep].all()
