@@ -213,7 +213,7 @@ __device__ __forceinline__ void fetch(const RopeArgs& g, int i, int t0, Item& x)
 }
 
 template <bool F32, int MODE, bool NORM>
-__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, float* staged, Item& x) {
+__device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, f32x8* staged, Item& x) {
   if constexpr (NORM) {
     const float f = norm_of(g, lanes_sum(squares(x.a) + squares(x.b), g.per));
     if (x.rot) {
@@ -226,9 +226,9 @@ __device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, fl
   const float2* cs = turn + x.tl * half;
   if constexpr (MODE == kHalfOdd && NORM) {
     // all lanes of a head are in this wave, and here or not here together (a lane past the head's items holds none of its dims)
-    float* head = staged + (threadIdx.x & ~(g.per - 1)) * 8;
+    const float* head = reinterpret_cast<const float*>(staged + (threadIdx.x & ~(g.per - 1)));
     if (x.rot) {
-      *reinterpret_cast<f32x8*>(staged + threadIdx.x * 8) = x.a;
+      staged[threadIdx.x] = x.a;
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -285,7 +285,7 @@ __device__ __forceinline__ void finish(const RopeArgs& g, const float2* turn, fl
 template <bool F32, int MODE, bool NORM>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs g) {
   __shared__ float2 turn[kMaxTokens * 128];  // [token][pair]: mscale (cos, sin)
-  __shared__ float staged[NORM && MODE == kHalfOdd ? 8 * kThreads : 1];  // [thread][dim of its chunk]
+  __shared__ f32x8 staged[NORM && MODE == kHalfOdd ? kThreads : 1];  // of each thread: its chunk (as vectors, for their alignment)
   const int t0 = blockIdx.x * g.tokens, nt = min(g.tokens, g.T - t0), half = g.R / 2, n = nt * g.n;
   Item x{};
   int i = threadIdx.x;
