@@ -351,7 +351,7 @@ struct WaveTiles {
     if (whole == 0) f0 = 0;
   }
   __device__ __forceinline__ int first_key(int i) const {
-    if constexpr (NB > 0) i = i < whole ? f0 + i : i - whole < f0 ? i - whole : i;
+    i = i < whole ? f0 + i : i - whole < f0 ? i - whole : i;
     return k0 + (i * NW + wave) * KT;
   }
   static __device__ __forceinline__ uint32_t buffer(int i) { return NB == 1 ? 0u : (uint32_t)(i % NB * 2 * TILE); }
@@ -1581,7 +1581,7 @@ __global__ __launch_bounds__((64 * kManyWaves), (many_per_cu<DP>())) void attent
 // latency (head, then the parts).  A workgroup of four waves takes one row, a quarter of the parts
 // each (WIDE), or a row per wave.  3.5 us for 13 parts of one token's 16 rows of 128 dims, 5.2 for 32 parts of 512
 // rows.
-template <bool FEW, bool WIDE, int EL>
+template <bool FEW, bool WIDE, int EL, bool TREE>
 __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
   typedef float vec __attribute__((ext_vector_type(EL)));
   constexpr int BATCH = WIDE ? 8 : 4, STEP = WIDE ? 4 : 1;
@@ -1649,7 +1649,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(Plan p) {
   if (d >= D) return;
   const int row = r0 + r, tok = divide(row, p.group);
   bool any = s.len - s.n + tok >= 0;
-  if (g.mask) any = (!g.window && s.len > s.n) || tree_row(g, s, tok).any;
+  if constexpr (TREE) any = (!g.window && s.len > s.n) || tree_row(g, s, tok).any;
   const float f = any ? (g.c.e4m3 && g.c.v_scale ? g.c.v_scale[kvh] : 1.f) / l : 0.f;
   uint16_t* out = g.out + (int64_t)(s.first + tok) * g.ldo + (int64_t)(kvh * p.G + row - tok * p.G) * D + d;
   typedef uint16_t bits __attribute__((ext_vector_type(EL)));
@@ -1710,6 +1710,11 @@ constexpr int tree_wave_lds() {
 template <int DP, bool FP8>
 constexpr int tree_lds() { return tree_waves<DP, FP8>() * tree_wave_lds<DP, FP8>() + 16 * tree_blocks<DP>() * (DP * 2 + 8 * kTreeWords); }
 int tree_rows(const AttnArgs& a) { return 16 * (a.c.dim <= 128 ? tree_blocks<128>() : tree_blocks<256>()); }
+int tree_per_cu_of(const AttnArgs& a) {
+  const int d = a.c.dim;
+  return a.c.e4m3 ? d <= 64 ? tree_per_cu<64, true>() : d <= 128 ? tree_per_cu<128, true>() : tree_per_cu<256, true>()
+                  : d <= 64 ? tree_per_cu<64, false>() : d <= 128 ? tree_per_cu<128, false>() : tree_per_cu<256, false>();
+}
 
 // Trees of many rows: rows of a tile, and about how many parts there should be of all tiles together, for one round of the
 // workgroups that the CUs hold.
@@ -1720,8 +1725,7 @@ void plan_tree(const AttnArgs& a, int64_t most, F row_tiles, Launch& x) {
   // The kernel for many rows in tiles of 128: 64 take 140 us against 127 for 4 sequences of 61 to 200 rows of two heads,
   // 256 dims, a window of 4096, 168 and 124 at 128 dims without it in e4m3, 24 and 22 for one of 512 rows and 4096 keys.
   x.many_rows = x.tree ? tree_rows(a) : 128;
-  const int per_cu = x.tree ? (a.c.dim * (a.c.e4m3 ? 1 : 2) <= 128 ? 2 : 1)
-                            : a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>();
+  const int per_cu = x.tree ? tree_per_cu_of(a) : a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>();
   // what a workgroup takes to start and end, and its part to be joined: about 12 us
   x.start_keys = (x.tree ? 1000 : 500) * 128 / std::max(a.c.dim, 64);
   const int64_t tiles = row_tiles(x.many_rows), slots = std::max(1, per_cu * kCus / a.c.heads);
@@ -1845,15 +1849,15 @@ void launch_many(const Plan& p, int items, hipStream_t st) {
   launch_many_ks<DP, FP8, 1, TREE>(p, items, st);
 }
 
-template <bool FEW, bool WIDE>
+template <bool FEW, bool WIDE, bool TREE>
 void launch_join(const Plan& p, int items, hipStream_t st) {
   const int D = p.a.c.dim, grid = items * (WIDE ? p.part_rows : (p.part_rows + 3) / 4);
   if (D <= 64)
-    attention_join_kernel<FEW, WIDE, 1><<<grid, 256, 0, st>>>(p);
+    attention_join_kernel<FEW, WIDE, 1, TREE><<<grid, 256, 0, st>>>(p);
   else if (D <= 128)
-    attention_join_kernel<FEW, WIDE, 2><<<grid, 256, 0, st>>>(p);
+    attention_join_kernel<FEW, WIDE, 2, TREE><<<grid, 256, 0, st>>>(p);
   else
-    attention_join_kernel<FEW, WIDE, 4><<<grid, 256, 0, st>>>(p);
+    attention_join_kernel<FEW, WIDE, 4, TREE><<<grid, 256, 0, st>>>(p);
 }
 
 template <bool FP8>
@@ -1870,7 +1874,7 @@ void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
     if (D <= 64) launch_few<64, FP8, TREE>(p, items, st);
     else if (D <= 128) launch_few<128, FP8, TREE>(p, items, st);
     else launch_few<256, FP8, TREE>(p, items, st);
-    if (x.few_parts) launch_join<true, true>(p, p.a.B * heads, st);
+    if (x.few_parts) launch_join<true, true, TREE>(p, p.a.B * heads, st);
   }
   if (x.many) {
     ws += x.few_bytes;
@@ -1892,8 +1896,8 @@ void launch_dims(const Launch& x, Plan p, char* ws, hipStream_t st) {
     }
     // many parts: a workgroup per row
     // (trees: or few rows)
-    if (p.part && ((TREE ? x.tree_parts / x.tiles : p.splits) >= 16 || (TREE && items * x.many_rows <= 2048))) launch_join<false, true>(p, items, st);
-    else if (p.part) launch_join<false, false>(p, items, st);
+    if (p.part && ((TREE ? x.tree_parts / x.tiles : p.splits) >= 16 || (TREE && items * x.many_rows <= 2048))) launch_join<false, true, TREE>(p, items, st);
+    else if (p.part) launch_join<false, false, TREE>(p, items, st);
   }
 }
 

@@ -21,7 +21,7 @@ namespace w4 {
 namespace {
 
 template <int DP, bool FP8>
-__global__ __launch_bounds__((64 * tree_waves<DP, FP8>()), (few_tile<DP, FP8>() == 16384 ? 1 : 2)) void attention_tree_kernel(Plan p) {
+__global__ __launch_bounds__((64 * tree_waves<DP, FP8>()), (tree_per_cu<DP, FP8>() * tree_waves<DP, FP8>() / 4)) void attention_tree_kernel(Plan p) {
   constexpr int NW = tree_waves<DP, FP8>(), KT = kFewKeys, ES = FP8 ? 1 : 2, ROWB = DP * ES;
   constexpr int TILE = few_tile<DP, FP8>(), NB = tree_buffers<DP, FP8>(), RT = tree_blocks<DP>(), ROWS = 16 * RT;
   constexpr int STEPS = DP / 32, DB = DP / 16;

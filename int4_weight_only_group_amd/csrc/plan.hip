@@ -25,8 +25,7 @@ namespace {
 constexpr int kPlanThreads = 1024, kRowThreads = 256;
 constexpr int kOneLaunchRows = 4096;  // rows that the first launch writes too, at most
 
-// Inclusive sum over the workgroup's threads; all: over all of them.  lds: one int64 per wave; the caller separates uses.
-template <int THREADS>
+// Inclusive sum over kPlanThreads threads; all: over all of them.  lds: one int64 per wave; the caller separates uses.
 __device__ __forceinline__ int64_t block_sum(int64_t mine, int64_t& all, int64_t* lds) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int64_t incl = mine;
@@ -39,7 +38,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t mine, int64_t& all, int64_t
   __syncthreads();
   all = 0;
 #pragma unroll
-  for (int w = 0; w < THREADS / 64; ++w) {
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
     const int64_t x = lds[w];
     if (w < wave) incl += x;
     all += x;
@@ -252,7 +251,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs g, bool row
   for (int b0 = 0; b0 < g.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
     Asked s = b < g.B ? asked(g, b) : Asked{};
-    const int64_t end = row0 + block_sum<kPlanThreads>(s.rows, all, sums[0]);
+    const int64_t end = row0 + block_sum(s.rows, all, sums[0]);
     row0 += all;
     const int start = (int)min((int64_t)g.T, end - s.rows);
     if (b < g.B) {
@@ -261,7 +260,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs g, bool row
       if (b == g.B - 1) g.q_start[g.B] = (int)min((int64_t)g.T, end);
     }
     const int back = max(0, s.have - s.need);
-    const int64_t at = min((int64_t)0x7fffffff, count + given + block_sum<kPlanThreads>(back, all, sums[1]) - back);
+    const int64_t at = min((int64_t)0x7fffffff, count + given + block_sum(back, all, sums[1]) - back);
     given += all;
     for_pages(b, back, at | (int64_t)s.need << 32, [&](int of, int64_t x, int i) {
       int32_t* entry = g.table + of * g.ldt + (x >> 32) + i;
@@ -279,7 +278,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs g, bool row
     Asked s = b < g.B ? asked(g, b) : Asked{};
     if (b < g.B) fit(g, g.q_start[b], s);
     const int want = max(0, s.need - s.have);
-    const int64_t end = wanted + block_sum<kPlanThreads>(want, all, sums[2]);
+    const int64_t end = wanted + block_sum(want, all, sums[2]);
     wanted += all;
     const bool granted = want == 0 || end <= there;
     const int64_t from = granted && want > 0 ? (there - 1 - (end - want)) | (int64_t)s.have << 32 : 0;
