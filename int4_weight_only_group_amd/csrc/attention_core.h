@@ -1691,7 +1691,8 @@ FewShape few_shape_of(const AttnArgs& a) {
 // Up to how many rows, and words of a mask: 16 sequences of up to 4096 keys, 8 kv heads, in that kernel and in the one for many rows:
 // e4m3, 128 dims: 64 rows 39.1 / 46.5 us, 96 rows 46.5 / 48.8, 128 rows 54.2 / 52.6; 256 dims, 96 rows 75.5 / 91.7;
 // f16, 128 dims: 64 rows 46.6 / 51.1, 96 rows 52.5 / 52.4, 128 rows 69.8 / 55.5; 256 dims, 64 rows 102 / 97 (two
-// sequences 30 / 39), 96 rows 120 / 101; 64 dims, 80 rows 33.7 / 38.6, 128 rows 41.8 / 40.4.
+// sequences 30 / 39), 96 rows 120 / 101; 64 dims, 80 rows 33.7 / 38.6, 128 rows 41.8 / 40.4.  (The number of sequences is not asked:
+// with 64 rows of 256 dims in f16 the many lose 5 % by it, the few gain 23.)
 int tree_most(const AttnArgs& a) { return a.c.e4m3 || a.c.dim <= 64 ? 96 : 64; }
 constexpr int kTreeWords = 2;
 template <int DP>
@@ -1726,8 +1727,10 @@ void plan_tree(const AttnArgs& a, int64_t most, F row_tiles, Launch& x) {
   // 256 dims, a window of 4096, 168 and 124 at 128 dims without it in e4m3, 24 and 22 for one of 512 rows and 4096 keys.
   x.many_rows = x.tree ? tree_rows(a) : 128;
   const int per_cu = x.tree ? tree_per_cu_of(a) : a.c.dim <= 128 ? many_per_cu<128>() : many_per_cu<256>();
-  // what a workgroup takes to start and end, and its part to be joined: about 12 us
-  x.start_keys = (x.tree ? 1000 : 500) * 128 / std::max(a.c.dim, 64);
+  // What a workgroup takes to start and end, and its part to be joined, as keys of 128 dims, in either kernel.  With 250, 500, 1000
+  // and 2000 of them 16 sequences of 7 to 16 rows of two heads, 256 dims, 301 to 8192 keys, take 130, 130, 122 and 123 us; 4 of 61 to 200 with a
+  // window of 4096 127 with 250 and 500, 123 with 1000; some twenty other shapes the same time with any.
+  x.start_keys = 1000 * 128 / std::max(a.c.dim, 64);
   const int64_t tiles = row_tiles(x.many_rows), slots = std::max(1, per_cu * kCus / a.c.heads);
   const int64_t keys = a.window ? std::min(most, (int64_t)a.window + a.max_q + 64) : most;
   x.tiles = (int)tiles;
