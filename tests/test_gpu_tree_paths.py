@@ -207,3 +207,70 @@ def test_more_rows_than_max_q_stay_in_place(w4, n, most, d, window):  # noqa: F8
     keep = np.r_[:lens[0][0], lens[0][0] + n:t]
     got = got.cpu().numpy().astype(np.float64)
     assert (np.abs(got - want) <= s.bound(want, size, wobble))[keep].all()
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,e4m3", [
+    ([(5, 4000), (3, 20)], 4, 2, 128, False), ([(20, 300), (7, 60)], 4, 2, 64, True), ([(20, 6000), (9, 900)], 4, 2, 128, False),
+    ([(16, 5000)], 4, 2, 256, True), ([(100, 3000), (90, 90)], 4, 2, 64, False), ([(70, 100)], 4, 2, 256, False)])
+def test_the_result_may_take_the_queries_place(w4, lens, hq, hkv, d, e4m3):  # noqa: F811
+    # in each kernel, in one part and in many
+    s = Tree(lens, hq, hkv, d, 16, e4m3, seed=d, kind="any")
+    want = s.run(w4)
+    rows = torch.full((s.q.shape[0], hq + 2, d), 5.0, device="cuda", dtype=torch.float16)
+    q = rows[:, 1:hq + 1]
+    q.copy_(dev(s.q))
+    s.run(w4, q=q, out=q)
+    assert torch.equal(q, want) and (rows[:, 0] == 5).all() and (rows[:, hq + 1] == 5).all()
+
+
+@pytest.mark.parametrize("hq,hkv,d,e4m3,window", [(4, 2, 64, False, 0), (2, 2, 128, True, 0), (4, 2, 256, False, 900), (4, 4, 128, False, 300)])
+@pytest.mark.parametrize("t", [6, 24, 60, 200])
+def test_captured_trees_replay_through_their_parts(w4, t, hq, hkv, d, e4m3, window):  # noqa: F811
+    # two graphs of one call, which share a workspace, replayed while starts, lengths and masks change: rows and keys are dealt out anew
+    # each time, into one part and into many; against an eager call with a workspace of its own, and the oracle
+    s = Tree([(t, 3200), (0, 3200), (0, 3200)], hq, hkv, d, 16, e4m3, seed=d + t)
+    rng = np.random.default_rng(t)
+    words = -(-t // 64)
+    bits = rng.integers(-2 ** 63, 2 ** 63, (t, words))
+    need = max(16, w4.attention_workspace_bytes(s.dev[0], 3, t, t, hq, s.table.shape[1], window, tree=True))  # (none in one part)
+    ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    q, table, kv_len, starts, mask = dev(s.q), dev(s.table), dev(s.kv_len), dev(s.starts), dev(bits)
+    args = {**s.kw(), "q_start": starts, "max_q": t}
+    outs = [torch.empty_like(q) for _ in range(2)]
+
+    def call(o, **kw):
+        w4.attention_paged_tree(q, *s.dev, table, kv_len, mask, window=window, out=o, **args, **kw)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(outs[0], workspace=ws[:need])
+    torch.cuda.current_stream().wait_stream(side)
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, o in zip(graphs, outs):
+        with torch.cuda.graph(g):
+            call(o, workspace=ws[:need])
+    for i, lens in enumerate((
+            [(t - 3, 3000), (2, 2000), (1, 5)], [(1, 3200), (t - 2, t - 2), (1, 0)], [(t, 3200), (0, 9), (0, 0)],
+            [(t // 3, 20), (t // 3, 3200), (t // 4, 0)], [(0, 0), (0, 0), (0, 0)], [(2, 3000), (1, 1), (t - 4, 2900)])):
+        s.lens = lens
+        s.starts = np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        s.kv_len = np.array([kv for _, kv in lens], dtype=np.int32)
+        s.sees = [{j for j in range(n) if bits[s.starts[b] + k, j // 64] >> (j % 64) & 1} for b, (n, _) in enumerate(lens) for k in range(n)]
+        for a, x in ((kv_len, s.kv_len), (starts, s.starts), (mask, bits)):
+            a.copy_(dev(x))
+        for g, o in zip(graphs, outs):
+            o.fill_(7.0)
+            g.replay()
+            torch.cuda.synchronize()
+        eager = torch.full_like(q, 7.0)
+        call(eager)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], eager) and torch.equal(outs[1], eager), i
+        live = int(s.starts[-1])
+        assert (eager[live:] == 7).all() and (ws[need:] == 0xFF).all()
+        whole, s.q = s.q, s.q[:live]
+        if live:
+            s.check(eager[:live], window=window)
+        s.q = whole
+        bits = np.roll(bits, 1, axis=0)
