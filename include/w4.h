@@ -354,10 +354,11 @@ int attention_paged(const uint16_t* q, int64_t ldq, const w4_kv_cache* cache, co
  * A decode step with drafted tokens: kv_plan gives each sequence its pages and each row its position and slot,
  * kv_append_norm_rope puts the rows' keys and values there, attention_paged_tree verifies them, logits_adjust
  * prepares the logits for logits_argmax_topk.
- * What a step accepts: where it is the first rows of a sequence's new ones, the next kv_len says so, and that is all.  Rows
- * of a tree stand in the cache in the order of the rows, so that any other path through it has to be appended again: its
- * rows of the projection (kept until the verdict), with kv_append_rope or kv_append_norm_rope, at the slots of the cached tokens kv_len, kv_len + 1, ..., which
- * the caller looks up in the table.  No call here does that, so it is work between two steps, and between two replays of a captured one.
+ * What a step accepts: where it is the first rows of a sequence's new ones, the next kv_len says so, and that is all.  Rows of a
+ * tree stand in the cache in the order of the rows, so that any other path through it has to be appended again: its rows of the
+ * projection (kept until the verdict), with kv_append_rope or kv_append_norm_rope, at the slots of the cached tokens kv_len,
+ * kv_len + 1, ..., which the caller looks up in the table.  No call here does that, so it is work between two steps, and between
+ * two replays of a captured one.
  *
  * norm_rope_f16 -- rope_f16 behind a norm of each head: x w / sqrt(mean over the head's D dims of x^2 + eps) instead
  * of x, with the same arguments, requirements and rotation (forward).  weight f32 [D], 16-byte aligned, or NULL for ones (a norm

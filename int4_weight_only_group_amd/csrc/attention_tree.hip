@@ -2,21 +2,22 @@
 // ones and, of these, those whose bits are set in its mask.  The mathematics, the kernel for at most 16 rows and the one for
 // many are attention_paged's (attention_core.h): tiles of old keys are seen whole, edge tiles take the bits.
 //
-// Between them, the kernel here: 17 to 64 or 96 rows (tree_most()).  Bound: the waits of a turn, at two waves a SIMD; for the case
-// below memory gives 3.0 TB/s of 5.1, and the matrix cores are 13 % busy, the VALU 35: with one buffer K and V have half
-// a turn each to arrive.  For one short sequence: latencies one after another, since the first K and V are asked for when the queries and
-// masks are in LDS (8 tokens of 8 heads after 1562: 12.6 us, where the kernel for few rows takes 6.5 for as many keys).  Waves take 32-key tiles in LDS of their own, as in the
-// kernel for few rows and without barriers, and multiply each with up to four blocks of 16 rows (two at 256 dims), so that an operand from K
-// or V serves them all; the queries are in LDS, once per workgroup; two waves of a SIMD cover each other's waits.  Tiles that all rows
-// see whole have a loop of their own: with the masks in it the sums of 64 rows do not fit the registers, and what is reloaded from scratch waits
-// for every tile in flight (172 us against 58 for the case below).
-// A weight is one f16, as in the kernel for many rows: the result's error is 2.5e-4 to 2.9e-4 of its norm, where its own rounding to f16 is 2.1e-4.
-// Two f16 a weight, as for few rows, make it 2.1e-4 here too and take their time though the matrix cores are 13 % busy, since a
-// wave's splitting and second products stand between its loads: with the join 70.0 us against 60.6 for that case, 53.1 against 47.0 for 64 dims in f16, 15.8 against
-// 15.2 for the 8 tokens, 1 % more at 256 dims; in the kernel for many rows 8 to 35 % more (2 sequences of 256 tokens, 64 heads on 8: 236 against 175).
-// Measured, 16 heads on 8: 16 sequences of 301 to 8192 keys, 7 to 48 tokens (up to 96 rows, two tiles) each, 128 dims, e4m3: 51.5 us and 7.8 for
-// the join; 155 MB read for 145, as the second tile's keys come from caches mostly.  With the join: 64 dims 47 from f16, 45 from e4m3; 7 to 24 tokens of
-// 256 dims 88 from e4m3, 132 from f16.
+// Between them, the kernel here: 17 to 64 or 96 rows (tree_most()).  Bound: the waits of a turn, at two waves a SIMD; for the case below
+// memory gives 3.0 TB/s of 5.1, and the matrix cores are 13 % busy, the VALU 35: with one buffer K and V have half a turn each to
+// arrive.  For one short sequence: latencies one after another, since the first K and V are asked for when the queries and masks are in LDS
+// (8 tokens of 8 heads after 1562: 12.6 us, where the kernel for few rows takes 6.5 for as many keys).  Waves take 32-key tiles in LDS of
+// their own, as in the kernel for few rows and without barriers, and multiply each with up to four blocks of 16 rows (two at 256 dims), so
+// that an operand from K or V serves them all; the queries are in LDS, once per workgroup; two waves of a SIMD cover each other's
+// waits.  Tiles that all rows see whole have a loop of their own: with the masks in it the sums of 64 rows do not fit the registers, and what
+// is reloaded from scratch waits for every tile in flight (172 us against 58 for the case below).
+// A weight is one f16, as in the kernel for many rows: the result's error is 2.5e-4 to 2.9e-4 of its norm, where its own rounding to f16
+// is 2.1e-4.  Two f16 a weight, as for few rows, make it 2.1e-4 here too and take their time though the matrix cores are 13 % busy, since a
+// wave's splitting and second products stand between its loads: with the join 70.0 us against 60.6 for that case, 53.1 against 47.0 for
+// 64 dims in f16, 15.8 against 15.2 for the 8 tokens, 1 % more at 256 dims; in the kernel for many rows 8 to 35 % more (2 sequences of
+// 256 tokens, 64 heads on 8: 236 against 175).
+// Measured, 16 heads on 8: 16 sequences of 301 to 8192 keys, 7 to 48 tokens (up to 96 rows, two tiles) each, 128 dims, e4m3: 51.5 us and
+// 7.8 for the join; 155 MB read for 145, as the second tile's keys come from caches mostly.  With the join: 64 dims 47 from f16, 45 from
+// e4m3; 7 to 24 tokens of 256 dims 88 from e4m3, 132 from f16.
 #include "attention_core.h"
 
 namespace w4 {

@@ -6,16 +6,16 @@
 // stack (of pages given back) and ranks from its top (of pages wanted).  Wants are summed whether they are met or not, so
 // the sequences that get pages are those whose running sum the stack covers: a prefix, whose ranks need no second sum.
 //
-// One workgroup: the sums are a few thousand additions, and pages given back are taken again in the same call.  (Many workgroups could
-// move the pages of a large step: a page that is given back and taken has its old entry for a source, which its rank names.  This is not done.)  Up to
-// 1024 sequences, a thread each, the sums stay in LDS, and every page that moves and every row finds its sequence there by
-// bisection, so that all are under way at once; above, sequences come in rounds of 1024.  Rows follow in the same launch while
-// there are few, else in one of their own.
+// One workgroup: the sums are a few thousand additions, and pages given back are taken again in the same call.  (Many workgroups could move
+// the pages of a large step: a page that is given back and taken has its old entry for a source, which its rank names.  This is not done.)
+// Up to 1024 sequences, a thread each, the sums stay in LDS, and every page that moves and every row finds its sequence there by
+// bisection, so that all are under way at once; above, sequences come in rounds of 1024.  Rows follow in the same launch while there are
+// few, else in one of their own.
 // Bound: latency, of the launch and the loads that follow from each other (lengths, page, table entry).
-// Measured: 64 single tokens 4 us where no page moves, 9.9 (10.8 in a replayed graph) with 5000 given back and as many taken; 256 sequences, 25 k rows, 26 k pages
-// back and taken 21.5 and 4.1 for the rows (through one CU, four loads of a thread under way; one load 22 as well: its stores bound it).
-// Above 1024 sequences, in a replayed graph: 2048 single tokens 17 us where no page moves and 35 with 3 in 10 replaced, 8192 44 and 103: rounds of 1024 one
-// after another.
+// Measured: 64 single tokens 4 us where no page moves, 9.9 (10.8 in a replayed graph) with 5000 given back and as many taken; 256
+// sequences, 25 k rows, 26 k pages back and taken 21.5 and 4.1 for the rows (through one CU, four loads of a thread under way; one load
+// 22 as well: its stores bound it). Above 1024 sequences, in a replayed graph: 2048 single tokens 17 us where no page moves and 35 with 3
+// in 10 replaced, 8192 44 and 103: rounds of 1024 one after another.
 #include <algorithm>
 
 #include "w4_internal.h"
